@@ -41,7 +41,21 @@ EXPORTS = [
     "moe_ffn_test_copy_h",
     "moe_ffn_set_mma_kind", "moe_ffn_set_routing_wait",
     "moe_ffn_profile_layer_only",
+    "moe_kv_pool_bytes", "moe_kv_create", "moe_kv_status", "moe_kv_destroy", "moe_rope_table", "moe_rope",
+    "moe_kv_append", "moe_attn_decode", "moe_kv_copy_pages",
+    "moe_kv_pages_create", "moe_kv_pages_open", "moe_kv_pages_extend", "moe_kv_pages_fork", "moe_kv_pages_free",
+    "moe_kv_pages_compact", "moe_kv_pages_row", "moe_kv_pages_length", "moe_kv_pages_free_pages",
+    "moe_kv_pages_refs", "moe_kv_pages_destroy",
 ]
+
+MOE_KV_BF16 = 0
+MOE_KV_E4M3_UE8M0 = 1
+MOE_ROPE_HALF = 0
+MOE_ROPE_INTERLEAVED = 1
+MOE_ROPE_SCALE_NONE = 0
+MOE_ROPE_SCALE_LINEAR = 1
+MOE_ROPE_SCALE_NTK = 2
+MOE_ROPE_SCALE_YARN = 3
 
 MOE_MMA_AUTO = 0
 MOE_MMA_MXF4_PIECES = 1
@@ -72,6 +86,21 @@ class moe_expert_table(ctypes.Structure):
     _fields_ = [("experts", ctypes.c_void_p)]
 
 
+class moe_kv_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "num_q_heads", "num_kv_heads", "head_dim", "page_size", "num_pages", "max_seqs", "max_pages_per_seq",
+        "kv_dtype", "out_dtype")]
+
+
+class moe_kv_pool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")]
+
+
+class moe_rope_desc(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -88,6 +117,8 @@ def lib() -> ctypes.CDLL:
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         cfgp = ctypes.POINTER(moe_ffn_config)
         tblp = ctypes.POINTER(moe_expert_table)
+        D, F, LL = ctypes.c_double, ctypes.c_float, ctypes.c_longlong
+        kvcp, poolp, ropep = (ctypes.POINTER(t) for t in (moe_kv_config, moe_kv_pool, moe_rope_desc))
         sig = {
             "moe_ffn_packed_expert_bytes": (S, [cfgp]),
             "moe_ffn_create": (I, [ctypes.POINTER(P), cfgp, I]),
@@ -121,6 +152,26 @@ def lib() -> ctypes.CDLL:
             "moe_ffn_set_mma_kind": (I, [P, I]),
             "moe_ffn_set_routing_wait": (I, [P, I]),
             "moe_ffn_profile_layer_only": (I, [P, I]),
+            "moe_kv_pool_bytes": (I, [kvcp, ctypes.POINTER(S), ctypes.POINTER(S)]),
+            "moe_kv_create": (I, [ctypes.POINTER(P), kvcp, I]),
+            "moe_kv_status": (I, [P, P]),
+            "moe_kv_destroy": (None, [P]),
+            "moe_rope_table": (I, [I, D, I, D, I, P, ctypes.POINTER(F)]),
+            "moe_rope": (I, [P, ropep, P, I, P, LL, P, P, LL, P, P]),
+            "moe_kv_append": (I, [P, poolp, P, LL, P, LL, P, P, P, I, ropep, P, LL, P, P]),
+            "moe_attn_decode": (I, [P, poolp, P, P, P, I, F, F, I, P, P, P]),
+            "moe_kv_copy_pages": (I, [P, poolp, I, P, I, P]),
+            "moe_kv_pages_create": (I, [I, I, I, I, ctypes.POINTER(P)]),
+            "moe_kv_pages_open": (I, [P, ctypes.POINTER(I)]),
+            "moe_kv_pages_extend": (I, [P, I, I, P]),
+            "moe_kv_pages_fork": (I, [P, I, ctypes.POINTER(I)]),
+            "moe_kv_pages_free": (I, [P, I]),
+            "moe_kv_pages_compact": (I, [P, P, I, ctypes.POINTER(I)]),
+            "moe_kv_pages_row": (I, [P, I, P, I]),
+            "moe_kv_pages_length": (I, [P, I]),
+            "moe_kv_pages_free_pages": (I, [P]),
+            "moe_kv_pages_refs": (I, [P, I]),
+            "moe_kv_pages_destroy": (None, [P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -385,3 +436,153 @@ def moe_expert_cache_stats(c):
 
 def moe_expert_cache_destroy(c) -> None:
     lib().moe_expert_cache_destroy(c)
+
+
+# ------------------------------------------- key-value cache and its attention
+
+def kv_config(num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_seqs, max_pages_per_seq,
+              kv_dtype=MOE_KV_BF16, out_dtype=MOE_OUT_BF16) -> moe_kv_config:
+    return moe_kv_config(num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_seqs, max_pages_per_seq,
+                         kv_dtype, out_dtype)
+
+
+def moe_kv_pool_bytes(cfg: moe_kv_config):
+    """Bytes of one pool's k (and of its v), and of its k_scales (and of its v_scales)."""
+    kv, sc = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_kv_pool_bytes(ctypes.byref(cfg), ctypes.byref(kv), ctypes.byref(sc)), "moe_kv_pool_bytes")
+    return kv.value, sc.value
+
+
+def moe_kv_create(cfg: moe_kv_config, device: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_kv_create(ctypes.byref(h), ctypes.byref(cfg), int(device)), "moe_kv_create")
+    return h.value
+
+
+def moe_kv_status(h, stream=None) -> int:
+    """Returns the (cleared) sticky device status code; does not raise."""
+    return lib().moe_kv_status(h, _s(stream))
+
+
+def moe_kv_destroy(h) -> None:
+    lib().moe_kv_destroy(h)
+
+
+def kv_pool(k, v, k_scales=None, v_scales=None) -> moe_kv_pool:
+    """One layer's pool (device memory; the scales for MOE_KV_E4M3_UE8M0 only)."""
+    return moe_kv_pool(_p(k), _p(v), _p(k_scales), _p(v_scales))
+
+
+def moe_rope_table(rot_dim: int, base: float, kind: int = MOE_ROPE_SCALE_NONE, factor: float = 1.0,
+                   trained_len: int = 0):
+    """(turns, scale): the frequencies as host uint64 [rot_dim / 2], to be
+    copied to the device, and the factor on cos and sin."""
+    import numpy as np
+
+    turns = np.zeros(max(1, int(rot_dim) // 2), np.uint64)
+    scale = ctypes.c_float()
+    _check(lib().moe_rope_table(int(rot_dim), float(base), int(kind), float(factor), int(trained_len),
+                                turns.ctypes.data, ctypes.byref(scale)), "moe_rope_table")
+    return turns, scale.value
+
+
+def rope(freqs, rot_dim: int, layout: int, scale: float = 1.0) -> moe_rope_desc:
+    """freqs: moe_rope_table's turns in device memory."""
+    return moe_rope_desc(_p(freqs), int(rot_dim), int(layout), float(scale))
+
+
+def moe_rope(h, rope: moe_rope_desc, pos, T: int, q=None, q_out=None, k=None, k_out=None, ldq: int = 0, ldk: int = 0,
+             stream=None):
+    _check(lib().moe_rope(h, ctypes.byref(rope), _p(pos), int(T), _p(q), int(ldq), _p(q_out), _p(k), int(ldk),
+                          _p(k_out), _s(stream)), "moe_rope")
+
+
+def moe_kv_append(h, pool: moe_kv_pool, k, v, pos, page_table, T: int, seq=None, rope: moe_rope_desc | None = None,
+                  q=None, q_out=None, ldq: int = 0, ldk: int = 0, ldv: int = 0, stream=None):
+    _check(lib().moe_kv_append(h, ctypes.byref(pool), _p(k), int(ldk), _p(v), int(ldv), _p(pos), _p(seq),
+                               _p(page_table), int(T), ctypes.byref(rope) if rope is not None else None, _p(q),
+                               int(ldq), _p(q_out), _s(stream)), "moe_kv_append")
+
+
+def moe_attn_decode(h, pool: moe_kv_pool, q, seq_lens, page_table, B: int, out, lse=None, scale: float = 0.0,
+                    softcap: float = 0.0, window: int = 0, stream=None):
+    """scale 0: 1 / sqrt(head_dim)."""
+    _check(lib().moe_attn_decode(h, ctypes.byref(pool), _p(q), _p(seq_lens), _p(page_table), int(B), float(scale),
+                                 float(softcap), int(window), _p(out), _p(lse), _s(stream)), "moe_attn_decode")
+
+
+def moe_kv_copy_pages(h, pools, pairs, n: int, stream=None):
+    """pools: a sequence of moe_kv_pool, one per layer; pairs: device int32 [n][2] of (src, dst) page ids."""
+    arr = (moe_kv_pool * len(pools))(*pools)
+    _check(lib().moe_kv_copy_pages(h, arr, len(pools), _p(pairs), int(n), _s(stream)), "moe_kv_copy_pages")
+
+
+def moe_kv_pages_create(num_pages: int, page_size: int, max_seqs: int, max_pages_per_seq: int) -> int:
+    m = ctypes.c_void_p()
+    _check(lib().moe_kv_pages_create(int(num_pages), int(page_size), int(max_seqs), int(max_pages_per_seq),
+                                     ctypes.byref(m)), "moe_kv_pages_create")
+    return m.value
+
+
+def moe_kv_pages_open(m) -> int:
+    s = ctypes.c_int()
+    _check(lib().moe_kv_pages_open(m, ctypes.byref(s)), "moe_kv_pages_open")
+    return s.value
+
+
+def moe_kv_pages_extend(m, seq: int, tokens: int):
+    """Returns the (src, dst) copy to make first, or None."""
+    c = (ctypes.c_int32 * 2)()
+    _check(lib().moe_kv_pages_extend(m, int(seq), int(tokens), c), "moe_kv_pages_extend")
+    return (c[0], c[1]) if c[0] >= 0 else None
+
+
+def moe_kv_pages_fork(m, parent: int) -> int:
+    s = ctypes.c_int()
+    _check(lib().moe_kv_pages_fork(m, int(parent), ctypes.byref(s)), "moe_kv_pages_fork")
+    return s.value
+
+
+def moe_kv_pages_free(m, seq: int) -> None:
+    _check(lib().moe_kv_pages_free(m, int(seq)), "moe_kv_pages_free")
+
+
+def moe_kv_pages_compact(m, max_pairs: int):
+    """The copies to make, host int32 [n][2] of (src, dst)."""
+    import numpy as np
+
+    pairs = np.empty((max(0, int(max_pairs)), 2), np.int32)
+    n = ctypes.c_int()
+    _check(lib().moe_kv_pages_compact(m, pairs.ctypes.data, int(max_pairs), ctypes.byref(n)), "moe_kv_pages_compact")
+    return pairs[:n.value]
+
+
+def moe_kv_pages_row(m, seq: int, entries: int):
+    """The sequence's page-table row, host int32 [entries], -1 behind its last page."""
+    import numpy as np
+
+    row = np.empty(max(0, int(entries)), np.int32)
+    _check(lib().moe_kv_pages_row(m, int(seq), row.ctypes.data, row.size), "moe_kv_pages_row")
+    return row
+
+
+def _count(rc: int, where: str) -> int:
+    if rc < 0:
+        raise MoeError(rc, where)
+    return rc
+
+
+def moe_kv_pages_length(m, seq: int) -> int:
+    return _count(lib().moe_kv_pages_length(m, int(seq)), "moe_kv_pages_length")
+
+
+def moe_kv_pages_free_pages(m) -> int:
+    return _count(lib().moe_kv_pages_free_pages(m), "moe_kv_pages_free_pages")
+
+
+def moe_kv_pages_refs(m, page: int) -> int:
+    return _count(lib().moe_kv_pages_refs(m, int(page)), "moe_kv_pages_refs")
+
+
+def moe_kv_pages_destroy(m) -> None:
+    lib().moe_kv_pages_destroy(m)

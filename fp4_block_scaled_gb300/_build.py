@@ -16,8 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
 SOURCES = ["api.cu", "gemv.cu", "group.cu", "gemm8.cu", "pack.cu", "route.cu", "router.cu", "actquant.cu", "noalloc.cu",
-           "sched.cpp", "cache.cpp"]
-HEADERS = ["common.cuh", "internal.h", "layout.h"]
+           "sched.cpp", "cache.cpp", "kv.cu", "rope.cu", "attn.cu", "pages.cu", "pages.cpp"]
+HEADERS = ["common.cuh", "internal.h", "layout.h", "rsel.cuh", "kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -54,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     extra = list(extra or [])
 
     def compile_one(src):
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD, src + ".o")
         cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

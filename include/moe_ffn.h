@@ -419,6 +419,209 @@ int moe_ffn_test_set_wait(moe_ffn_t h, unsigned long long wait_ns, int withhold)
 int moe_ffn_test_copy_h(moe_ffn_t h, float* h_dst, int32_t* perm_dst, int n, void* stream);
 void moe_ffn_test_fail_allocs(int n);
 
+/* ---------------------------------------------------------------------------
+ * The attention half of a decode layer ([A100] §然后又发现每 token 启动 2000 次内核
+ * lists it around the experts: RoPE, the quantizers, attention): rotary
+ * positions, a paged key-value cache in HBM, the attention of one new token
+ * per sequence over it, and the cache's pages.  The pages give none of its
+ * formulas; they are the usual ones, stated here.
+ *
+ * The pool of one layer is a number of pages of page_size tokens:
+ *   k, v                [num_pages][Hkv][page_size][D]
+ *   k_scales, v_scales  [num_pages][Hkv][page_size]      (MOE_KV_E4M3_UE8M0)
+ * and a sequence is a row of the page table, device int32
+ * [max_seqs][max_pages_per_seq]: its token j lies in page
+ * row[j / page_size] at offset j % page_size.  Sequences may share pages.
+ * All layers of a model can share one page table and one handle.
+ *
+ * The conventions at the top of this file hold, with one more: the q, k and v
+ * that moe_rope and moe_kv_append read may have a token stride (ldq, ldk,
+ * ldv, in elements; 0: contiguous), so that they can be parts of one
+ * projection's rows. */
+typedef struct moe_kv_s* moe_kv_t;
+
+enum {
+    MOE_KV_BF16 = 0,        /* bf16 rows                                       */
+    MOE_KV_E4M3_UE8M0 = 1   /* E4M3 codes, one ue8m0 byte per row of one head:
+                               moe_ffn_act_quant's rule with n = D             */
+};
+
+typedef struct {
+    int num_q_heads;        /* Hq, a multiple of Hkv, at most 512               */
+    int num_kv_heads;       /* Hkv; query head i reads key head i / (Hq / Hkv)  */
+    int head_dim;           /* D, a multiple of 16 (E4M3: of 32), at most 128   */
+    int page_size;          /* tokens of a page, a multiple of 16, at most 1024 */
+    int num_pages;          /* pages of every pool                              */
+    int max_seqs;           /* rows of the page table, at most 65536            */
+    int max_pages_per_seq;  /* entries of a row                                 */
+    int kv_dtype;           /* MOE_KV_*                                         */
+    int out_dtype;          /* MOE_OUT_*: the attention's output                */
+} moe_kv_config;
+
+/* One layer's pool: DEVICE memory of the caller, each base 16-byte aligned.
+ * The scales are NULL for MOE_KV_BF16. */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+} moe_kv_pool;
+
+/* Bytes of k (and of v), and of k_scales (and of v_scales), of one pool. */
+int moe_kv_pool_bytes(const moe_kv_config* cfg, size_t* kv_bytes, size_t* scale_bytes);
+
+/* Validate cfg, select `device`, allocate the workspace of the split
+ * attention and return a handle.  Errors: INVALID_ARG, UNSUPPORTED (a shape
+ * the kernels do not serve; max_seqs * Hq * capacity of a sequence above
+ * 2^40), OOM, CUDA. */
+int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device);
+
+/* Wait for `stream`, then return and clear the handle's sticky device status:
+ * MOE_OK or MOE_ERR_BAD_INDEX (a page id, a sequence, a position or a length
+ * outside its range). */
+int moe_kv_status(moe_kv_t h, void* stream);
+
+/* Free the workspace (no call of the handle may be pending, and graphs that
+ * captured its calls may not run again).  NULL is a no-op. */
+void moe_kv_destroy(moe_kv_t h);
+
+/* Rotary positions.  Pair i of a head's first rot_dim elements turns by the
+ * angle p * f_i at position p, and both are multiplied by `scale`:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ *   MOE_ROPE_HALF:        a = x[i],  b = x[i + rot_dim / 2]
+ *   MOE_ROPE_INTERLEAVED: a = x[2i], b = x[2i + 1]
+ * computed in fp32 and rounded once to bf16; the rest of the head is copied.
+ * freqs is a DEVICE array [rot_dim / 2] of f_i / (2 pi) * 2^64, rounded
+ * (moe_rope_table): p * freqs[i] modulo 2^64 is the angle's fraction of a
+ * turn, so that far positions lose nothing. */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const uint64_t* freqs;
+    int rot_dim;            /* a multiple of 16, 16 .. D */
+    int layout;             /* MOE_ROPE_* */
+    float scale;
+} moe_rope_desc;
+
+/* The table of a rotary embedding (host code): turns, host [rot_dim / 2], and
+ * the factor on cos and sin.  f_i = base^(-2i / rot_dim), and for contexts
+ * `factor` times as long as the trained_len (kinds other than NONE):
+ *   LINEAR  f_i / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *   YARN    f_i / factor * r_i + f_i * (1 - r_i), with r_i rising linearly from
+ *           0 to 1 between i = floor(d(32)) and ceil(d(1)), d(t) = rot_dim *
+ *           ln(trained_len / (2 pi t)) / (2 ln base) being the pair that makes
+ *           t turns over the trained length (clamped to 0 .. rot_dim - 1);
+ *           scale 0.1 ln(factor) + 1
+ * INVALID_ARG: rot_dim not even, below 2 (NTK: 4) or above 1024, base <= 1 or
+ * not finite, factor < 1 or not finite, trained_len <= 0 (YARN). */
+enum { MOE_ROPE_SCALE_NONE = 0, MOE_ROPE_SCALE_LINEAR = 1, MOE_ROPE_SCALE_NTK = 2, MOE_ROPE_SCALE_YARN = 3 };
+int moe_rope_table(int rot_dim, double base, int kind, double factor, int trained_len, uint64_t* turns,
+                   float* scale);
+
+/* Rotate q and / or k of T tokens (either may be NULL, with its output).
+ *   rope     host struct
+ *   pos      device int32 [T]; a token with a negative position is padding:
+ *            its output rows are left as they were
+ *   q        device bf16 [T][Hq][D], token stride ldq;  k: [T][Hkv][D], ldk
+ *   q_out    device bf16 [T][Hq][D], contiguous -- or q itself, rotated in
+ *            place with the stride ldq; k_out likewise
+ * A stride is 0 or a multiple of 8 that holds a token's heads.  An output may
+ * overlap no input other than by being it. */
+int moe_rope(moe_kv_t h, const moe_rope_desc* rope, const int32_t* pos, int T, const void* q, long long ldq,
+             void* q_out, const void* k, long long ldk, void* k_out, void* stream);
+
+/* Write k and v of T tokens to their places in the pool, rotating k (and q)
+ * on the way: one launch.
+ *   k, v     device bf16 [T][Hkv][D], token strides ldk, ldv
+ *   pos      device int32 [T]: the token's index in its sequence, which is
+ *            its rotary position too; negative: padding, nothing is written
+ *   seq      device int32 [T]: the token's sequence, a row of page_table;
+ *            NULL: token t is of sequence t (T <= max_seqs)
+ *   rope     host struct, or NULL: k is written as it is and q must be NULL
+ *   q, q_out as for moe_rope; both NULL: only k and v
+ * k is rounded to bf16 as moe_rope rounds it; MOE_KV_E4M3_UE8M0 then
+ * quantizes the bf16 rows of k and v as moe_ffn_act_quant does.  No two
+ * tokens of a call may have the same place; several calls may write one
+ * sequence.  A sequence or position outside its range, or a page id outside
+ * [0, num_pages), sets MOE_ERR_BAD_INDEX, and that token's k and v are not
+ * written (its q is rotated). */
+int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long ldk, const void* v, long long ldv,
+                  const int32_t* pos, const int32_t* seq, const int32_t* page_table, int T,
+                  const moe_rope_desc* rope, const void* q, long long ldq, void* q_out, void* stream);
+
+/* Attention of one new token per sequence over its cached keys:
+ *   s_j = scale * q . k_j, or softcap * tanh(scale * q . k_j / softcap)
+ *   out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j)
+ * over j in [max(0, n - window), n) of the sequence's n keys (all of them for
+ * window = 0).
+ *   q          device bf16 [B][Hq][D]
+ *   seq_lens   device int32 [B], n of each sequence (the new token's key
+ *              among them, once it is appended); 0: out = 0, lse = -inf
+ *   page_table device int32; row b is sequence b's
+ *   out        device [B][Hq][D], bf16 or fp32 per cfg.out_dtype
+ *   lse        device fp32 [B][Hq], or NULL
+ *   scale      finite; 0: 1 / sqrt(D).  softcap >= 0 and finite (0: none);
+ *              window >= 0
+ * Scores, softmax and sums are fp32; the weights enter the product with v as
+ * two bf16 terms (16 significant bits).  A key or value that is not finite
+ * makes the outputs it enters not finite; pool contents outside the keys
+ * above are never used, whatever they are.  A page id outside
+ * [0, num_pages) sets MOE_ERR_BAD_INDEX and its keys are left out; so does a
+ * length below 0 (taken as 0) or above the row's capacity (taken as that).
+ * Deterministic.  The split of the work follows the lengths on the device,
+ * so a captured call can be replayed as the sequences grow. */
+int moe_attn_decode(moe_kv_t h, const moe_kv_pool* pool, const void* q, const int32_t* seq_lens,
+                    const int32_t* page_table, int B, float scale, float softcap, int window, void* out, float* lse,
+                    void* stream);
+
+/* Copy pages inside every pool of a model, one launch for up to 64 layers:
+ * pools[l] page pairs[i][1] = pools[l] page pairs[i][0], whole pages of k, v
+ * and scales.
+ *   pools  host array [num_pools];  pairs  device int32 [n][2] (src, dst)
+ * No dst may be another pair's src or dst (a pair of one page twice copies
+ * nothing).  A page id outside [0, num_pages) sets MOE_ERR_BAD_INDEX and its
+ * pair is left out. */
+int moe_kv_copy_pages(moe_kv_t h, const moe_kv_pool* pools, int num_pools, const int32_t* pairs, int n, void* stream);
+
+/* The pages' bookkeeping (host code; needs no GPU and no other handle): which
+ * page holds which tokens of which sequence, with pages shared by forked
+ * sequences counted.  Deterministic: a new page is the lowest free one.
+ *   create   num_pages pages, max_seqs sequences of up to max_pages_per_seq
+ *            pages each
+ *   open     a new empty sequence, the lowest free id, in *seq
+ *   extend   appends `tokens` tokens to a sequence: takes the pages they
+ *            need.  If they begin inside a page that another sequence shares,
+ *            the sequence gets a page of its own for it and copy[0..1] = (src,
+ *            dst) is the copy to make before the tokens are written, else
+ *            copy[0] = -1.
+ *   fork     a new sequence with the parent's tokens, sharing its pages
+ *   free     ends a sequence; its pages that no other shares become free
+ *   compact  moves the pages in use to ids below their count: pairs, host
+ *            [max_pairs][2], are the copies to make (no dst is a src), *n their
+ *            number; at most max_pairs pages move.  The table rows change with
+ *            them: upload them after the copies are enqueued.
+ *   row      writes the sequence's page ids to row, host [entries], -1 behind
+ *            the last; INVALID_ARG if it has more pages than that
+ *   length / free_pages / refs: tokens of a sequence, pages not in use, and
+ *            sequences that hold a page; negative MOE_ERR_* on a bad argument
+ * OOM (nothing changed) where pages, sequence ids or host memory run out;
+ * INVALID_ARG for an id that is not open, or a sequence longer than its row.
+ * Copies of several extend calls may go into one moe_kv_copy_pages call if no
+ * fork, free or compact lies between them.  Calls on one manager must be
+ * ordered. */
+typedef struct moe_kv_pages_s* moe_kv_pages_t;
+int moe_kv_pages_create(int num_pages, int page_size, int max_seqs, int max_pages_per_seq, moe_kv_pages_t* out);
+int moe_kv_pages_open(moe_kv_pages_t m, int* seq);
+int moe_kv_pages_extend(moe_kv_pages_t m, int seq, int tokens, int32_t* copy);
+int moe_kv_pages_fork(moe_kv_pages_t m, int parent, int* seq);
+int moe_kv_pages_free(moe_kv_pages_t m, int seq);
+int moe_kv_pages_compact(moe_kv_pages_t m, int32_t* pairs, int max_pairs, int* n);
+int moe_kv_pages_row(moe_kv_pages_t m, int seq, int32_t* row, int entries);
+int moe_kv_pages_length(moe_kv_pages_t m, int seq);
+int moe_kv_pages_free_pages(moe_kv_pages_t m);
+int moe_kv_pages_refs(moe_kv_pages_t m, int page);
+void moe_kv_pages_destroy(moe_kv_pages_t m);
+
 /* Wait for `stream`, then return and clear the sticky device status:
  * MOE_OK, MOE_ERR_BAD_INDEX or MOE_ERR_DEVICE_TIMEOUT (or MOE_ERR_CUDA if the
  * read itself failed). */
