@@ -1,8 +1,26 @@
-// attn.cu -- attention of one new token per sequence over the paged cache.
+// attn.cu -- attention of one new token per sequence over the paged cache, in
+// one launch.
 //
-// One warp per (sequence, query head): the keys one after another, the
-// running maximum and sum of the softmax in fp32, the output vector in
-// registers (lane l holds elements 4l .. 4l+3).
+// The work is cut into tiles of TT keys of one row, a row being a (sequence,
+// key head, group of up to NROW query heads); the rows' tiles in order are one
+// line, and every warp of the grid takes an equal stretch of it, so the split
+// along the cache follows the lengths by itself: a long sequence spreads over
+// many warps, short ones share one.  A warp keeps the running maximum and sum
+// of the softmax and its output rows in registers while it stays in a row
+// (softmax(s)_j v_j summed with weights 2^(s_j - m), rescaled when m moves), and
+// writes the rows that lie inside its stretch itself.  What is left of a row
+// at the two ends of a stretch is merged in the CTA, and across CTAs by the
+// last of them to finish the row (a ticket per row; it adds the parts in CTA
+// order, so the sums do not depend on which CTA is last, and no CTA waits).
+//
+// Bound: HBM -- the keys and values are read once, 4 to 16 flops a byte.  So a
+// warp streams its tiles through a ring of its own in shared memory (cp.async,
+// 16 bytes a lane, two of three 8 KB tiles in flight: 128 KB an SM, where the
+// rate times the latency is about 40 KB), with no barrier between warps.  The products are
+// mma.sync m16n8k16: at one token's 8 query heads a tile fills half of an MMA's
+// 16 rows, and the tensor core is idle most of the time either way; a tcgen05 MMA
+// would need 128 keys in one place and a TMEM round trip per tile for the
+// same bytes.
 #include "common.cuh"
 #include "kv.h"
 
@@ -10,20 +28,100 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ void load4(const uint8_t* base, size_t row, int D, int lane, int e4m3, float f, float (&x)[4])
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// The softmax's reference is moved when a score passes it by more than this
+// (in powers of two): weights stay below 2^8, and most tiles rescale nothing.
+constexpr float kSlack = 8.0f;
+
+__host__ __device__ constexpr int tile_keys(int DP, bool F8) { return F8 || DP <= 64 ? 32 : 16; }
+__host__ __device__ constexpr int row_bytes(int DP, bool F8) { return DP * (F8 ? 1 : 2); }
+// a tile in the ring: k rows, v rows, then (E4M3) their scale bytes
+__host__ __device__ constexpr int stage_bytes(int DP, bool F8)
 {
-    if (e4m3) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(base + row * D + 4 * lane);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((uint8_t)(u >> (8 * i)), __NV_E4M3))) * f;
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(base + (row * D + 4 * lane) * 2);
-        x[0] = __uint_as_float(u.x << 16);
-        x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(u.y << 16);
-        x[3] = __uint_as_float(u.y & 0xFFFF0000u);
-    }
+    return 2 * tile_keys(DP, F8) * row_bytes(DP, F8) + (F8 ? 2 * tile_keys(DP, F8) : 0);
+}
+__host__ __device__ constexpr int num_stages(int DP, bool F8) { return stage_bytes(DP, F8) < 6000 ? 5 : 3; }
+
+// a part of a row: NROW output rows (not divided by the sum), their maxima and sums
+__host__ __device__ constexpr int part_floats(int DP, int NROW) { return NROW * DP + 2 * NROW; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool Far, class T>
+__device__ __forceinline__ T get(const T* p)
+{
+    return Far ? __ldcg(p) : *p;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// p as two bf16 terms: hi = bf16(p), lo = bf16(p - hi), together 16
+// significant bits (bf16 alone would put an error of 2^-9 on every weight)
+__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo)
+{
+    hi = pack_bf16(p0, p1);
+    lo = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// Four E4M3 codes as two pairs of bf16, bytes (0, 2) and (1, 3): sign, exponent
+// and mantissa moved to their places give the value times 2^-120 (the
+// exponents' biases differ by 120, subnormals included), and one exact
+// multiplication takes the factor back.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t r, uint32_t& even, uint32_t& odd)
+{
+    const uint32_t e = ((r << 4) & 0x07F007F0u) | ((r << 8) & 0x80008000u);
+    const uint32_t o = ((r >> 4) & 0x07F007F0u) | (r & 0x80008000u);
+    constexpr uint32_t k2p120 = 0x7B807B80u;                 // 2^120, twice
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(k2p120));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(k2p120));
 }
 
 // 2^(s - 127); 255 is the NaN scale
@@ -32,65 +130,690 @@ __device__ __forceinline__ float ue8m0_value(uint32_t s)
     return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FFFFFFFu : s << 23);
 }
 
-__global__ void __launch_bounds__(128) k_attn(AttnArgs a)
+// Chunk c of row r of a tile, swizzled so that eight rows' chunks of one
+// column lie in different banks.
+template <int ROWB>
+__device__ __forceinline__ uint32_t at_chunk(uint32_t base, int r, int c)
 {
-    pdl_wait();
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (w >= a.B * a.hq) return;
-    const int b = w / a.hq, hq = w % a.hq, h = hq / (a.hq / a.hkv);
-    const bool in = 4 * lane < a.D;
-    int n = a.lens[b];
-    const int cap = a.row * a.page_size;
-    if ((n < 0 || n > cap) && lane == 0) atomicOr(a.status, kStatusBadIndex);
-    n = min(max(n, 0), cap);
-    const int first = a.window > 0 ? max(0, n - a.window) : 0;
-    float q[4] = {}, o[4] = {}, m = -INFINITY, l = 0.0f;
-    if (in) load4((const uint8_t*)a.q, (size_t)b * a.hq + hq, a.D, lane, 0, 1.0f, q);
-    for (int j = first; j < n; j++) {
-        const int page = a.table[(size_t)b * a.row + j / a.page_size];
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(a.status, kStatusBadIndex);
-            continue;
-        }
-        const size_t row = ((size_t)page * a.hkv + h) * a.page_size + j % a.page_size;
-        float x[4] = {};
-        if (in) load4(a.pool.k, row, a.D, lane, a.e4m3, a.e4m3 ? ue8m0_value(a.pool.ks[row]) : 1.0f, x);
-        float s = warp_sum(q[0] * x[0] + q[1] * x[1] + q[2] * x[2] + q[3] * x[3]) * a.scale;
-        if (a.softcap > 0.0f) s = a.softcap * tanhf(s / a.softcap);
-        const float m1 = fmaxf(m, s), down = expf(m - m1), p = expf(s - m1);
-        l = l * down + p;
-        if (in) load4(a.pool.v, row, a.D, lane, a.e4m3, a.e4m3 ? ue8m0_value(a.pool.vs[row]) : 1.0f, x);
-#pragma unroll
-        for (int i = 0; i < 4; i++) o[i] = o[i] * down + p * x[i];
-        m = m1;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (in) {
-        const size_t at = ((size_t)b * a.hq + hq) * a.D + 4 * lane;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (a.out_f32) ((float*)a.out)[at + i] = o[i] * inv;
-            else ((__nv_bfloat16*)a.out)[at + i] = __float2bfloat16_rn(o[i] * inv);
-        }
-    }
-    if (lane == 0 && a.lse) a.lse[(size_t)b * a.hq + hq] = l == 0.0f ? -INFINITY : m + logf(l);
+    const int x = ROWB >= 128 ? (r & 7) : ((r >> 1) & 3);
+    return base + (uint32_t)(r * ROWB + ((c ^ x) << 4));
 }
 
-}  // namespace
+struct SplitArgs {
+    AttnArgs a;
+    int G, chunks, R;           // query heads per key head, groups of NROW of them, rows per sequence
+    float* frags;               // [grid][kWarps] parts
+    float* parts;               // [grid][2] parts
+    int* tickets;               // [max_seqs * R], zero between launches
+};
 
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s)
+template <int DP, bool F8, int NROW>
+struct Kernel {
+    static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
+    static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
+    static constexpr int PART = part_floats(DP, NROW);
+    static constexpr int QR = NROW == 8 ? 2 : 4;
+
+    // ---- a row's state in one warp: lane 4 g + j holds row g (and g + 8 for
+    // NROW 16), columns 2j, 2j + 1 of every 8
+    float o[ND][4];
+    float m[2], l[2];
+    uint32_t q[KS][QR];
+
+    __device__ __forceinline__ void reset()
+    {
+#pragma unroll
+        for (int i = 0; i < ND; i++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) o[i][k] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+
+    // Query rows as the A operand.  E4M3: the contraction index runs as
+    // e4m3_to_bf16 yields the keys' elements, (4j, 4j + 2), (4j + 1, 4j + 3) of 16.
+    __device__ __forceinline__ void load_q(const SplitArgs& s, int b, int row, int lane)
+    {
+        const int g = lane >> 2, j = lane & 3, D = s.a.D;
+        const int h = row / s.chunks, c = row - h * s.chunks;
+#pragma unroll
+        for (int half = 0; half < NROW / 8; half++) {
+            const int hg = c * NROW + g + 8 * half;
+            const bool in = hg < s.G;
+            const uint16_t* src = s.a.q + ((size_t)b * s.a.hq + h * s.G + (in ? hg : 0)) * D;
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) {
+                uint32_t x = 0, y = 0;
+                if (in && 16 * ks < D) {
+                    if (F8) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(src + 16 * ks + 4 * j);
+                        x = __byte_perm(u.x, u.y, 0x5410);
+                        y = __byte_perm(u.x, u.y, 0x7632);
+                    } else {
+                        x = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j);
+                        y = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j + 8);
+                    }
+                }
+                q[ks][NROW == 8 ? 0 : half] = x;
+                q[ks][NROW == 8 ? 1 : 2 + half] = y;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void mma_q(float (&d)[4], int ks, uint32_t b0, uint32_t b1)
+    {
+        if (NROW == 8) mma_bf16(d, q[ks][0], 0u, q[ks][1], 0u, b0, b1);
+        else mma_bf16(d, q[ks][0], q[ks][1], q[ks][2], q[ks][3], b0, b1);
+    }
+
+    // One tile: `lo`, `hi` are the first and one past the last key of it that
+    // count; bad: a bit per 16 keys left out.
+    __device__ __forceinline__ void tile(const SplitArgs& s, uint32_t st, const uint8_t* stp, int lane, int lo, int hi, uint32_t bad)
+    {
+        const int j = lane & 3;
+        const uint32_t kb = st, vb = st + TT * ROWB;
+        float x[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) x[i][k] = 0.0f;
+        // scores: 16 keys x 32 bytes of their rows per load
+        const int kr = (lane & 7) + ((lane >> 4) & 1) * 8, kc = (lane >> 3) & 1;
+#pragma unroll
+        for (int c2 = 0; c2 < CPR / 2; c2++) {
+#pragma unroll
+            for (int n2 = 0; n2 < NT / 2; n2++) {
+                uint32_t r[4];
+                ldsm4(r, at_chunk<ROWB>(kb, 16 * n2 + kr, 2 * c2 + kc));
+                if (F8) {
+                    uint32_t e, d;
+                    e4m3_to_bf16(r[0], e, d);
+                    mma_q(x[2 * n2], 2 * c2, e, d);
+                    e4m3_to_bf16(r[2], e, d);
+                    mma_q(x[2 * n2 + 1], 2 * c2, e, d);
+                    e4m3_to_bf16(r[1], e, d);
+                    mma_q(x[2 * n2], 2 * c2 + 1, e, d);
+                    e4m3_to_bf16(r[3], e, d);
+                    mma_q(x[2 * n2 + 1], 2 * c2 + 1, e, d);
+                } else {
+                    mma_q(x[2 * n2], c2, r[0], r[1]);
+                    mma_q(x[2 * n2 + 1], c2, r[2], r[3]);
+                }
+            }
+        }
+        // the softmax works in powers of two: x = s log2(e)
+        constexpr float kLog2e = 1.4426950408889634f;
+        constexpr int NV = NROW == 8 ? 2 : 4;
+        const float f = s.a.softcap > 0.0f ? s.a.scale / s.a.softcap : s.a.scale * kLog2e;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            float f0 = f, f1 = f;
+            if (F8) {
+                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + 8 * n + 2 * j);
+                f0 *= ue8m0_value(sc & 0xFF);
+                f1 *= ue8m0_value(sc >> 8);
+            }
+#pragma unroll
+            for (int k = 0; k < NV; k++) x[n][k] *= (k & 1) ? f1 : f0;
+        }
+        if (s.a.softcap > 0.0f) {
+            const float cap = s.a.softcap * kLog2e;
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < NV; k++) x[n][k] = cap * tanhf(x[n][k]);
+        }
+        if (lo > 0 || hi < TT || bad) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < NV; k++) {
+                    const int at = 8 * n + 2 * j + (k & 1);
+                    if (at < lo || at >= hi || ((bad >> (n / 2)) & 1)) x[n][k] = -INFINITY;
+                }
+        }
+        float t[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int k = 0; k < NV; k++) t[k >> 1] = fmaxf(t[k >> 1], x[n][k]);
+#pragma unroll
+        for (int k = 0; k < NV / 2; k++) {
+            t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], 1));
+            t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], 2));
+        }
+        if (__any_sync(0xFFFFFFFFu, t[0] > m[0] + kSlack || (NROW == 16 && t[1] > m[1] + kSlack))) {
+            float down[2] = {1.0f, 1.0f};
+#pragma unroll
+            for (int k = 0; k < NV / 2; k++) {
+                const float to = fmaxf(m[k], t[k]);
+                if (to != m[k]) down[k] = ex2(m[k] - to);            // 0 from -inf
+                m[k] = to;
+                l[k] *= down[k];
+            }
+#pragma unroll
+            for (int i = 0; i < ND; i++) {
+                o[i][0] *= down[0];
+                o[i][1] *= down[0];
+                o[i][2] *= NROW == 8 ? down[0] : down[1];            // NROW 8: the low terms' sums
+                o[i][3] *= NROW == 8 ? down[0] : down[1];
+            }
+        }
+        const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            x[n][0] = ex2(x[n][0] - m0);
+            x[n][1] = ex2(x[n][1] - m0);
+            l[0] += x[n][0] + x[n][1];
+            if (NROW == 16) {
+                x[n][2] = ex2(x[n][2] - m1);
+                x[n][3] = ex2(x[n][3] - m1);
+                l[1] += x[n][2] + x[n][3];
+            }
+            if (F8) {
+                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + TT + 8 * n + 2 * j);
+                const float f0 = ue8m0_value(sc & 0xFF), f1 = ue8m0_value(sc >> 8);
+                // a key left out weighs nothing, whatever its scale byte is
+                x[n][0] = x[n][0] == 0.0f ? 0.0f : x[n][0] * f0;
+                x[n][1] = x[n][1] == 0.0f ? 0.0f : x[n][1] * f1;
+                if (NROW == 16) {
+                    x[n][2] = x[n][2] == 0.0f ? 0.0f : x[n][2] * f0;
+                    x[n][3] = x[n][3] == 0.0f ? 0.0f : x[n][3] * f1;
+                }
+            }
+        }
+        // values: 16 keys x 32 bytes of their rows per load.  NROW 8: rows 0..7 of
+        // the A operand hold the weights' high terms and rows 8..15 their low
+        // terms, so one MMA multiplies both; NROW 16 takes two.
+        const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+#pragma unroll
+        for (int n2 = 0; n2 < NT / 2; n2++) {
+            uint32_t h0, l0, h2, l2, h1 = 0, l1 = 0, h3 = 0, l3 = 0;
+            split_pair(x[2 * n2][0], x[2 * n2][1], h0, l0);
+            split_pair(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2);
+            if (NROW == 16) {
+                split_pair(x[2 * n2][2], x[2 * n2][3], h1, l1);
+                split_pair(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3);
+            }
+            auto mma_p = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
+                if (NROW == 8) {
+                    mma_bf16(d, h0, l0, h2, l2, b0, b1);
+                } else {
+                    mma_bf16(d, h0, h1, h2, h3, b0, b1);
+                    mma_bf16(d, l0, l1, l2, l3, b0, b1);
+                }
+            };
+#pragma unroll
+            for (int c2 = 0; c2 < CPR / 2; c2++) {
+                uint32_t r[4];
+                ldsm4t(r, at_chunk<ROWB>(vb, 16 * n2 + vr, 2 * c2 + vc));
+                if (F8) {
+                    // chunk 2 c2 (r0, r1) and 2 c2 + 1 (r2, r3), 16 columns each: even ones, odd ones
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        uint32_t e0, d0, e1, d1;
+                        e4m3_to_bf16(r[2 * c], e0, d0);
+                        e4m3_to_bf16(r[2 * c + 1], e1, d1);
+                        mma_p(o[2 * (2 * c2 + c)], e0, e1);
+                        mma_p(o[2 * (2 * c2 + c) + 1], d0, d1);
+                    }
+                } else {
+                    mma_p(o[2 * c2], r[0], r[1]);
+                    mma_p(o[2 * c2 + 1], r[2], r[3]);
+                }
+            }
+        }
+    }
+
+    // The sums over the row's four lanes, and (NROW 8) the two terms' rows added.
+    __device__ __forceinline__ void close()
+    {
+#pragma unroll
+        for (int k = 0; k < NROW / 8; k++) {
+            l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
+            l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
+        }
+        if (NROW == 8) {
+#pragma unroll
+            for (int i = 0; i < ND; i++) {
+                o[i][0] += o[i][2];
+                o[i][1] += o[i][3];
+            }
+        }
+    }
+
+    // Column of o[i][k] (k = 0, 1), and of the pair (i, k), (i + 1, k) in E4M3.
+    __device__ __forceinline__ static int column(int i, int k, int j)
+    {
+        return F8 ? 16 * (i / 2) + 4 * j + 2 * k + (i & 1) : 8 * i + 2 * j + k;
+    }
+
+    __device__ __forceinline__ void store_part(float* p, int lane) const
+    {
+        const int g = lane >> 2, j = lane & 3;
+#pragma unroll
+        for (int half = 0; half < NROW / 8; half++) {
+#pragma unroll
+            for (int i = 0; i < ND; i++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) p[(g + 8 * half) * DP + column(i, k, j)] = o[i][2 * half + k];
+            if (j == 0) {
+                p[NROW * DP + g + 8 * half] = m[half];
+                p[NROW * DP + NROW + g + 8 * half] = l[half];
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store_out(const SplitArgs& s, int b, int row, int lane) const
+    {
+        const int g = lane >> 2, j = lane & 3;
+        const int h = row / s.chunks, c = row - h * s.chunks;
+#pragma unroll
+        for (int half = 0; half < NROW / 8; half++) {
+            const int hg = c * NROW + g + 8 * half;
+            if (hg >= s.G) continue;
+            const size_t at = (size_t)b * s.a.hq + h * s.G + hg;
+            const float inv = l[half] == 0.0f ? 0.0f : 1.0f / l[half];
+#pragma unroll
+            for (int i = 0; i < ND; i++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int d = column(i, k, j);
+                    if (d < s.a.D) put(s.a, at * s.a.D + d, o[i][2 * half + k] * inv);
+                }
+            if (j == 0) put_lse(s.a, at, m[half], l[half]);
+        }
+    }
+
+    __device__ __forceinline__ static void put(const AttnArgs& a, size_t at, float v)
+    {
+        if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    }
+
+    __device__ __forceinline__ static void put_lse(const AttnArgs& a, size_t at, float m, float l)
+    {
+        if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    }
+
+    // Parts of one row, in order: data(i) for i < n, written by this CTA, or
+    // (Far) by others, in global memory.  All threads; the result to the output
+    // (final) or to `to` as a part.
+    template <bool Far, class F>
+    __device__ __forceinline__ static void merge(const SplitArgs& s, int n, F data, int b, int row, bool final, float* to)
+    {
+        for (int e = threadIdx.x; e < NROW * DP / 4; e += kThreads) {
+            const int g = e / (DP / 4), d = e % (DP / 4) * 4;
+            float top = -INFINITY;
+            for (int i = 0; i < n; i++) top = fmaxf(top, get<Far>(data(i) + NROW * DP + g));
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < n; i++) {
+                const float* p = data(i);
+                const float mi = get<Far>(p + NROW * DP + g);
+                const float w = mi == -INFINITY ? 0.0f : ex2(mi - top);
+                const float4 v = get<Far>(reinterpret_cast<const float4*>(p + g * DP + d));
+                sum += w * get<Far>(p + NROW * DP + NROW + g);
+                acc.x += w * v.x;
+                acc.y += w * v.y;
+                acc.z += w * v.z;
+                acc.w += w * v.w;
+            }
+            if (final) {
+                const int h = row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
+                if (hg >= s.G) continue;
+                const size_t at = (size_t)b * s.a.hq + h * s.G + hg;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+                for (int k = 0; k < 4; k++)
+                    if (d + k < s.a.D) put(s.a, at * s.a.D + d + k, r[k]);
+                if (d == 0) put_lse(s.a, at, top, sum);
+            } else {
+                *reinterpret_cast<float4*>(to + g * DP + d) = acc;
+                if (d == 0) {
+                    to[NROW * DP + g] = top;
+                    to[NROW * DP + NROW + g] = sum;
+                }
+            }
+        }
+    }
+};
+
+struct Frag {
+    const float* at;            // null: none
+    int b, row;
+    int from_start, to_end;     // the part holds the row's first tile, its last tile
+};
+
+// A place on the line of tiles.
+struct Place {
+    int b, row, t, tiles;
+};
+
+template <int DP, bool F8, int NROW>
+__global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ SplitArgs s)
 {
-    if (a.B == 0) return cudaSuccess;
+    using K = Kernel<DP, F8, NROW>;
+    constexpr int TT = K::TT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_warp[kWarps];
+    __shared__ Frag s_frag[2 * kWarps];
+    __shared__ int s_last;
+    uint8_t* ring = smem;
+    uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kWarps * K::STAGES * K::STAGE);   // [B + 1]
+    int* slen = reinterpret_cast<int*>(pre + s.a.B + 1);                               // [B]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = s.a.B, ps = s.a.page_size, cap = s.a.row * ps;
+    pdl_wait();
+
+    // tiles before each sequence (of one row), by a scan over the lengths
+    uint32_t base = 0;
+    for (int i0 = 0; i0 < B; i0 += kThreads) {
+        const int i = i0 + tid;
+        uint32_t v = 0;
+        if (i < B) {
+            int n = s.a.lens[i];
+            if ((n < 0 || n > cap) && blockIdx.x == 0) atomicOr(s.a.status, kStatusBadIndex);
+            n = min(max(n, 0), cap);
+            slen[i] = n;
+            const int first = s.a.window > 0 ? max(0, n - s.a.window) : 0;
+            v = (uint32_t)max(1, (n + TT - 1) / TT - first / TT);
+        }
+        uint32_t x = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        uint32_t before = base, all = base;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) before += s_warp[w];
+            all += s_warp[w];
+        }
+        if (i < B) pre[i + 1] = before + x;
+        base = all;
+        __syncthreads();
+    }
+    if (tid == 0) pre[0] = 0;
+    if (tid < 2 * kWarps) s_frag[tid].at = nullptr;
+    __syncthreads();
+    const unsigned long long W = (unsigned long long)base * s.R;
+    // enough tiles for every warp of a CTA, else fewer CTAs
+    const unsigned long long grid = min((unsigned long long)gridDim.x, (W + kWarps - 1) / kWarps);
+    if (blockIdx.x >= grid) return;
+    const unsigned long long NW = grid * kWarps, me = (unsigned long long)blockIdx.x * kWarps + warp;
+    unsigned long long u = W * me / NW;
+    const unsigned long long end = W * (me + 1) / NW;
+
+    auto place_of = [&](unsigned long long at) {
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {                       // the last sequence that begins at or before `at`
+            const int mid = (lo + hi + 1) >> 1;
+            if ((unsigned long long)pre[mid] * s.R <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        Place p;
+        p.b = lo;
+        p.tiles = (int)(pre[lo + 1] - pre[lo]);
+        const unsigned long long in = at - (unsigned long long)pre[lo] * s.R;
+        p.row = (int)(in / (unsigned)p.tiles);
+        p.t = (int)(in - (unsigned long long)p.row * p.tiles);
+        return p;
+    };
+    auto advance = [&](Place& p) {
+        if (++p.t < p.tiles) return;
+        p.t = 0;
+        if (++p.row < s.R) return;
+        p.row = 0;
+        p.b++;
+        if (p.b < B) p.tiles = (int)(pre[p.b + 1] - pre[p.b]);
+    };
+    auto first_key = [&](int b) { return s.a.window > 0 ? max(0, slen[b] - s.a.window) : 0; };
+
+    K k;
+    if (u < end) {
+        uint8_t* my = ring + warp * (K::STAGES * K::STAGE);
+        const uint32_t my32 = smem_u32(my);
+        // the producer's side: a window of 32 tiles' places in the pool, one a lane
+        // (in blocks of 16 rows of one head: a page is a whole number of them)
+        const int hblk = ps / 16;
+        int wb = -1, wt = 0;
+        uint32_t blk[TT / 16];
+        uint32_t badq = 0;                      // 2 bits a stage
+        Place pp = place_of(u);
+        unsigned long long up = u;
+        const int rb = s.a.D * (F8 ? 1 : 2);    // bytes of a cached row
+        const int c = lane % K::CPR, r0 = lane / K::CPR;
+        const bool cin = c * 16 < rb;
+
+        auto issue = [&](int stage) {
+            const int n = slen[pp.b], first = first_key(pp.b), t0 = first / TT, tile = t0 + pp.t;
+            if (pp.b != wb || tile < wt || tile >= wt + 32) {
+                wb = pp.b;
+                wt = tile;
+#pragma unroll
+                for (int i = 0; i < TT / 16; i++) {
+                    const int key = (tile + lane) * TT + 16 * i;
+                    uint32_t at = 0xFFFFFFFFu;
+                    if (key < n) {
+                        const int pi = key / ps;
+                        const int page = s.a.table[(size_t)pp.b * s.a.row + pi];
+                        if (page >= 0 && page < s.a.num_pages)
+                            at = (uint32_t)page * (uint32_t)(s.a.hkv * hblk) + (uint32_t)((key - pi * ps) / 16);
+                        else if (key + 16 > first)
+                            atomicOr(s.a.status, kStatusBadIndex);
+                    }
+                    blk[i] = at;
+                }
+            }
+            const uint32_t st = my32 + stage * K::STAGE;
+            const int h = pp.row / s.chunks;
+            const int lo = max(0, first - tile * TT), hi = min(TT, n - tile * TT);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < TT / 16; i++) {
+                const uint32_t at = __shfl_sync(0xFFFFFFFFu, blk[i], tile - wt);
+                const bool ok = at != 0xFFFFFFFFu;
+                bad |= ok ? 0u : 1u << i;
+                const size_t row = ok ? ((size_t)at + (size_t)(h * hblk)) * 16 : 0;
+                const uint8_t* ksrc = s.a.pool.k + row * rb + (cin ? c * 16 : 0);
+                const uint8_t* vsrc = s.a.pool.v + row * rb + (cin ? c * 16 : 0);
+#pragma unroll
+                for (int r = 0; r < 16; r += K::RPI) {
+                    const int rr = 16 * i + r + r0;
+                    // rows that no key has are zeros, whatever the pool holds there
+                    const bool in = ok && cin && rr >= lo && rr < hi;
+                    const size_t off = in ? (size_t)(r + r0) * rb : 0;
+                    cp_async16(at_chunk<K::ROWB>(st, rr, c), ksrc + off, in ? 16 : 0);
+                    cp_async16(at_chunk<K::ROWB>(st + TT * K::ROWB, rr, c), vsrc + off, in ? 16 : 0);
+                }
+                if (F8 && lane < 2) {
+                    const uint8_t* src = (lane ? s.a.pool.vs : s.a.pool.ks) + row;
+                    cp_async16(st + 2 * TT * K::ROWB + lane * TT + 16 * i, src, ok ? 16 : 0);
+                }
+            }
+            badq = (badq & ~(3u << (2 * stage))) | (bad << (2 * stage));
+            up++;
+            if (up < end) advance(pp);
+        };
+
+#pragma unroll
+        for (int i = 0; i < K::STAGES - 1; i++) {
+            if (up < end) issue(i);
+            cp_async_commit();
+        }
+        Place cp = place_of(u);
+        int start = cp.t, first_seg = 1, stage = 0;
+        k.load_q(s, cp.b, cp.row, lane);
+        k.reset();
+        while (true) {
+            if (up < end) issue(stage == 0 ? K::STAGES - 1 : stage - 1);
+            cp_async_commit();
+            cp_async_wait<K::STAGES - 1>();
+            __syncwarp();
+            const int n = slen[cp.b], first = first_key(cp.b), at = (first / TT + cp.t) * TT;
+            k.tile(s, my32 + stage * K::STAGE, my + stage * K::STAGE, lane, max(0, first - at), min(TT, n - at),
+                   (badq >> (2 * stage)) & 3u);
+            __syncwarp();
+            stage = stage + 1 == K::STAGES ? 0 : stage + 1;
+            u++;
+            const bool row_done = cp.t + 1 == cp.tiles;
+            if (!row_done && u < end) {
+                cp.t++;
+                continue;
+            }
+            k.close();
+            if (row_done && start == 0) {
+                k.store_out(s, cp.b, cp.row, lane);
+            } else {
+                // a part: the last one of the stretch stays in the warp's ring, which
+                // is drained then; one that ends a row goes to global memory
+                float* to = u == end ? reinterpret_cast<float*>(my)
+                                     : s.frags + ((size_t)blockIdx.x * kWarps + warp) * K::PART;
+                k.store_part(to, lane);
+                if (lane == 0) {
+                    Frag& f = s_frag[2 * warp + (first_seg ? 0 : 1)];
+                    f.at = to;
+                    f.b = cp.b;
+                    f.row = cp.row;
+                    f.from_start = start == 0;
+                    f.to_end = row_done;
+                }
+            }
+            if (u == end) break;
+            advance(cp);
+            start = 0;
+            first_seg = 0;
+            k.load_q(s, cp.b, cp.row, lane);
+            k.reset();
+        }
+    }
+    __syncthreads();
+
+    // the parts of each row in this CTA, then across CTAs
+    for (int i = 0; i < 2 * kWarps;) {
+        if (!s_frag[i].at) {
+            i++;
+            continue;
+        }
+        const int b = s_frag[i].b, row = s_frag[i].row;
+        const bool from_start = s_frag[i].from_start;
+        bool to_end = false;
+        int cnt = 0, e = i;
+        unsigned long long list = 0;            // indices, 4 bits each
+        for (; e < 2 * kWarps; e++) {
+            if (!s_frag[e].at) continue;
+            if (s_frag[e].b != b || s_frag[e].row != row) break;
+            list |= (unsigned long long)e << (4 * cnt);
+            cnt++;
+            to_end = s_frag[e].to_end;
+        }
+        const bool whole = from_start && to_end;
+        const int slot = from_start ? 1 : 0;
+        K::template merge<false>(s, cnt, [&](int x) { return s_frag[(list >> (4 * x)) & 15].at; }, b, row, whole,
+                 s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
+        if (!whole) {
+            const unsigned long long tiles = pre[b + 1] - pre[b];
+            const unsigned long long r0 = (unsigned long long)pre[b] * s.R + row * tiles, r1 = r0 + tiles - 1;
+            const int c0 = (int)(((r0 + 1) * grid - 1) / W), c1 = (int)(((r1 + 1) * grid - 1) / W);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(s.tickets + (size_t)b * s.R + row, 1) == c1 - c0;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // c0 begins the row (slot 1) unless it begins with the row, too
+                K::template merge<true>(s, c1 - c0 + 1, [&](int x) { return s.parts + ((size_t)(c0 + x) * 2 + (x == 0 ? 1 : 0)) * K::PART; }, b, row,
+                         true, nullptr);
+                if (tid == 0) s.tickets[(size_t)b * s.R + row] = 0;
+            }
+        }
+        i = e;
+    }
+}
+
+template <int DP, bool F8, int NROW>
+cudaError_t launch(const SplitArgs& s, cudaStream_t st)
+{
+    using K = Kernel<DP, F8, NROW>;
+    const size_t smem = (size_t)kWarps * K::STAGES * K::STAGE + (2 * (size_t)s.a.B + 1) * 4;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.B * a.hq + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
+    cfg.gridDim = dim3((unsigned)s.a.sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn, a);
+    return cudaLaunchKernelEx(&cfg, k_attn<DP, F8, NROW>, s);
+}
+
+template <int DP, bool F8, int NROW>
+cudaError_t allow()
+{
+    using K = Kernel<DP, F8, NROW>;
+    return cudaFuncSetAttribute(k_attn<DP, F8, NROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kWarps * K::STAGES * K::STAGE + (2 * kAttnMaxSeqs + 1) * 4);
+}
+
+int rows_of(int hq, int hkv)
+{
+    const int G = hq / hkv;
+    return hkv * (G <= 8 ? 1 : (G + 15) / 16);
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms)
+{
+    const size_t part = (size_t)part_floats(D <= 64 ? 64 : 128, hq / hkv <= 8 ? 8 : 16) * sizeof(float);
+    AttnWorkspace w;
+    w.tickets = 0;
+    w.frags = align256((size_t)max_seqs * rows_of(hq, hkv) * sizeof(int));
+    w.parts = w.frags + align256((size_t)sms * kWarps * part);
+    w.bytes = w.parts + align256((size_t)sms * 2 * part);
+    return w;
+}
+
+cudaError_t attn_init_device()
+{
+    cudaError_t e = allow<64, false, 8>();
+    if (e == cudaSuccess) e = allow<64, false, 16>();
+    if (e == cudaSuccess) e = allow<128, false, 8>();
+    if (e == cudaSuccess) e = allow<128, false, 16>();
+    if (e == cudaSuccess) e = allow<64, true, 8>();
+    if (e == cudaSuccess) e = allow<64, true, 16>();
+    if (e == cudaSuccess) e = allow<128, true, 8>();
+    if (e == cudaSuccess) e = allow<128, true, 16>();
+    return e;
+}
+
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
+{
+    if (a.B == 0) return cudaSuccess;
+    SplitArgs s;
+    s.a = a;
+    s.G = a.hq / a.hkv;
+    s.chunks = s.G <= 8 ? 1 : (s.G + 15) / 16;
+    s.R = a.hkv * s.chunks;
+    const AttnWorkspace w = attn_workspace(a.max_seqs, a.hq, a.hkv, a.D, a.sms);
+    s.tickets = reinterpret_cast<int*>(a.ws + w.tickets);
+    s.frags = reinterpret_cast<float*>(a.ws + w.frags);
+    s.parts = reinterpret_cast<float*>(a.ws + w.parts);
+    if (a.D <= 64) {
+        if (a.e4m3) return s.G <= 8 ? launch<64, true, 8>(s, st) : launch<64, true, 16>(s, st);
+        return s.G <= 8 ? launch<64, false, 8>(s, st) : launch<64, false, 16>(s, st);
+    }
+    if (a.e4m3) return s.G <= 8 ? launch<128, true, 8>(s, st) : launch<128, true, 16>(s, st);
+    return s.G <= 8 ? launch<128, false, 8>(s, st) : launch<128, false, 16>(s, st);
 }
 
 }  // namespace moe

@@ -17,6 +17,7 @@ struct moe_kv_s {
     int device;
     int sms;
     int* status;
+    uint8_t* attn_ws;           // the attention's workspace, in the same allocation
 };
 
 namespace {
@@ -48,11 +49,14 @@ int check_kv_cfg(const moe_kv_config* c)
     if (c->kv_dtype != MOE_KV_BF16 && c->kv_dtype != MOE_KV_E4M3_UE8M0) return MOE_ERR_INVALID_ARG;
     if (c->out_dtype != MOE_OUT_BF16 && c->out_dtype != MOE_OUT_F32) return MOE_ERR_INVALID_ARG;
     if (c->num_q_heads > 512 || c->head_dim > 128 || c->head_dim % (c->kv_dtype == MOE_KV_BF16 ? 16 : 32) ||
-        c->page_size % 16 || c->page_size > 1024 || c->max_seqs > 65536)
+        c->page_size % 16 || c->page_size > 1024 || c->max_seqs > kAttnMaxSeqs)
         return MOE_ERR_UNSUPPORTED;
     const long long cap = (long long)c->max_pages_per_seq * c->page_size;      // tokens of a sequence: int32 positions
-    if (cap > INT32_MAX - 1024) return MOE_ERR_UNSUPPORTED;
-    if ((double)cap * c->max_seqs * c->num_q_heads > 1099511627776.0) return MOE_ERR_UNSUPPORTED;
+    if (cap > INT32_MAX - 4096) return MOE_ERR_UNSUPPORTED;
+    // the attention counts a batch's tiles of 16 keys in 32 bits
+    if ((cap + 15) / 16 * c->max_seqs > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // and pool places in blocks of 16 rows
+    if ((double)c->num_pages * c->num_kv_heads * (c->page_size / 16) > 4294967294.0) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -136,21 +140,25 @@ int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device)
     h->cfg = *cfg;
     h->device = device;
     void* ws = nullptr;
-    if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        attn_init_device() != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;
     }
-    if (lib_malloc(&ws, 256) != cudaSuccess) {
+    const AttnWorkspace w = attn_workspace(cfg->max_seqs, cfg->num_q_heads, cfg->num_kv_heads, cfg->head_dim, h->sms);
+    if (lib_malloc(&ws, 256 + w.bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return MOE_ERR_OOM;
     }
-    if (cudaMemset(ws, 0, 256) != cudaSuccess) {
+    // the status word and the attention's tickets start at zero
+    if (cudaMemset(ws, 0, 256 + w.frags) != cudaSuccess) {
         cudaFree(ws);
         delete h;
         return MOE_ERR_CUDA;
     }
     h->status = (int*)ws;
+    h->attn_ws = (uint8_t*)ws + 256;
     *out = h;
     return MOE_OK;
 }
@@ -339,6 +347,8 @@ int moe_attn_decode(moe_kv_t h, const moe_kv_pool* pool, const void* q, const in
     a.lse = lse;
     a.status = h->status;
     a.sms = h->sms;
+    a.max_seqs = c.max_seqs;
+    a.ws = h->attn_ws;
     KvGuard guard(h->device);
     return cuda_rc(launch_attn(a, (cudaStream_t)stream));
 }

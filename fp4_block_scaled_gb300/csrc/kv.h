@@ -52,8 +52,17 @@ struct AttnArgs {
     void* out;
     float* lse;
     int* status;
-    int sms;
+    int sms, max_seqs;
+    uint8_t* ws;                // attn_workspace's bytes
 };
+
+// The split attention's workspace: byte offsets and the size.
+struct AttnWorkspace {
+    size_t tickets, frags, parts, bytes;
+};
+constexpr int kAttnMaxSeqs = 4096;
+AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms);
+cudaError_t attn_init_device();
 
 constexpr int kCopyLayers = 64;
 struct CopyArgs {

@@ -452,7 +452,7 @@ typedef struct {
     int head_dim;           /* D, a multiple of 16 (E4M3: of 32), at most 128   */
     int page_size;          /* tokens of a page, a multiple of 16, at most 1024 */
     int num_pages;          /* pages of every pool                              */
-    int max_seqs;           /* rows of the page table, at most 65536            */
+    int max_seqs;           /* rows of the page table, at most 4096             */
     int max_pages_per_seq;  /* entries of a row                                 */
     int kv_dtype;           /* MOE_KV_*                                         */
     int out_dtype;          /* MOE_OUT_*: the attention's output                */
@@ -472,8 +472,8 @@ int moe_kv_pool_bytes(const moe_kv_config* cfg, size_t* kv_bytes, size_t* scale_
 
 /* Validate cfg, select `device`, allocate the workspace of the split
  * attention and return a handle.  Errors: INVALID_ARG, UNSUPPORTED (a shape
- * the kernels do not serve; max_seqs * Hq * capacity of a sequence above
- * 2^40), OOM, CUDA. */
+ * the kernels do not serve; a capacity of a sequence near 2^31 tokens or of
+ * all above 2^35; a pool above 2^36 rows), OOM, CUDA. */
 int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device);
 
 /* Wait for `stream`, then return and clear the handle's sticky device status:
