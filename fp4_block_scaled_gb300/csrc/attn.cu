@@ -44,8 +44,9 @@ __host__ __device__ constexpr int stage_bytes(int DP, bool F8)
 }
 __host__ __device__ constexpr int num_stages(int DP, bool F8) { return stage_bytes(DP, F8) < 6000 ? 5 : 3; }
 
-// a part of a row: NROW output rows (not divided by the sum), their maxima and sums
-__host__ __device__ constexpr int part_floats(int DP, int NROW) { return NROW * DP + 2 * NROW; }
+// A part of a row: NROW output rows (not divided by the sums), the powers of
+// two that they are multiples of, the sums of weights, and (E4M3) theirs.
+__host__ __device__ constexpr int part_floats(int DP, bool F8, int NROW) { return NROW * DP + (F8 ? 3 : 2) * NROW; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
 {
@@ -84,10 +85,20 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool Far, class T>
-__device__ __forceinline__ T get(const T* p)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
 {
-    return Far ? __ldcg(p) : *p;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// bf16 rows as they are; E4M3 rows as f16
+template <bool F8>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if (F8) mma_f16(d, a0, a1, a2, a3, b0, b1);
+    else mma_bf16(d, a0, a1, a2, a3, b0, b1);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -111,23 +122,57 @@ __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uin
     lo = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
 }
 
-// Four E4M3 codes as two pairs of bf16, bytes (0, 2) and (1, 3): sign, exponent
-// and mantissa moved to their places give the value times 2^-120 (the
-// exponents' biases differ by 120, subnormals included), and one exact
-// multiplication takes the factor back.
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t r, uint32_t& even, uint32_t& odd)
+template <bool F8>
+__device__ __forceinline__ void split(float w0, float w1, uint32_t& hi, uint32_t& lo);
+
+// Four E4M3 codes as two pairs of f16 (exact: 4 significant bits, exponents
+// -9 .. 8), bytes (0, 1) and (2, 3).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t r, uint32_t& lo, uint32_t& hi)
 {
-    const uint32_t e = ((r << 4) & 0x07F007F0u) | ((r << 8) & 0x80008000u);
-    const uint32_t o = ((r >> 4) & 0x07F007F0u) | (r & 0x80008000u);
-    constexpr uint32_t k2p120 = 0x7B807B80u;                 // 2^120, twice
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(k2p120));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(k2p120));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(r));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// w as two f16 terms of 11 bits: its upper bits, which f16 holds exactly above
+// 2^-14, and the rest; below, f16's steps of 2^-24 remain, 2^-39 of the largest
+// weight that can occur.
+__device__ __forceinline__ void split_pair_f16(float w0, float w1, uint32_t& hi, uint32_t& lo)
+{
+    const float t0 = __uint_as_float(__float_as_uint(w0) & 0xFFFFE000u), t1 = __uint_as_float(__float_as_uint(w1) & 0xFFFFE000u);
+    hi = pack_f16(t0, t1);
+    lo = pack_f16(w0 - t0, w1 - t1);
+}
+
+template <>
+__device__ __forceinline__ void split<false>(float w0, float w1, uint32_t& hi, uint32_t& lo)
+{
+    split_pair(w0, w1, hi, lo);
+}
+
+template <>
+__device__ __forceinline__ void split<true>(float w0, float w1, uint32_t& hi, uint32_t& lo)
+{
+    split_pair_f16(w0, w1, hi, lo);
 }
 
 // 2^(s - 127); 255 is the NaN scale
 __device__ __forceinline__ float ue8m0_value(uint32_t s)
 {
     return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FFFFFFFu : s << 23);
+}
+
+// s - 127, NaN for the NaN scale
+__device__ __forceinline__ float ue8m0_exponent(uint32_t s)
+{
+    return s == 255 ? __uint_as_float(0x7FFFFFFFu) : (float)(int)s - 127.0f;
 }
 
 // Chunk c of row r of a tile, swizzled so that eight rows' chunks of one
@@ -151,14 +196,20 @@ template <int DP, bool F8, int NROW>
 struct Kernel {
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
-    static constexpr int PART = part_floats(DP, NROW);
+    static constexpr int PART = part_floats(DP, F8, NROW);
+    static constexpr int REGION = STAGES * STAGE;            // a warp's ring, and at the end its parts
+    static_assert(REGION % 16 == 0 && PART % 4 == 0 && 4 * 2 * PART <= REGION, "a warp's parts fit its ring");
     static constexpr int QR = NROW == 8 ? 2 : 4;
 
     // ---- a row's state in one warp: lane 4 g + j holds row g (and g + 8 for
     // NROW 16), columns 2j, 2j + 1 of every 8
+    // o 2^mo is the row's sum of weights times values, l 2^m its sum of weights.
+    // E4M3: the values' scales 2^(s - 127) enter o's weights as exponents, so o
+    // has a reference of its own; bf16: mo is m.
     float o[ND][4];
-    float m[2], l[2];
+    float m[2], l[2], mo[2];
     uint32_t q[KS][QR];
+    float qf[2];                // score factor of a row: E4M3 queries are scaled
 
     __device__ __forceinline__ void reset()
     {
@@ -166,44 +217,72 @@ struct Kernel {
         for (int i = 0; i < ND; i++)
 #pragma unroll
             for (int k = 0; k < 4; k++) o[i][k] = 0.0f;
-        m[0] = m[1] = -INFINITY;
+        m[0] = m[1] = mo[0] = mo[1] = -INFINITY;
         l[0] = l[1] = 0.0f;
     }
 
+    // (scores pass the references by at most kSlack; o's lies 2^7 lower, so that
+    // its weights, below 2^15, use f16's range)
+    static constexpr float kLift = 7.0f;
+
     // Query rows as the A operand.  E4M3: the contraction index runs as
-    // e4m3_to_bf16 yields the keys' elements, (4j, 4j + 2), (4j + 1, 4j + 3) of 16.
+    // e4m3_to_f16 yields the keys' elements, (4j, 4j + 1), (4j + 2, 4j + 3) of 16, and a
+    // row is scaled by the power of two that brings its largest element to
+    // [2^14, 2^15): f16 holds the bf16 elements exactly down to 2^-31 of that.
     __device__ __forceinline__ void load_q(const SplitArgs& s, int b, int row, int lane)
     {
         const int g = lane >> 2, j = lane & 3, D = s.a.D;
         const int h = row / s.chunks, c = row - h * s.chunks;
+        const float f = s.a.softcap > 0.0f ? s.a.scale / s.a.softcap : s.a.scale * 1.4426950408889634f;
 #pragma unroll
         for (int half = 0; half < NROW / 8; half++) {
             const int hg = c * NROW + g + 8 * half;
             const bool in = hg < s.G;
             const uint16_t* src = s.a.q + ((size_t)b * s.a.hq + h * s.G + (in ? hg : 0)) * D;
+            uint32_t x[KS], y[KS];
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) {
-                uint32_t x = 0, y = 0;
+                x[ks] = y[ks] = 0;
                 if (in && 16 * ks < D) {
                     if (F8) {
                         const uint2 u = *reinterpret_cast<const uint2*>(src + 16 * ks + 4 * j);
-                        x = __byte_perm(u.x, u.y, 0x5410);
-                        y = __byte_perm(u.x, u.y, 0x7632);
+                        x[ks] = u.x;
+                        y[ks] = u.y;
                     } else {
-                        x = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j);
-                        y = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j + 8);
+                        x[ks] = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j);
+                        y[ks] = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j + 8);
                     }
                 }
-                q[ks][NROW == 8 ? 0 : half] = x;
-                q[ks][NROW == 8 ? 1 : 2 + half] = y;
+            }
+            qf[half] = f;
+            if (F8) {
+                uint32_t top = 0;               // bf16 magnitudes order as integers
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) top = __vmaxu2(top, __vmaxu2(x[ks] & 0x7FFF7FFFu, y[ks] & 0x7FFF7FFFu));
+                top = max(top & 0xFFFFu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int e = min(14 - ((int)(top >> 7) - 127), 126);
+                const float up = exp2i(e);
+                qf[half] = f * exp2i(-e);
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) {
+                    x[ks] = pack_f16(__uint_as_float(x[ks] << 16) * up, __uint_as_float(x[ks] & 0xFFFF0000u) * up);
+                    y[ks] = pack_f16(__uint_as_float(y[ks] << 16) * up, __uint_as_float(y[ks] & 0xFFFF0000u) * up);
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) {
+                q[ks][NROW == 8 ? 0 : half] = x[ks];
+                q[ks][NROW == 8 ? 1 : 2 + half] = y[ks];
             }
         }
     }
 
     __device__ __forceinline__ void mma_q(float (&d)[4], int ks, uint32_t b0, uint32_t b1)
     {
-        if (NROW == 8) mma_bf16(d, q[ks][0], 0u, q[ks][1], 0u, b0, b1);
-        else mma_bf16(d, q[ks][0], q[ks][1], q[ks][2], q[ks][3], b0, b1);
+        if (NROW == 8) mma<F8>(d, q[ks][0], 0u, q[ks][1], 0u, b0, b1);
+        else mma<F8>(d, q[ks][0], q[ks][1], q[ks][2], q[ks][3], b0, b1);
     }
 
     // One tile: `lo`, `hi` are the first and one past the last key of it that
@@ -227,13 +306,13 @@ struct Kernel {
                 ldsm4(r, at_chunk<ROWB>(kb, 16 * n2 + kr, 2 * c2 + kc));
                 if (F8) {
                     uint32_t e, d;
-                    e4m3_to_bf16(r[0], e, d);
+                    e4m3_to_f16(r[0], e, d);
                     mma_q(x[2 * n2], 2 * c2, e, d);
-                    e4m3_to_bf16(r[2], e, d);
+                    e4m3_to_f16(r[2], e, d);
                     mma_q(x[2 * n2 + 1], 2 * c2, e, d);
-                    e4m3_to_bf16(r[1], e, d);
+                    e4m3_to_f16(r[1], e, d);
                     mma_q(x[2 * n2], 2 * c2 + 1, e, d);
-                    e4m3_to_bf16(r[3], e, d);
+                    e4m3_to_f16(r[3], e, d);
                     mma_q(x[2 * n2 + 1], 2 * c2 + 1, e, d);
                 } else {
                     mma_q(x[2 * n2], c2, r[0], r[1]);
@@ -241,20 +320,21 @@ struct Kernel {
                 }
             }
         }
-        // the softmax works in powers of two: x = s log2(e)
+        // the softmax works in powers of two: x = s log2(e); y: the same with the
+        // value's scale, the exponent of o's weight
         constexpr float kLog2e = 1.4426950408889634f;
         constexpr int NV = NROW == 8 ? 2 : 4;
-        const float f = s.a.softcap > 0.0f ? s.a.scale / s.a.softcap : s.a.scale * kLog2e;
+        float y[F8 ? NT : 1][4];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            float f0 = f, f1 = f;
+            float f0 = 1.0f, f1 = 1.0f;
             if (F8) {
                 const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + 8 * n + 2 * j);
-                f0 *= ue8m0_value(sc & 0xFF);
-                f1 *= ue8m0_value(sc >> 8);
+                f0 = ue8m0_value(sc & 0xFF);
+                f1 = ue8m0_value(sc >> 8);
             }
 #pragma unroll
-            for (int k = 0; k < NV; k++) x[n][k] *= (k & 1) ? f1 : f0;
+            for (int k = 0; k < NV; k++) x[n][k] *= F8 ? qf[k >> 1] * ((k & 1) ? f1 : f0) : qf[k >> 1];
         }
         if (s.a.softcap > 0.0f) {
             const float cap = s.a.softcap * kLog2e;
@@ -263,26 +343,50 @@ struct Kernel {
 #pragma unroll
                 for (int k = 0; k < NV; k++) x[n][k] = cap * tanhf(x[n][k]);
         }
+        if (F8) {
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + TT + 8 * n + 2 * j);
+                const float e0 = ue8m0_exponent(sc & 0xFF), e1 = ue8m0_exponent(sc >> 8);
+#pragma unroll
+                for (int k = 0; k < NV; k++) y[n][k] = x[n][k] + ((k & 1) ? e1 : e0);
+            }
+        }
         if (lo > 0 || hi < TT || bad) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int k = 0; k < NV; k++) {
                     const int at = 8 * n + 2 * j + (k & 1);
-                    if (at < lo || at >= hi || ((bad >> (n / 2)) & 1)) x[n][k] = -INFINITY;
+                    if (at < lo || at >= hi || ((bad >> (n / 2)) & 1)) {
+                        x[n][k] = -INFINITY;
+                        if (F8) y[n][k] = -INFINITY;
+                    }
                 }
         }
-        float t[2] = {-INFINITY, -INFINITY};
+        float t[2] = {-INFINITY, -INFINITY}, ty[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int k = 0; k < NV; k++) t[k >> 1] = fmaxf(t[k >> 1], x[n][k]);
+            for (int k = 0; k < NV; k++) {
+                t[k >> 1] = fmaxf(t[k >> 1], x[n][k]);
+                if (F8) ty[k >> 1] = fmaxf(ty[k >> 1], y[n][k]);
+            }
 #pragma unroll
-        for (int k = 0; k < NV / 2; k++) {
-            t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], 1));
-            t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], 2));
+        for (int d = 1; d <= 2; d++)
+#pragma unroll
+            for (int k = 0; k < NV / 2; k++) {
+                t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], d));
+                if (F8) ty[k] = fmaxf(ty[k], __shfl_xor_sync(0xFFFFFFFFu, ty[k], d));
+            }
+        bool move = t[0] > m[0] + kSlack || (NROW == 16 && t[1] > m[1] + kSlack);
+        if (F8) {
+            // o's references lie kLift lower
+            ty[0] -= kLift;
+            ty[1] -= kLift;
+            move = move || ty[0] > mo[0] + kSlack || (NROW == 16 && ty[1] > mo[1] + kSlack);
         }
-        if (__any_sync(0xFFFFFFFFu, t[0] > m[0] + kSlack || (NROW == 16 && t[1] > m[1] + kSlack))) {
+        if (__any_sync(0xFFFFFFFFu, move)) {
             float down[2] = {1.0f, 1.0f};
 #pragma unroll
             for (int k = 0; k < NV / 2; k++) {
@@ -290,6 +394,11 @@ struct Kernel {
                 if (to != m[k]) down[k] = ex2(m[k] - to);            // 0 from -inf
                 m[k] = to;
                 l[k] *= down[k];
+                if (F8) {
+                    const float too = fmaxf(mo[k], ty[k]);
+                    down[k] = too != mo[k] ? ex2(mo[k] - too) : 1.0f;
+                    mo[k] = too;
+                }
             }
 #pragma unroll
             for (int i = 0; i < ND; i++) {
@@ -299,29 +408,20 @@ struct Kernel {
                 o[i][3] *= NROW == 8 ? down[0] : down[1];
             }
         }
-        const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+        float r[2], ro[2];                      // before the first key the references are -inf, and every x as well
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-            x[n][0] = ex2(x[n][0] - m0);
-            x[n][1] = ex2(x[n][1] - m0);
-            l[0] += x[n][0] + x[n][1];
-            if (NROW == 16) {
-                x[n][2] = ex2(x[n][2] - m1);
-                x[n][3] = ex2(x[n][3] - m1);
-                l[1] += x[n][2] + x[n][3];
-            }
-            if (F8) {
-                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + TT + 8 * n + 2 * j);
-                const float f0 = ue8m0_value(sc & 0xFF), f1 = ue8m0_value(sc >> 8);
-                // a key left out weighs nothing, whatever its scale byte is
-                x[n][0] = x[n][0] == 0.0f ? 0.0f : x[n][0] * f0;
-                x[n][1] = x[n][1] == 0.0f ? 0.0f : x[n][1] * f1;
-                if (NROW == 16) {
-                    x[n][2] = x[n][2] == 0.0f ? 0.0f : x[n][2] * f0;
-                    x[n][3] = x[n][3] == 0.0f ? 0.0f : x[n][3] * f1;
-                }
-            }
+        for (int k = 0; k < 2; k++) {
+            r[k] = m[k] == -INFINITY ? 0.0f : m[k];
+            ro[k] = mo[k] == -INFINITY ? 0.0f : mo[k];
         }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int k = 0; k < NV; k++) {
+                x[n][k] = ex2(x[n][k] - r[k >> 1]);
+                l[k >> 1] += x[n][k];
+                if (F8) x[n][k] = ex2(y[n][k] - ro[k >> 1]);
+            }
         // values: 16 keys x 32 bytes of their rows per load.  NROW 8: rows 0..7 of
         // the A operand hold the weights' high terms and rows 8..15 their low
         // terms, so one MMA multiplies both; NROW 16 takes two.
@@ -329,18 +429,18 @@ struct Kernel {
 #pragma unroll
         for (int n2 = 0; n2 < NT / 2; n2++) {
             uint32_t h0, l0, h2, l2, h1 = 0, l1 = 0, h3 = 0, l3 = 0;
-            split_pair(x[2 * n2][0], x[2 * n2][1], h0, l0);
-            split_pair(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2);
+            split<F8>(x[2 * n2][0], x[2 * n2][1], h0, l0);
+            split<F8>(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2);
             if (NROW == 16) {
-                split_pair(x[2 * n2][2], x[2 * n2][3], h1, l1);
-                split_pair(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3);
+                split<F8>(x[2 * n2][2], x[2 * n2][3], h1, l1);
+                split<F8>(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3);
             }
             auto mma_p = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
                 if (NROW == 8) {
-                    mma_bf16(d, h0, l0, h2, l2, b0, b1);
+                    mma<F8>(d, h0, l0, h2, l2, b0, b1);
                 } else {
-                    mma_bf16(d, h0, h1, h2, h3, b0, b1);
-                    mma_bf16(d, l0, l1, l2, l3, b0, b1);
+                    mma<F8>(d, h0, h1, h2, h3, b0, b1);
+                    mma<F8>(d, l0, l1, l2, l3, b0, b1);
                 }
             };
 #pragma unroll
@@ -352,8 +452,8 @@ struct Kernel {
 #pragma unroll
                     for (int c = 0; c < 2; c++) {
                         uint32_t e0, d0, e1, d1;
-                        e4m3_to_bf16(r[2 * c], e0, d0);
-                        e4m3_to_bf16(r[2 * c + 1], e1, d1);
+                        e4m3_to_f16(__byte_perm(r[2 * c], 0, 0x3120), e0, d0);
+                        e4m3_to_f16(__byte_perm(r[2 * c + 1], 0, 0x3120), e1, d1);
                         mma_p(o[2 * (2 * c2 + c)], e0, e1);
                         mma_p(o[2 * (2 * c2 + c) + 1], d0, d1);
                     }
@@ -382,6 +482,13 @@ struct Kernel {
         }
     }
 
+    // 2^mo / (l 2^m), the factor from o to the output; 0 for a row without keys
+    __device__ __forceinline__ static float quotient(float l, float m, float mo)
+    {
+        if (l == 0.0f) return 0.0f;
+        return F8 ? ex2(mo - m) / l : 1.0f / l;
+    }
+
     // Column of o[i][k] (k = 0, 1), and of the pair (i, k), (i + 1, k) in E4M3.
     __device__ __forceinline__ static int column(int i, int k, int j)
     {
@@ -398,8 +505,9 @@ struct Kernel {
 #pragma unroll
                 for (int k = 0; k < 2; k++) p[(g + 8 * half) * DP + column(i, k, j)] = o[i][2 * half + k];
             if (j == 0) {
-                p[NROW * DP + g + 8 * half] = m[half];
+                p[NROW * DP + g + 8 * half] = F8 ? mo[half] : m[half];
                 p[NROW * DP + NROW + g + 8 * half] = l[half];
+                if (F8) p[NROW * DP + 2 * NROW + g + 8 * half] = m[half];
             }
         }
     }
@@ -413,22 +521,37 @@ struct Kernel {
             const int hg = c * NROW + g + 8 * half;
             if (hg >= s.G) continue;
             const size_t at = (size_t)b * s.a.hq + h * s.G + hg;
-            const float inv = l[half] == 0.0f ? 0.0f : 1.0f / l[half];
+            const float inv = quotient(l[half], m[half], F8 ? mo[half] : m[half]);
+            const size_t out = at * s.a.D;
+            if (F8) {           // four columns in a row from an even and an odd MMA column block
 #pragma unroll
-            for (int i = 0; i < ND; i++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const int d = column(i, k, j);
-                    if (d < s.a.D) put(s.a, at * s.a.D + d, o[i][2 * half + k] * inv);
+                for (int i = 0; i < ND; i += 2) {
+                    const int d = column(i, 0, j);
+                    if (d < s.a.D)
+                        put4(s.a, out + d, o[i][2 * half] * inv, o[i + 1][2 * half] * inv, o[i][2 * half + 1] * inv,
+                             o[i + 1][2 * half + 1] * inv);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < ND; i++) {
+                    const int d = column(i, 0, j);
+                    if (d < s.a.D) put2(s.a, out + d, o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
+                }
+            }
             if (j == 0) put_lse(s.a, at, m[half], l[half]);
         }
     }
 
-    __device__ __forceinline__ static void put(const AttnArgs& a, size_t at, float v)
+    __device__ __forceinline__ static void put2(const AttnArgs& a, size_t at, float x, float y)
     {
-        if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = v;
-        else reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+        if (a.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x, y);
+        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at) = pack_bf16(x, y);
+    }
+
+    __device__ __forceinline__ static void put4(const AttnArgs& a, size_t at, float x, float y, float z, float w)
+    {
+        if (a.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x, y, z, w);
+        else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16(x, y), pack_bf16(z, w));
     }
 
     __device__ __forceinline__ static void put_lse(const AttnArgs& a, size_t at, float m, float l)
@@ -436,54 +559,81 @@ struct Kernel {
         if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
 
-    // Parts of one row, in order: data(i) for i < n, written by this CTA, or
-    // (Far) by others, in global memory.  All threads; the result to the output
-    // (final) or to `to` as a part.
-    template <bool Far, class F>
-    __device__ __forceinline__ static void merge(const SplitArgs& s, int n, F data, int b, int row, bool final, float* to)
+    // The parts at(i), i < n, of a row, four columns from d of its row g: one
+    // pass, N parts at a time with all their loads in flight.  Far: written by
+    // other CTAs.  The result is the row's output, or part `to`.
+    template <int N, bool Far, class At>
+    __device__ __forceinline__ static void merge(const SplitArgs& s, int n, At at, int b, int row, int g, int d, float* to)
     {
-        for (int e = threadIdx.x; e < NROW * DP / 4; e += kThreads) {
-            const int g = e / (DP / 4), d = e % (DP / 4) * 4;
-            float top = -INFINITY;
-            for (int i = 0; i < n; i++) top = fmaxf(top, get<Far>(data(i) + NROW * DP + g));
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float sum = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < n; i++) {
-                const float* p = data(i);
-                const float mi = get<Far>(p + NROW * DP + g);
-                const float w = mi == -INFINITY ? 0.0f : ex2(mi - top);
-                const float4 v = get<Far>(reinterpret_cast<const float4*>(p + g * DP + d));
-                sum += w * get<Far>(p + NROW * DP + NROW + g);
-                acc.x += w * v.x;
-                acc.y += w * v.y;
-                acc.z += w * v.z;
-                acc.w += w * v.w;
-            }
-            if (final) {
-                const int h = row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
-                if (hg >= s.G) continue;
-                const size_t at = (size_t)b * s.a.hq + h * s.G + hg;
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-                for (int k = 0; k < 4; k++)
-                    if (d + k < s.a.D) put(s.a, at * s.a.D + d + k, r[k]);
-                if (d == 0) put_lse(s.a, at, top, sum);
-            } else {
-                *reinterpret_cast<float4*>(to + g * DP + d) = acc;
-                if (d == 0) {
-                    to[NROW * DP + g] = top;
-                    to[NROW * DP + NROW + g] = sum;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float top = -INFINITY, topo = -INFINITY, sum = 0.0f;
+        for (int i0 = 0; i0 < n; i0 += N) {
+            float4 v[N];
+            float mo[N], l[N], m[N];
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                mo[i] = m[i] = -INFINITY;
+                l[i] = 0.0f;
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i0 + i < n) {
+                    const float* p = at(i0 + i);
+                    const float* e = p + NROW * DP + g;
+                    v[i] = Far ? __ldcg(reinterpret_cast<const float4*>(p + g * DP + d)) : *reinterpret_cast<const float4*>(p + g * DP + d);
+                    mo[i] = Far ? __ldcg(e) : e[0];
+                    l[i] = Far ? __ldcg(e + NROW) : e[NROW];
+                    m[i] = !F8 ? mo[i] : Far ? __ldcg(e + 2 * NROW) : e[2 * NROW];
                 }
             }
+            float t = top, to_ = topo;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                t = fmaxf(t, m[i]);
+                if (F8) to_ = fmaxf(to_, mo[i]);
+            }
+            if (!F8) to_ = t;
+            // -inf before the first key: nothing to bring to the new references
+            const float rt = t == -INFINITY ? 0.0f : t, ro = to_ == -INFINITY ? 0.0f : to_;
+            const float down = ex2(topo - ro);
+            sum *= F8 ? ex2(top - rt) : down;
+            acc.x *= down;
+            acc.y *= down;
+            acc.z *= down;
+            acc.w *= down;
+            top = t;
+            topo = to_;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float w = ex2(mo[i] - ro);
+                sum += (F8 ? ex2(m[i] - rt) : w) * l[i];
+                acc.x += w * v[i].x;
+                acc.y += w * v[i].y;
+                acc.z += w * v[i].z;
+                acc.w += w * v[i].w;
+            }
         }
+        if (to) {
+            *reinterpret_cast<float4*>(to + g * DP + d) = acc;
+            if (d == 0) {
+                to[NROW * DP + g] = topo;
+                to[NROW * DP + NROW + g] = sum;
+                if (F8) to[NROW * DP + 2 * NROW + g] = top;
+            }
+            return;
+        }
+        const int h = row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
+        if (hg >= s.G || d >= s.a.D) return;
+        const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
+        const float inv = quotient(sum, top, topo);
+        put4(s.a, out * s.a.D + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (d == 0) put_lse(s.a, out, top, sum);
     }
 };
 
+// A part that a warp leaves behind: 2 w + 0 from its first row, 2 w + 1 from its last.
 struct Frag {
-    const float* at;            // null: none
-    int b, row;
+    int b, row;                 // b < 0: none
     int from_start, to_end;     // the part holds the row's first tile, its last tile
+    int far;                    // it lies in global memory (s.frags)
 };
 
 // A place on the line of tiles.
@@ -499,9 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t s_warp[kWarps];
     __shared__ Frag s_frag[2 * kWarps];
-    __shared__ int s_last;
+    __shared__ int s_first[2], s_c0[2], s_count[2];
     uint8_t* ring = smem;
-    uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kWarps * K::STAGES * K::STAGE);   // [B + 1]
+    uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kWarps * K::REGION);   // [B + 1]
     int* slen = reinterpret_cast<int*>(pre + s.a.B + 1);                               // [B]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = s.a.B, ps = s.a.page_size, cap = s.a.row * ps;
@@ -539,29 +689,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         __syncthreads();
     }
     if (tid == 0) pre[0] = 0;
-    if (tid < 2 * kWarps) s_frag[tid].at = nullptr;
+    if (tid < 2 * kWarps) s_frag[tid].b = -1;
     __syncthreads();
-    const unsigned long long W = (unsigned long long)base * s.R;
-    // enough tiles for every warp of a CTA, else fewer CTAs
-    const unsigned long long grid = min((unsigned long long)gridDim.x, (W + kWarps - 1) / kWarps);
+    // the CTAs' stretches, equal to one tile, and the warps' within them; fewer
+    // CTAs where they would not have a tile for every warp
+    const uint32_t W = base * (uint32_t)s.R;
+    const uint32_t grid = min(gridDim.x, (W + kWarps - 1) / kWarps);
     if (blockIdx.x >= grid) return;
-    const unsigned long long NW = grid * kWarps, me = (unsigned long long)blockIdx.x * kWarps + warp;
-    unsigned long long u = W * me / NW;
-    const unsigned long long end = W * (me + 1) / NW;
+    const uint32_t wq = W / grid, wr = W - wq * grid;
+    const uint32_t mine = wq + (blockIdx.x < wr ? 1u : 0u), per = mine / kWarps, left = mine % kWarps;
+    uint32_t u = blockIdx.x * wq + min((uint32_t)blockIdx.x, wr) + warp * per + min((uint32_t)warp, left);
+    const uint32_t end = u + per + ((uint32_t)warp < left ? 1u : 0u);
+    auto cta_of = [&](uint32_t at) { return at < wr * (wq + 1) ? at / (wq + 1) : wr + (at - wr * (wq + 1)) / wq; };
 
-    auto place_of = [&](unsigned long long at) {
+    auto place_of = [&](uint32_t at) {
         int lo = 0, hi = B - 1;
         while (lo < hi) {                       // the last sequence that begins at or before `at`
             const int mid = (lo + hi + 1) >> 1;
-            if ((unsigned long long)pre[mid] * s.R <= at) lo = mid;
+            if (pre[mid] * (uint32_t)s.R <= at) lo = mid;
             else hi = mid - 1;
         }
         Place p;
         p.b = lo;
         p.tiles = (int)(pre[lo + 1] - pre[lo]);
-        const unsigned long long in = at - (unsigned long long)pre[lo] * s.R;
-        p.row = (int)(in / (unsigned)p.tiles);
-        p.t = (int)(in - (unsigned long long)p.row * p.tiles);
+        const uint32_t in = at - pre[lo] * (uint32_t)s.R;
+        p.row = (int)(in / (uint32_t)p.tiles);
+        p.t = (int)(in - (uint32_t)p.row * (uint32_t)p.tiles);
         return p;
     };
     auto advance = [&](Place& p) {
@@ -576,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
 
     K k;
     if (u < end) {
-        uint8_t* my = ring + warp * (K::STAGES * K::STAGE);
+        uint8_t* my = ring + warp * K::REGION;
         const uint32_t my32 = smem_u32(my);
         // the producer's side: a window of 32 tiles' places in the pool, one a lane
         // (in blocks of 16 rows of one head: a page is a whole number of them)
@@ -584,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         int wb = -1, wt = 0;
         uint32_t blk[TT / 16];
         uint32_t badq = 0;                      // 2 bits a stage
-        Place pp = place_of(u);
-        unsigned long long up = u;
+        Place pp = place_of(u), cp = pp;
+        uint32_t up = u;
         const int rb = s.a.D * (F8 ? 1 : 2);    // bytes of a cached row
         const int c = lane % K::CPR, r0 = lane / K::CPR;
         const bool cin = c * 16 < rb;
@@ -646,7 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             if (up < end) issue(i);
             cp_async_commit();
         }
-        Place cp = place_of(u);
         int start = cp.t, first_seg = 1, stage = 0;
         k.load_q(s, cp.b, cp.row, lane);
         k.reset();
@@ -671,13 +823,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
                 k.store_out(s, cp.b, cp.row, lane);
             } else {
                 // a part: the last one of the stretch stays in the warp's ring, which
-                // is drained then; one that ends a row goes to global memory
-                float* to = u == end ? reinterpret_cast<float*>(my)
-                                     : s.frags + ((size_t)blockIdx.x * kWarps + warp) * K::PART;
-                k.store_part(to, lane);
+                // is drained then; one that ends a row before goes to global memory
+                const bool far = u != end;
+                k.store_part(far ? s.frags + ((size_t)blockIdx.x * kWarps + warp) * K::PART
+                                 : reinterpret_cast<float*>(my) + (first_seg ? 0 : K::PART), lane);
                 if (lane == 0) {
                     Frag& f = s_frag[2 * warp + (first_seg ? 0 : 1)];
-                    f.at = to;
+                    f.far = far;
                     f.b = cp.b;
                     f.row = cp.row;
                     f.from_start = start == 0;
@@ -692,47 +844,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             k.reset();
         }
     }
+    pdl_trigger();
     __syncthreads();
 
-    // the parts of each row in this CTA, then across CTAs
-    for (int i = 0; i < 2 * kWarps;) {
-        if (!s_frag[i].at) {
-            i++;
-            continue;
+    // Parts of one row in this CTA, at most one a warp.  Every warp reads the
+    // parts' heads at once, a lane each, and finds the rows' first parts by votes.
+    Frag fr;
+    fr.b = -1;
+    fr.row = fr.from_start = fr.to_end = fr.far = 0;
+    if (lane < 2 * kWarps) fr = s_frag[lane];
+    const unsigned there = __ballot_sync(0xFFFFFFFFu, fr.b >= 0);
+    const unsigned before = there & ((1u << lane) - 1u);
+    const int prev = before ? 31 - __clz(before) : lane;
+    const int pb = __shfl_sync(0xFFFFFFFFu, fr.b, prev), pr = __shfl_sync(0xFFFFFFFFu, fr.row, prev);
+    const unsigned heads = __ballot_sync(0xFFFFFFFFu, fr.b >= 0 && (!before || pb != fr.b || pr != fr.row));
+    const unsigned starts = __ballot_sync(0xFFFFFFFFu, fr.from_start), ends = __ballot_sync(0xFFFFFFFFu, fr.to_end);
+    const unsigned far = __ballot_sync(0xFFFFFFFFu, fr.b >= 0 && fr.far);
+    // those in global memory come to their warps' rings first, all in one trip
+    if (far) {
+#pragma unroll 1
+        for (unsigned rest = far; rest; rest &= rest - 1) {
+            const int w = (__ffs(rest) - 1) >> 1;
+            const float* from = s.frags + ((size_t)blockIdx.x * kWarps + w) * K::PART;
+            const uint32_t to = smem_u32(ring + w * K::REGION);
+            for (int i = tid; i < K::PART / 4; i += kThreads) cp_async16(to + 16 * i, from + 4 * i, 16);
         }
-        const int b = s_frag[i].b, row = s_frag[i].row;
-        const bool from_start = s_frag[i].from_start;
-        bool to_end = false;
-        int cnt = 0, e = i;
-        unsigned long long list = 0;            // indices, 4 bits each
-        for (; e < 2 * kWarps; e++) {
-            if (!s_frag[e].at) continue;
-            if (s_frag[e].b != b || s_frag[e].row != row) break;
-            list |= (unsigned long long)e << (4 * cnt);
-            cnt++;
-            to_end = s_frag[e].to_end;
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+    }
+    int open[2] = {-1, -1};                     // the parts of rows that began before this CTA, that go on after it
+    for (unsigned rest = heads; rest; rest &= rest - 1) {
+        const int f = __ffs(rest) - 1;
+        const unsigned after = rest & (rest - 1);
+        unsigned mem = there & ~((1u << f) - 1u) & (after ? (after & -after) - 1u : 0xFFFFFFFFu);
+        const int n = __popc(mem), last = 31 - __clz(mem);
+        const int b = __shfl_sync(0xFFFFFFFFu, fr.b, f), row = __shfl_sync(0xFFFFFFFFu, fr.row, f);
+        const int slot = (starts >> f) & 1;
+        const bool whole = slot && ((ends >> last) & 1);
+        if (!whole) open[slot] = f;
+        float* to = whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART;
+        for (int e = tid; e < NROW * DP / 4; e += kThreads) {
+            unsigned m = mem;
+            K::template merge<kWarps, false>(
+                s, n,
+                [&](int) {
+                    const int x = __ffs(m) - 1;
+                    m &= m - 1;
+                    return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART;
+                },
+                b, row, e / (DP / 4), e % (DP / 4) * 4, to);
         }
-        const bool whole = from_start && to_end;
-        const int slot = from_start ? 1 : 0;
-        K::template merge<false>(s, cnt, [&](int x) { return s_frag[(list >> (4 * x)) & 15].at; }, b, row, whole,
-                 s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
-        if (!whole) {
-            const unsigned long long tiles = pre[b + 1] - pre[b];
-            const unsigned long long r0 = (unsigned long long)pre[b] * s.R + row * tiles, r1 = r0 + tiles - 1;
-            const int c0 = (int)(((r0 + 1) * grid - 1) / W), c1 = (int)(((r1 + 1) * grid - 1) / W);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(s.tickets + (size_t)b * s.R + row, 1) == c1 - c0;
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                // c0 begins the row (slot 1) unless it begins with the row, too
-                K::template merge<true>(s, c1 - c0 + 1, [&](int x) { return s.parts + ((size_t)(c0 + x) * 2 + (x == 0 ? 1 : 0)) * K::PART; }, b, row,
-                         true, nullptr);
-                if (tid == 0) s.tickets[(size_t)b * s.R + row] = 0;
-            }
+    }
+    if (open[0] < 0 && open[1] < 0) return;
+
+    // Rows that other CTAs hold parts of, too: the last CTA to finish joins them.
+    if (tid < 2) {
+        s_first[tid] = -1;
+        const int f = open[tid];
+        if (f >= 0) {
+            const uint32_t tiles = pre[s_frag[f].b + 1] - pre[s_frag[f].b];
+            const uint32_t r0 = pre[s_frag[f].b] * (uint32_t)s.R + (uint32_t)s_frag[f].row * tiles;
+            s_c0[tid] = (int)cta_of(r0);
+            s_count[tid] = (int)cta_of(r0 + tiles - 1) - s_c0[tid] + 1;
         }
-        i = e;
+    }
+    __syncthreads();
+    if (tid < 2 && open[tid] >= 0) {
+        // the CTA's part was written before the barrier; its release and the
+        // others' acquisition are the ticket's
+        int* ticket = s.tickets + (size_t)s_frag[open[tid]].b * s.R + s_frag[open[tid]].row;
+        int old;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+        if (old == s_count[tid] - 1) {
+            *ticket = 0;
+            s_first[tid] = s_c0[tid];
+        }
+    }
+    __syncthreads();
+    for (int slot = 0; slot < 2; slot++) {
+        const int c0 = s_first[slot];
+        if (c0 < 0) continue;
+        // c0 holds the row's beginning, in its slot 1; the others' parts are in slot 0
+        for (int e = tid; e < NROW * DP / 4; e += kThreads)
+            K::template merge<16, true>(
+                s, s_count[slot],
+                [&](int i) { return s.parts + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * K::PART; }, s_frag[open[slot]].b,
+                s_frag[open[slot]].row, e / (DP / 4), e % (DP / 4) * 4, nullptr);
     }
 }
 
@@ -740,7 +938,7 @@ template <int DP, bool F8, int NROW>
 cudaError_t launch(const SplitArgs& s, cudaStream_t st)
 {
     using K = Kernel<DP, F8, NROW>;
-    const size_t smem = (size_t)kWarps * K::STAGES * K::STAGE + (2 * (size_t)s.a.B + 1) * 4;
+    const size_t smem = (size_t)kWarps * K::REGION + (2 * (size_t)s.a.B + 1) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.a.sms);
     cfg.blockDim = dim3(kThreads);
@@ -759,7 +957,7 @@ cudaError_t allow()
 {
     using K = Kernel<DP, F8, NROW>;
     return cudaFuncSetAttribute(k_attn<DP, F8, NROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kWarps * K::STAGES * K::STAGE + (2 * kAttnMaxSeqs + 1) * 4);
+                                kWarps * K::REGION + (2 * kAttnMaxSeqs + 1) * 4);
 }
 
 int rows_of(int hq, int hkv)
@@ -774,7 +972,7 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms)
 {
-    const size_t part = (size_t)part_floats(D <= 64 ? 64 : 128, hq / hkv <= 8 ? 8 : 16) * sizeof(float);
+    const size_t part = (size_t)part_floats(D <= 64 ? 64 : 128, true, hq / hkv <= 8 ? 8 : 16) * sizeof(float);
     AttnWorkspace w;
     w.tickets = 0;
     w.frags = align256((size_t)max_seqs * rows_of(hq, hkv) * sizeof(int));

@@ -45,6 +45,12 @@ def rope(x, pos, f, scale, layout):
     return y
 
 
+def scale_of(byte):
+    """ue8m0 bytes to fp64; 255 is NaN."""
+    s = byte.astype(np.float64)
+    return np.where(s == 255, np.nan, 2.0 ** (s - 127))
+
+
 def rows(pool, scales, pages, h, n):
     """The first n cached rows of one head over a list of pages, fp64 [n][D];
     a page id of None gives rows of NaN (to be left out)."""
@@ -56,17 +62,17 @@ def rows(pool, scales, pages, h, n):
         if scales is None:
             got[i * ps:(i + 1) * ps] = bf16(pool[p, h])
         else:
-            s = scales[p, h].astype(np.float64)
-            got[i * ps:(i + 1) * ps] = E4M3[pool[p, h]] * np.where(s == 255, np.nan, 2.0 ** (s - 127))[:, None]
+            got[i * ps:(i + 1) * ps] = E4M3[pool[p, h]] * scale_of(scales[p, h])[:, None]
     return got[:n]
 
 
 def attention(q, k, v, seen, scale, softcap=0.0):
     """q [G][D], k and v [n][D] in fp64, seen bool [n].  Returns (out [G][D],
-    lse [G], sum_j p_j |v_j| [G][D], max_j scale sum_i |q_i k_ij| [G], max |s|)."""
+    lse [G], sum_j p_j |v_j| [G][D], max_j scale sum_i |q_i k_ij| [G], max |s|,
+    p [G][seen])."""
     G, D = q.shape
     if not seen.any():
-        return np.zeros((G, D)), np.full(G, -np.inf), np.zeros((G, D)), np.zeros(G), 0.0
+        return np.zeros((G, D)), np.full(G, -np.inf), np.zeros((G, D)), np.zeros(G), 0.0, np.zeros((G, 0))
     k, v = k[seen], v[seen]
     s = scale * (q @ k.T)
     if softcap:
@@ -75,7 +81,7 @@ def attention(q, k, v, seen, scale, softcap=0.0):
     w = np.exp(s - top)
     p = w / w.sum(1, keepdims=True)
     size = np.array([(np.abs(q[g]) * np.abs(k)).sum(1).max() for g in range(G)]) * abs(scale)
-    return p @ v, top[:, 0] + np.log(w.sum(1)), p @ np.abs(v), size, float(np.abs(s).max())
+    return p @ v, top[:, 0] + np.log(w.sum(1)), p @ np.abs(v), size, float(np.abs(s).max()), p
 
 
 class Pages:

@@ -79,7 +79,14 @@ def check_attention(pool, q, lens, tab, page, out, lse, scale, softcap=0.0, wind
     the weights are off by the same relative amounts, twice (numerator and
     denominator); weights enter the product with 16 significant bits (2^-17),
     and n fp32 additions are taken as 4 sqrt(n) 2^-24.  All of it applies to
-    sum_j p_j |v_j|.  A bf16 output is off by half a step more."""
+    sum_j p_j |v_j|.  A bf16 output is off by half a step more.
+
+    An E4M3 row's weight is w_j = p_j s_j (s_j its scale) times codes c_j, held
+    as two f16 terms relative to a reference that keeps the largest weight so
+    far at 2^7 or above: f16's smallest steps are 2^-24, so each term is off by at
+    most 2^-25 beside its relative error, together 2^-24 = 2^-31 2^7.  The
+    output is therefore off by up to 2^-31 max_i w_i sum_j |c_jd| more (this
+    matters only where the row that dominates has a code of zero)."""
     hkv, D = pool.k.shape[1], pool.k.shape[3]
     B, hq = q.shape[:2]
     G = hq // hkv
@@ -95,10 +102,14 @@ def check_attention(pool, q, lens, tab, page, out, lse, scale, softcap=0.0, wind
             g = slice(h * G, (h + 1) * G)
             k = okv.rows(pool.k, pool.ks, ids, h, n)
             v = okv.rows(pool.v, pool.vs, ids, h, n)
-            ref, rl, size, prod, big = okv.attention(q[b, g], k, v, seen, scale, softcap)
+            ref, rl, size, prod, big, p = okv.attention(q[b, g], k, v, seen, scale, softcap)
             ds = 4 * np.sqrt(D) * 2.0 ** -24 * prod + 2.0 ** -21 * max(1.0, big)
             sums = 4 * np.sqrt(max(1, n)) * 2.0 ** -24
             tol = (2 * ds + 2.0 ** -16 + sums)[:, None] * size + 1e-37
+            if pool.ks is not None and p.size:
+                f = np.concatenate([okv.scale_of(pool.vs[i, h]) if i is not None else np.zeros(page) for i in ids])[:n][seen]
+                codes = np.abs(v[seen] / f[:, None]).sum(0)
+                tol = tol + 2.0 ** -31 * (p * f).max(1)[:, None] * codes
             if out_bf16:
                 tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
             err = np.abs(out[b, g] - ref)
