@@ -163,18 +163,6 @@ __device__ __forceinline__ void split<true>(float w0, float w1, uint32_t& hi, ui
     split_pair_f16(w0, w1, hi, lo);
 }
 
-// 2^(s - 127); 255 is the NaN scale
-__device__ __forceinline__ float ue8m0_value(uint32_t s)
-{
-    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FFFFFFFu : s << 23);
-}
-
-// s - 127, NaN for the NaN scale
-__device__ __forceinline__ float ue8m0_exponent(uint32_t s)
-{
-    return s == 255 ? __uint_as_float(0x7FFFFFFFu) : (float)(int)s - 127.0f;
-}
-
 // Chunk c of row r of a tile, swizzled so that eight rows' chunks of one
 // column lie in different banks.
 template <int ROWB>
@@ -197,7 +185,8 @@ struct Kernel {
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
     static constexpr int PART = part_floats(DP, F8, NROW);
-    static constexpr int REGION = STAGES * STAGE;            // a warp's ring, and at the end its parts
+    static constexpr int SCALES = F8 ? 8 * TT : 0;           // a tile's scales as numbers
+    static constexpr int REGION = STAGES * STAGE + SCALES;   // a warp's ring, and at the end its parts
     static_assert(REGION % 16 == 0 && PART % 4 == 0 && 4 * 2 * PART <= REGION, "a warp's parts fit its ring");
     static constexpr int QR = NROW == 8 ? 2 : 4;
 
@@ -287,9 +276,19 @@ struct Kernel {
 
     // One tile: `lo`, `hi` are the first and one past the last key of it that
     // count; bad: a bit per 16 keys left out.
-    __device__ __forceinline__ void tile(const SplitArgs& s, uint32_t st, const uint8_t* stp, int lane, int lo, int hi, uint32_t bad)
+    __device__ __forceinline__ void tile(const SplitArgs& s, uint32_t st, const uint8_t* stp, float* sc, int lane, int lo, int hi,
+                                         uint32_t bad)
     {
         const int j = lane & 3;
+        if (F8) {
+            // a key a lane: k's scale as a number (byte 0 as zero: below 2^-117 with any
+            // code), v's as an exponent; a NaN row has NaN codes
+            static_assert(!F8 || TT == 32, "a key a lane");
+            const uint8_t* b = stp + 2 * TT * ROWB + lane;
+            sc[lane] = __uint_as_float((uint32_t)b[0] << 23);
+            sc[TT + lane] = __uint_as_float(0x4B000000u | b[TT]) - 8388735.0f;      // 2^23 + byte, less 2^23 + 127
+            __syncwarp();
+        }
         const uint32_t kb = st, vb = st + TT * ROWB;
         float x[NT][4];
 #pragma unroll
@@ -327,14 +326,10 @@ struct Kernel {
         float y[F8 ? NT : 1][4];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            float f0 = 1.0f, f1 = 1.0f;
-            if (F8) {
-                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + 8 * n + 2 * j);
-                f0 = ue8m0_value(sc & 0xFF);
-                f1 = ue8m0_value(sc >> 8);
-            }
+            float2 f = make_float2(1.0f, 1.0f);
+            if (F8) f = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * j);
 #pragma unroll
-            for (int k = 0; k < NV; k++) x[n][k] *= F8 ? qf[k >> 1] * ((k & 1) ? f1 : f0) : qf[k >> 1];
+            for (int k = 0; k < NV; k++) x[n][k] *= F8 ? qf[k >> 1] * ((k & 1) ? f.y : f.x) : qf[k >> 1];
         }
         if (s.a.softcap > 0.0f) {
             const float cap = s.a.softcap * kLog2e;
@@ -346,10 +341,9 @@ struct Kernel {
         if (F8) {
 #pragma unroll
             for (int n = 0; n < NT; n++) {
-                const uint32_t sc = *reinterpret_cast<const uint16_t*>(stp + 2 * TT * ROWB + TT + 8 * n + 2 * j);
-                const float e0 = ue8m0_exponent(sc & 0xFF), e1 = ue8m0_exponent(sc >> 8);
+                const float2 e = *reinterpret_cast<const float2*>(sc + TT + 8 * n + 2 * j);
 #pragma unroll
-                for (int k = 0; k < NV; k++) y[n][k] = x[n][k] + ((k & 1) ? e1 : e0);
+                for (int k = 0; k < NV; k++) y[n][k] = x[n][k] + ((k & 1) ? e.y : e.x);
             }
         }
         if (lo > 0 || hi < TT || bad) {
@@ -742,6 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         const int rb = s.a.D * (F8 ? 1 : 2);    // bytes of a cached row
         const int c = lane % K::CPR, r0 = lane / K::CPR;
         const bool cin = c * 16 < rb;
+        // a lane's places in the pool's first row block
+        const uint8_t* klane = s.a.pool.k + (cin ? (size_t)r0 * rb + c * 16 : 0);
+        const uint8_t* vlane = s.a.pool.v + (cin ? (size_t)r0 * rb + c * 16 : 0);
+        const uint8_t* slane = lane ? s.a.pool.vs : s.a.pool.ks;
 
         auto issue = [&](int stage) {
             const int n = slen[pp.b], first = first_key(pp.b), t0 = first / TT, tile = t0 + pp.t;
@@ -764,29 +762,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
                 }
             }
             const uint32_t st = my32 + stage * K::STAGE;
-            const int h = pp.row / s.chunks;
-            const int lo = max(0, first - tile * TT), hi = min(TT, n - tile * TT);
-            uint32_t bad = 0;
+            const int h = s.chunks == 1 ? pp.row : pp.row / s.chunks;
+            const int lo = first - tile * TT, hi = n - tile * TT;           // keys [lo, hi) of the tile count
+            uint32_t at[TT / 16], bad = 0;
 #pragma unroll
             for (int i = 0; i < TT / 16; i++) {
-                const uint32_t at = __shfl_sync(0xFFFFFFFFu, blk[i], tile - wt);
-                const bool ok = at != 0xFFFFFFFFu;
-                bad |= ok ? 0u : 1u << i;
-                const size_t row = ok ? ((size_t)at + (size_t)(h * hblk)) * 16 : 0;
-                const uint8_t* ksrc = s.a.pool.k + row * rb + (cin ? c * 16 : 0);
-                const uint8_t* vsrc = s.a.pool.v + row * rb + (cin ? c * 16 : 0);
+                at[i] = __shfl_sync(0xFFFFFFFFu, blk[i], tile - wt);
+                bad |= at[i] == 0xFFFFFFFFu ? 1u << i : 0u;
+            }
+            if (rb == K::ROWB && lo <= 0 && hi >= TT && !bad) {
+                // the common tile: every address is one of two and a constant
 #pragma unroll
-                for (int r = 0; r < 16; r += K::RPI) {
-                    const int rr = 16 * i + r + r0;
-                    // rows that no key has are zeros, whatever the pool holds there
-                    const bool in = ok && cin && rr >= lo && rr < hi;
-                    const size_t off = in ? (size_t)(r + r0) * rb : 0;
-                    cp_async16(at_chunk<K::ROWB>(st, rr, c), ksrc + off, in ? 16 : 0);
-                    cp_async16(at_chunk<K::ROWB>(st + TT * K::ROWB, rr, c), vsrc + off, in ? 16 : 0);
+                for (int i = 0; i < TT / 16; i++) {
+                    const size_t row = ((size_t)at[i] + (uint32_t)(h * hblk)) * 16;
+                    const uint8_t* ksrc = klane + row * K::ROWB;
+                    const uint8_t* vsrc = vlane + row * K::ROWB;
+#pragma unroll
+                    for (int r = 0; r < 16; r += K::RPI) {
+                        cp_async16(at_chunk<K::ROWB>(st, 16 * i + r + r0, c), ksrc + r * K::ROWB, 16);
+                        cp_async16(at_chunk<K::ROWB>(st + TT * K::ROWB, 16 * i + r + r0, c), vsrc + r * K::ROWB, 16);
+                    }
+                    if (F8 && lane < 2) cp_async16(st + 2 * TT * K::ROWB + lane * TT + 16 * i, slane + row, 16);
                 }
-                if (F8 && lane < 2) {
-                    const uint8_t* src = (lane ? s.a.pool.vs : s.a.pool.ks) + row;
-                    cp_async16(st + 2 * TT * K::ROWB + lane * TT + 16 * i, src, ok ? 16 : 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < TT / 16; i++) {
+                    const bool ok = !((bad >> i) & 1);
+                    const size_t row = ok ? ((size_t)at[i] + (uint32_t)(h * hblk)) * 16 : 0;
+#pragma unroll
+                    for (int r = 0; r < 16; r += K::RPI) {
+                        const int rr = 16 * i + r + r0;
+                        // rows that no key has are zeros, whatever the pool holds there
+                        const bool in = ok && cin && rr >= lo && rr < hi;
+                        const size_t off = in ? row * rb + (size_t)r * rb : 0;
+                        cp_async16(at_chunk<K::ROWB>(st, rr, c), klane + off, in ? 16 : 0);
+                        cp_async16(at_chunk<K::ROWB>(st + TT * K::ROWB, rr, c), vlane + off, in ? 16 : 0);
+                    }
+                    if (F8 && lane < 2) cp_async16(st + 2 * TT * K::ROWB + lane * TT + 16 * i, slane + row, ok ? 16 : 0);
                 }
             }
             badq = (badq & ~(3u << (2 * stage))) | (bad << (2 * stage));
@@ -808,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             cp_async_wait<K::STAGES - 1>();
             __syncwarp();
             const int n = slen[cp.b], first = first_key(cp.b), at = (first / TT + cp.t) * TT;
-            k.tile(s, my32 + stage * K::STAGE, my + stage * K::STAGE, lane, max(0, first - at), min(TT, n - at),
+            k.tile(s, my32 + stage * K::STAGE, my + stage * K::STAGE, reinterpret_cast<float*>(my + K::STAGES * K::STAGE), lane, max(0, first - at), min(TT, n - at),
                    (badq >> (2 * stage)) & 3u);
             __syncwarp();
             stage = stage + 1 == K::STAGES ? 0 : stage + 1;
@@ -873,28 +885,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         cp_async_wait<0>();
         __syncthreads();
     }
-    int open[2] = {-1, -1};                     // the parts of rows that began before this CTA, that go on after it
-    for (unsigned rest = heads; rest; rest &= rest - 1) {
-        const int f = __ffs(rest) - 1;
-        const unsigned after = rest & (rest - 1);
-        unsigned mem = there & ~((1u << f) - 1u) & (after ? (after & -after) - 1u : 0xFFFFFFFFu);
-        const int n = __popc(mem), last = 31 - __clz(mem);
-        const int b = __shfl_sync(0xFFFFFFFFu, fr.b, f), row = __shfl_sync(0xFFFFFFFFu, fr.row, f);
-        const int slot = (starts >> f) & 1;
+    // four columns of a head a thread, the rows side by side
+    const int heads_in = min(NROW, s.G), items = heads_in * (DP / 4);
+    auto last_of = [&](int f) {                 // the last part of the row whose first is f
+        const unsigned after = heads & ~((2u << f) - 1u);
+        return 31 - __clz(there & (after ? (after & -after) - 1u : 0xFFFFFFFFu));
+    };
+    for (int e = tid; e < __popc(heads) * items; e += kThreads) {
+        unsigned rest = heads;
+        for (int i = e / items; i > 0; i--) rest &= rest - 1;
+        const int f = __ffs(rest) - 1, last = last_of(f);
+        unsigned mem = there & ((2u << last) - 1u) & ~((1u << f) - 1u);
+        const int n = __popc(mem), slot = (starts >> f) & 1;
         const bool whole = slot && ((ends >> last) & 1);
-        if (!whole) open[slot] = f;
         float* to = whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART;
-        for (int e = tid; e < NROW * DP / 4; e += kThreads) {
-            unsigned m = mem;
-            K::template merge<kWarps, false>(
-                s, n,
-                [&](int) {
-                    const int x = __ffs(m) - 1;
-                    m &= m - 1;
-                    return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART;
-                },
-                b, row, e / (DP / 4), e % (DP / 4) * 4, to);
-        }
+        const int i = e % items;
+        K::template merge<kWarps, false>(
+            s, n,
+            [&](int) {
+                const int x = __ffs(mem) - 1;
+                mem &= mem - 1;
+                return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART;
+            },
+            s_frag[f].b, s_frag[f].row, i / (DP / 4), i % (DP / 4) * 4, to);
+    }
+    // rows that began before this CTA, that go on after it: their first parts here
+    int open[2] = {-1, -1};
+    if (heads) {
+        const int f = __ffs(heads) - 1, l = 31 - __clz(heads);
+        if (!((starts >> f) & 1)) open[0] = f;
+        if (((starts >> l) & 1) && !((ends >> last_of(l)) & 1)) open[1] = l;
     }
     if (open[0] < 0 && open[1] < 0) return;
 
@@ -922,15 +942,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         }
     }
     __syncthreads();
-    for (int slot = 0; slot < 2; slot++) {
-        const int c0 = s_first[slot];
+    for (int e = tid; e < 2 * items; e += kThreads) {
+        const int slot = e >= items, i = slot ? e - items : e, c0 = s_first[slot];
         if (c0 < 0) continue;
         // c0 holds the row's beginning, in its slot 1; the others' parts are in slot 0
-        for (int e = tid; e < NROW * DP / 4; e += kThreads)
-            K::template merge<16, true>(
-                s, s_count[slot],
-                [&](int i) { return s.parts + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * K::PART; }, s_frag[open[slot]].b,
-                s_frag[open[slot]].row, e / (DP / 4), e % (DP / 4) * 4, nullptr);
+        K::template merge<16, true>(
+            s, s_count[slot],
+            [&](int x) { return s.parts + ((size_t)(c0 + x) * 2 + (x == 0 ? 1 : 0)) * K::PART; }, s_frag[open[slot]].b,
+            s_frag[open[slot]].row, i / (DP / 4), i % (DP / 4) * 4, nullptr);
     }
 }
 

@@ -60,7 +60,7 @@ struct AttnArgs {
 struct AttnWorkspace {
     size_t tickets, frags, parts, bytes;
 };
-constexpr int kAttnMaxSeqs = 4096;
+constexpr int kAttnMaxSeqs = 2048;
 AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms);
 cudaError_t attn_init_device();
 

@@ -452,7 +452,7 @@ typedef struct {
     int head_dim;           /* D, a multiple of 16 (E4M3: of 32), at most 128   */
     int page_size;          /* tokens of a page, a multiple of 16, at most 1024 */
     int num_pages;          /* pages of every pool                              */
-    int max_seqs;           /* rows of the page table, at most 4096             */
+    int max_seqs;           /* rows of the page table, at most 2048             */
     int max_pages_per_seq;  /* entries of a row                                 */
     int kv_dtype;           /* MOE_KV_*                                         */
     int out_dtype;          /* MOE_OUT_*: the attention's output                */

@@ -153,7 +153,7 @@ def test_cache_configs_and_null_handles_are_refused():
     bad += [("num_q_heads", 7, moe.MOE_ERR_INVALID_ARG), ("kv_dtype", 2, moe.MOE_ERR_INVALID_ARG),
             ("out_dtype", 2, moe.MOE_ERR_INVALID_ARG)]
     bad += [(k, v, moe.MOE_ERR_UNSUPPORTED) for k, v in
-            [("head_dim", 40), ("head_dim", 144), ("page_size", 24), ("page_size", 2048), ("max_seqs", 4097),
+            [("head_dim", 40), ("head_dim", 144), ("page_size", 24), ("page_size", 2048), ("max_seqs", 2049),
              ("num_q_heads", 514), ("max_pages_per_seq", 1 << 27)]]
     L = moe.lib()
     h = ctypes.c_void_p()
