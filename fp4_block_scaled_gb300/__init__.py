@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -42,7 +43,7 @@ EXPORTS = [
     "moe_ffn_set_mma_kind", "moe_ffn_set_routing_wait",
     "moe_ffn_profile_layer_only",
     "moe_kv_pool_bytes", "moe_kv_create", "moe_kv_status", "moe_kv_destroy", "moe_rope_table", "moe_rope",
-    "moe_kv_append", "moe_attn_decode", "moe_kv_copy_pages",
+    "moe_kv_append", "moe_attn_decode", "moe_kv_copy_pages", "moe_kv_call",
     "moe_kv_pages_create", "moe_kv_pages_open", "moe_kv_pages_extend", "moe_kv_pages_fork", "moe_kv_pages_free",
     "moe_kv_pages_compact", "moe_kv_pages_row", "moe_kv_pages_length", "moe_kv_pages_free_pages",
     "moe_kv_pages_refs", "moe_kv_pages_destroy",
@@ -161,6 +162,7 @@ def lib() -> ctypes.CDLL:
             "moe_kv_append": (I, [P, poolp, P, LL, P, LL, P, P, P, I, ropep, P, LL, P, P]),
             "moe_attn_decode": (I, [P, poolp, P, P, P, I, F, F, I, P, P, P]),
             "moe_kv_copy_pages": (I, [P, poolp, I, P, I, P]),
+            "moe_kv_call": (I, [I, ctypes.c_char_p]),
             "moe_kv_pages_create": (I, [I, I, I, I, ctypes.POINTER(P)]),
             "moe_kv_pages_open": (I, [P, ctypes.POINTER(I)]),
             "moe_kv_pages_extend": (I, [P, I, I, P]),
@@ -491,30 +493,62 @@ def rope(freqs, rot_dim: int, layout: int, scale: float = 1.0) -> moe_rope_desc:
     return moe_rope_desc(_p(freqs), int(rot_dim), int(layout), float(scale))
 
 
+# The calls of a decode step go through moe_kv_call: one ctypes argument where
+# each of a dozen would cost a conversion.  Tensors and streams are read first as
+# torch's; what is none (an address, a raw stream) takes _p and _s.
+_ROPE, _APPEND, _ATTN, _COPY = struct.Struct("=3Qq Qq QQq QQ"), struct.Struct("=3QqQq 3Qq QQq QQ"), \
+    struct.Struct("=5QqddqQQQ"), struct.Struct("=QQqQqQ")
+
+
+def _kv_call(op: int, words: bytes, where: str) -> None:
+    rc = (_lib or lib()).moe_kv_call(op, words)
+    if rc:
+        raise MoeError(rc, where)
+
+
 def moe_rope(h, rope: moe_rope_desc, pos, T: int, q=None, q_out=None, k=None, k_out=None, ldq: int = 0, ldk: int = 0,
              stream=None):
-    _check(lib().moe_rope(h, ctypes.byref(rope), _p(pos), int(T), _p(q), int(ldq), _p(q_out), _p(k), int(ldk),
-                          _p(k_out), _s(stream)), "moe_rope")
+    d = ctypes.addressof(rope)
+    try:
+        w = _ROPE.pack(h, d, pos.data_ptr(), T, 0 if q is None else q.data_ptr(), ldq, 0 if q_out is None else q_out.data_ptr(),
+                       0 if k is None else k.data_ptr(), ldk, 0 if k_out is None else k_out.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _ROPE.pack(h or 0, d, _p(pos) or 0, T, _p(q) or 0, ldq, _p(q_out) or 0, _p(k) or 0, ldk, _p(k_out) or 0,
+                       _s(stream) or 0)
+    _kv_call(0, w, "moe_rope")
 
 
 def moe_kv_append(h, pool: moe_kv_pool, k, v, pos, page_table, T: int, seq=None, rope: moe_rope_desc | None = None,
                   q=None, q_out=None, ldq: int = 0, ldk: int = 0, ldv: int = 0, stream=None):
-    _check(lib().moe_kv_append(h, ctypes.byref(pool), _p(k), int(ldk), _p(v), int(ldv), _p(pos), _p(seq),
-                               _p(page_table), int(T), ctypes.byref(rope) if rope is not None else None, _p(q),
-                               int(ldq), _p(q_out), _s(stream)), "moe_kv_append")
+    p, d = ctypes.addressof(pool), 0 if rope is None else ctypes.addressof(rope)
+    try:
+        w = _APPEND.pack(h, p, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(), 0 if seq is None else seq.data_ptr(),
+                         page_table.data_ptr(), T, d, 0 if q is None else q.data_ptr(), ldq,
+                         0 if q_out is None else q_out.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _APPEND.pack(h or 0, p, _p(k) or 0, ldk, _p(v) or 0, ldv, _p(pos) or 0, _p(seq) or 0, _p(page_table) or 0, T, d,
+                         _p(q) or 0, ldq, _p(q_out) or 0, _s(stream) or 0)
+    _kv_call(1, w, "moe_kv_append")
 
 
 def moe_attn_decode(h, pool: moe_kv_pool, q, seq_lens, page_table, B: int, out, lse=None, scale: float = 0.0,
                     softcap: float = 0.0, window: int = 0, stream=None):
     """scale 0: 1 / sqrt(head_dim)."""
-    _check(lib().moe_attn_decode(h, ctypes.byref(pool), _p(q), _p(seq_lens), _p(page_table), int(B), float(scale),
-                                 float(softcap), int(window), _p(out), _p(lse), _s(stream)), "moe_attn_decode")
+    p = ctypes.addressof(pool)
+    try:
+        w = _ATTN.pack(h, p, q.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B, scale, softcap, window,
+                       out.data_ptr(), 0 if lse is None else lse.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _ATTN.pack(h or 0, p, _p(q) or 0, _p(seq_lens) or 0, _p(page_table) or 0, B, scale, softcap, window,
+                       _p(out) or 0, _p(lse) or 0, _s(stream) or 0)
+    _kv_call(2, w, "moe_attn_decode")
 
 
 def moe_kv_copy_pages(h, pools, pairs, n: int, stream=None):
     """pools: a sequence of moe_kv_pool, one per layer; pairs: device int32 [n][2] of (src, dst) page ids."""
-    arr = (moe_kv_pool * len(pools))(*pools)
-    _check(lib().moe_kv_copy_pages(h, arr, len(pools), _p(pairs), int(n), _s(stream)), "moe_kv_copy_pages")
+    arr = ctypes.create_string_buffer(b"".join(pools))
+    _kv_call(3, _COPY.pack(h or 0, ctypes.addressof(arr), len(pools), _p(pairs) or 0, n, _s(stream) or 0),
+             "moe_kv_copy_pages")
 
 
 def moe_kv_pages_create(num_pages: int, page_size: int, max_seqs: int, max_pages_per_seq: int) -> int:

@@ -222,32 +222,42 @@ struct Kernel {
     {
         const int g = lane >> 2, j = lane & 3, D = s.a.D;
         const int h = row / s.chunks, c = row - h * s.chunks;
-        const float f = s.a.softcap > 0.0f ? s.a.scale / s.a.softcap : s.a.scale * 1.4426950408889634f;
 #pragma unroll
         for (int half = 0; half < NROW / 8; half++) {
             const int hg = c * NROW + g + 8 * half;
             const bool in = hg < s.G;
             const uint16_t* src = s.a.q + ((size_t)b * s.a.hq + h * s.G + (in ? hg : 0)) * D;
-            uint32_t x[KS], y[KS];
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) {
-                x[ks] = y[ks] = 0;
+                uint32_t x = 0, y = 0;
                 if (in && 16 * ks < D) {
                     if (F8) {
                         const uint2 u = *reinterpret_cast<const uint2*>(src + 16 * ks + 4 * j);
-                        x[ks] = u.x;
-                        y[ks] = u.y;
+                        x = u.x;
+                        y = u.y;
                     } else {
-                        x[ks] = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j);
-                        y[ks] = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j + 8);
+                        x = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j);
+                        y = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * j + 8);
                     }
                 }
+                q[ks][NROW == 8 ? 0 : half] = x;
+                q[ks][NROW == 8 ? 1 : 2 + half] = y;
             }
+        }
+    }
+
+    // What load_q left, ready for the products.
+    __device__ __forceinline__ void ready_q(const SplitArgs& s)
+    {
+        const float f = s.a.softcap > 0.0f ? s.a.scale / s.a.softcap : s.a.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int half = 0; half < NROW / 8; half++) {
             qf[half] = f;
             if (F8) {
+                const int qx = NROW == 8 ? 0 : half, qy = NROW == 8 ? 1 : 2 + half;
                 uint32_t top = 0;               // bf16 magnitudes order as integers
 #pragma unroll
-                for (int ks = 0; ks < KS; ks++) top = __vmaxu2(top, __vmaxu2(x[ks] & 0x7FFF7FFFu, y[ks] & 0x7FFF7FFFu));
+                for (int ks = 0; ks < KS; ks++) top = __vmaxu2(top, __vmaxu2(q[ks][qx] & 0x7FFF7FFFu, q[ks][qy] & 0x7FFF7FFFu));
                 top = max(top & 0xFFFFu, top >> 16);
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
@@ -256,14 +266,10 @@ struct Kernel {
                 qf[half] = f * exp2i(-e);
 #pragma unroll
                 for (int ks = 0; ks < KS; ks++) {
-                    x[ks] = pack_f16(__uint_as_float(x[ks] << 16) * up, __uint_as_float(x[ks] & 0xFFFF0000u) * up);
-                    y[ks] = pack_f16(__uint_as_float(y[ks] << 16) * up, __uint_as_float(y[ks] & 0xFFFF0000u) * up);
+                    const uint32_t x = q[ks][qx], y = q[ks][qy];
+                    q[ks][qx] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up);
+                    q[ks][qy] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up);
                 }
-            }
-#pragma unroll
-            for (int ks = 0; ks < KS; ks++) {
-                q[ks][NROW == 8 ? 0 : half] = x[ks];
-                q[ks][NROW == 8 ? 1 : 2 + half] = y[ks];
             }
         }
     }
@@ -553,74 +559,101 @@ struct Kernel {
         if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
 
-    // The parts at(i), i < n, of a row, four columns from d of its row g: one
-    // pass, N parts at a time with all their loads in flight.  Far: written by
-    // other CTAs.  The result is the row's output, or part `to`.
-    template <int N, bool Far, class At>
-    __device__ __forceinline__ static void merge(const SplitArgs& s, int n, At at, int b, int row, int g, int d, float* to)
+    static constexpr int VEC = DP / 32;         // columns a lane in a merge
+
+    __device__ __forceinline__ static void load_vec(float (&v)[VEC], const float* p, bool far)
     {
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float top = -INFINITY, topo = -INFINITY, sum = 0.0f;
-        for (int i0 = 0; i0 < n; i0 += N) {
-            float4 v[N];
-            float mo[N], l[N], m[N];
+        if (VEC == 4) {
+            const float4 x = far ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
+            v[0] = x.x;
+            v[1] = x.y;
+            v[VEC - 2] = x.z;
+            v[VEC - 1] = x.w;
+        } else {
+            const float2 x = far ? __ldcg(reinterpret_cast<const float2*>(p)) : *reinterpret_cast<const float2*>(p);
+            v[0] = x.x;
+            v[1] = x.y;
+        }
+    }
+
+    // A row's parts merged by one warp: lane i holds part i's numbers (mine: it
+    // has one), every lane VEC columns of all.  N parts' loads are in flight at a
+    // time; at(i) is part i, i < n.  Far: written by other CTAs.
+    template <int N, bool Far, class At>
+    struct Merge {
+        float acc[VEC], top, topo, sum;
+
+        __device__ __forceinline__ void reset()
+        {
 #pragma unroll
-            for (int i = 0; i < N; i++) {
-                mo[i] = m[i] = -INFINITY;
-                l[i] = 0.0f;
-                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (i0 + i < n) {
-                    const float* p = at(i0 + i);
-                    const float* e = p + NROW * DP + g;
-                    v[i] = Far ? __ldcg(reinterpret_cast<const float4*>(p + g * DP + d)) : *reinterpret_cast<const float4*>(p + g * DP + d);
-                    mo[i] = Far ? __ldcg(e) : e[0];
-                    l[i] = Far ? __ldcg(e + NROW) : e[NROW];
-                    m[i] = !F8 ? mo[i] : Far ? __ldcg(e + 2 * NROW) : e[2 * NROW];
-                }
+            for (int k = 0; k < VEC; k++) acc[k] = 0.0f;
+            top = topo = -INFINITY;
+            sum = 0.0f;
+        }
+
+        // up to 32 more parts, of which `members` are there
+        __device__ __forceinline__ void add(unsigned members, At at, int g, int lane)
+        {
+            float mo = -INFINITY, m = -INFINITY, l = 0.0f;
+            if ((members >> lane) & 1) {
+                const float* e = at(lane) + NROW * DP + g;
+                mo = Far ? __ldcg(e) : e[0];
+                l = Far ? __ldcg(e + NROW) : e[NROW];
+                m = !F8 ? mo : Far ? __ldcg(e + 2 * NROW) : e[2 * NROW];
             }
-            float t = top, to_ = topo;
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                t = fmaxf(t, m[i]);
-                if (F8) to_ = fmaxf(to_, mo[i]);
-            }
-            if (!F8) to_ = t;
+            const float to_ = fmaxf(topo, warp_max(mo)), t = F8 ? fmaxf(top, warp_max(m)) : to_;
             // -inf before the first key: nothing to bring to the new references
             const float rt = t == -INFINITY ? 0.0f : t, ro = to_ == -INFINITY ? 0.0f : to_;
-            const float down = ex2(topo - ro);
-            sum *= F8 ? ex2(top - rt) : down;
-            acc.x *= down;
-            acc.y *= down;
-            acc.z *= down;
-            acc.w *= down;
+            const float down = ex2(topo - ro), w = ex2(mo - ro);
+            sum = sum * (F8 ? ex2(top - rt) : down) + warp_sum((F8 ? ex2(m - rt) : w) * l);
             top = t;
             topo = to_;
 #pragma unroll
-            for (int i = 0; i < N; i++) {
-                const float w = ex2(mo[i] - ro);
-                sum += (F8 ? ex2(m[i] - rt) : w) * l[i];
-                acc.x += w * v[i].x;
-                acc.y += w * v[i].y;
-                acc.z += w * v[i].z;
-                acc.w += w * v[i].w;
+            for (int k = 0; k < VEC; k++) acc[k] *= down;
+            while (members) {
+                float v[N][VEC], f[N];
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    const int x = members ? __ffs(members) - 1 : -1;
+                    members &= members - 1;
+                    f[i] = __shfl_sync(0xFFFFFFFFu, w, x & 31);
+                    if (x < 0) f[i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < VEC; k++) v[i][k] = 0.0f;
+                    if (x >= 0) load_vec(v[i], at(x) + g * DP + lane * VEC, Far);
+                }
+#pragma unroll
+                for (int i = 0; i < N; i++)
+#pragma unroll
+                    for (int k = 0; k < VEC; k++) acc[k] = fmaf(f[i], v[i][k], acc[k]);
             }
         }
-        if (to) {
-            *reinterpret_cast<float4*>(to + g * DP + d) = acc;
-            if (d == 0) {
-                to[NROW * DP + g] = topo;
-                to[NROW * DP + NROW + g] = sum;
-                if (F8) to[NROW * DP + 2 * NROW + g] = top;
+
+        // to the row's part `to`, or as the row's output
+        __device__ __forceinline__ void finish(const SplitArgs& s, int b, int row, int g, int lane, float* to) const
+        {
+            const int d = lane * VEC;
+            if (to) {
+                if (VEC == 4) *reinterpret_cast<float4*>(to + g * DP + d) = make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]);
+                else *reinterpret_cast<float2*>(to + g * DP + d) = make_float2(acc[0], acc[1]);
+                if (lane == 0) {
+                    to[NROW * DP + g] = topo;
+                    to[NROW * DP + NROW + g] = sum;
+                    if (F8) to[NROW * DP + 2 * NROW + g] = top;
+                }
+                return;
             }
-            return;
+            const int h = s.chunks == 1 ? row : row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
+            if (hg >= s.G) return;
+            const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
+            const float inv = quotient(sum, top, topo);
+            if (d < s.a.D) {
+                if (VEC == 4) put4(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv, acc[VEC - 2] * inv, acc[VEC - 1] * inv);
+                else put2(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv);
+            }
+            if (lane == 0) put_lse(s.a, out, top, sum);
         }
-        const int h = row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
-        if (hg >= s.G || d >= s.a.D) return;
-        const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
-        const float inv = quotient(sum, top, topo);
-        put4(s.a, out * s.a.D + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (d == 0) put_lse(s.a, out, top, sum);
-    }
+    };
 };
 
 // A part that a warp leaves behind: 2 w + 0 from its first row, 2 w + 1 from its last.
@@ -806,13 +839,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             if (up < end) advance(pp);
         };
 
-#pragma unroll
+        k.load_q(s, cp.b, cp.row, lane);        // ahead of the ring's first loads
+#pragma unroll 1
         for (int i = 0; i < K::STAGES - 1; i++) {
             if (up < end) issue(i);
             cp_async_commit();
         }
         int start = cp.t, first_seg = 1, stage = 0;
-        k.load_q(s, cp.b, cp.row, lane);
+        k.ready_q(s);
         k.reset();
         while (true) {
             if (up < end) issue(stage == 0 ? K::STAGES - 1 : stage - 1);
@@ -853,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             start = 0;
             first_seg = 0;
             k.load_q(s, cp.b, cp.row, lane);
+            k.ready_q(s);
             k.reset();
         }
     }
@@ -885,29 +920,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         cp_async_wait<0>();
         __syncthreads();
     }
-    // four columns of a head a thread, the rows side by side
-    const int heads_in = min(NROW, s.G), items = heads_in * (DP / 4);
+    // a warp a head, the rows side by side
+    const int heads_in = min(NROW, s.G);
     auto last_of = [&](int f) {                 // the last part of the row whose first is f
         const unsigned after = heads & ~((2u << f) - 1u);
         return 31 - __clz(there & (after ? (after & -after) - 1u : 0xFFFFFFFFu));
     };
-    for (int e = tid; e < __popc(heads) * items; e += kThreads) {
+    auto near = [&](int x) { return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART; };
+    for (int e = warp; e < __popc(heads) * heads_in; e += kWarps) {
         unsigned rest = heads;
-        for (int i = e / items; i > 0; i--) rest &= rest - 1;
-        const int f = __ffs(rest) - 1, last = last_of(f);
-        unsigned mem = there & ((2u << last) - 1u) & ~((1u << f) - 1u);
-        const int n = __popc(mem), slot = (starts >> f) & 1;
+        for (int i = e / heads_in; i > 0; i--) rest &= rest - 1;
+        const int f = __ffs(rest) - 1, last = last_of(f), g = e % heads_in;
+        const int slot = (starts >> f) & 1;
         const bool whole = slot && ((ends >> last) & 1);
-        float* to = whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART;
-        const int i = e % items;
-        K::template merge<kWarps, false>(
-            s, n,
-            [&](int) {
-                const int x = __ffs(mem) - 1;
-                mem &= mem - 1;
-                return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART;
-            },
-            s_frag[f].b, s_frag[f].row, i / (DP / 4), i % (DP / 4) * 4, to);
+        typename K::template Merge<4, false, decltype(near)> m;
+        m.reset();
+        m.add(there & ((2u << last) - 1u) & ~((1u << f) - 1u), near, g, lane);
+        m.finish(s, s_frag[f].b, s_frag[f].row, g, lane, whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
     }
     // rows that began before this CTA, that go on after it: their first parts here
     int open[2] = {-1, -1};
@@ -942,14 +971,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         }
     }
     __syncthreads();
-    for (int e = tid; e < 2 * items; e += kThreads) {
-        const int slot = e >= items, i = slot ? e - items : e, c0 = s_first[slot];
+    for (int e = warp; e < 2 * heads_in; e += kWarps) {
+        const int slot = e >= heads_in, g = slot ? e - heads_in : e, c0 = s_first[slot], n = s_count[slot];
         if (c0 < 0) continue;
+        int i0 = 0;
         // c0 holds the row's beginning, in its slot 1; the others' parts are in slot 0
-        K::template merge<16, true>(
-            s, s_count[slot],
-            [&](int x) { return s.parts + ((size_t)(c0 + x) * 2 + (x == 0 ? 1 : 0)) * K::PART; }, s_frag[open[slot]].b,
-            s_frag[open[slot]].row, i / (DP / 4), i % (DP / 4) * 4, nullptr);
+        auto far_part = [&](int x) { return s.parts + ((size_t)(c0 + i0 + x) * 2 + (i0 + x == 0 ? 1 : 0)) * K::PART; };
+        typename K::template Merge<16, true, decltype(far_part)> m;
+        m.reset();
+        for (; i0 < n; i0 += 32) m.add(n - i0 >= 32 ? 0xFFFFFFFFu : (1u << (n - i0)) - 1u, far_part, g, lane);
+        m.finish(s, s_frag[open[slot]].b, s_frag[open[slot]].row, g, lane, nullptr);
     }
 }
 

@@ -381,4 +381,89 @@ int moe_kv_copy_pages(moe_kv_t h, const moe_kv_pool* pools, int num_pools, const
     return cuda_rc(e);
 }
 
+namespace {
+
+// The words of a moe_kv_call, in order.
+struct Words {
+    const int64_t* w;
+    bool ok = true;
+    void* p() { return (void*)(uintptr_t)*w++; }
+    long long ll() { return *w++; }
+    int i()
+    {
+        ok = ok && *w >= INT32_MIN && *w <= INT32_MAX;
+        return (int)*w++;
+    }
+    float f()
+    {
+        double d;
+        memcpy(&d, w++, 8);
+        return (float)d;
+    }
+};
+
+}  // namespace
+
+int moe_kv_call(int op, const int64_t* words)
+{
+    if (!words) return MOE_ERR_INVALID_ARG;
+    Words a{words};
+    if (op == MOE_KV_CALL_ROPE) {
+        auto h = (moe_kv_t)a.p();
+        auto rope = (const moe_rope_desc*)a.p();
+        auto pos = (const int32_t*)a.p();
+        const int T = a.i();
+        const void* q = a.p();
+        const long long ldq = a.ll();
+        void* q_out = a.p();
+        const void* k = a.p();
+        const long long ldk = a.ll();
+        void* k_out = a.p();
+        void* stream = a.p();
+        return a.ok ? moe_rope(h, rope, pos, T, q, ldq, q_out, k, ldk, k_out, stream) : MOE_ERR_INVALID_ARG;
+    }
+    if (op == MOE_KV_CALL_APPEND) {
+        auto h = (moe_kv_t)a.p();
+        auto pool = (const moe_kv_pool*)a.p();
+        const void* k = a.p();
+        const long long ldk = a.ll();
+        const void* v = a.p();
+        const long long ldv = a.ll();
+        auto pos = (const int32_t*)a.p();
+        auto seq = (const int32_t*)a.p();
+        auto table = (const int32_t*)a.p();
+        const int T = a.i();
+        auto rope = (const moe_rope_desc*)a.p();
+        const void* q = a.p();
+        const long long ldq = a.ll();
+        void* q_out = a.p();
+        void* stream = a.p();
+        return a.ok ? moe_kv_append(h, pool, k, ldk, v, ldv, pos, seq, table, T, rope, q, ldq, q_out, stream) : MOE_ERR_INVALID_ARG;
+    }
+    if (op == MOE_KV_CALL_ATTN_DECODE) {
+        auto h = (moe_kv_t)a.p();
+        auto pool = (const moe_kv_pool*)a.p();
+        const void* q = a.p();
+        auto lens = (const int32_t*)a.p();
+        auto table = (const int32_t*)a.p();
+        const int B = a.i();
+        const float scale = a.f(), softcap = a.f();
+        const int window = a.i();
+        void* out = a.p();
+        auto lse = (float*)a.p();
+        void* stream = a.p();
+        return a.ok ? moe_attn_decode(h, pool, q, lens, table, B, scale, softcap, window, out, lse, stream) : MOE_ERR_INVALID_ARG;
+    }
+    if (op == MOE_KV_CALL_COPY_PAGES) {
+        auto h = (moe_kv_t)a.p();
+        auto pools = (const moe_kv_pool*)a.p();
+        const int num = a.i();
+        auto pairs = (const int32_t*)a.p();
+        const int n = a.i();
+        void* stream = a.p();
+        return a.ok ? moe_kv_copy_pages(h, pools, num, pairs, n, stream) : MOE_ERR_INVALID_ARG;
+    }
+    return MOE_ERR_INVALID_ARG;
+}
+
 }  // extern "C"

@@ -66,134 +66,154 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float down)
+// Eight bf16 values times `down`, as E4M3.
+__device__ __forceinline__ uint2 quant8(const uint4& u, float down)
 {
-    uint32_t o[2];
+    float f[8];
+    unpack8(u, f);
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
-        o[i] = (uint32_t)e4m3_rn_sat(f[4 * i] * down) | ((uint32_t)e4m3_rn_sat(f[4 * i + 1] * down) << 8) |
-               ((uint32_t)e4m3_rn_sat(f[4 * i + 2] * down) << 16) | ((uint32_t)e4m3_rn_sat(f[4 * i + 3] * down) << 24);
-    return make_uint2(o[0], o[1]);
+    for (int i = 0; i < 4; i++)
+        o[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * down, f[2 * i + 1] * down), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
 }
 
-// One lane holds 16 elements of a head, as two runs of 8: with MOE_ROPE_HALF
-// the rotated lanes hold a pair's halves (8 e and rot / 2 + 8 e), all others 16
-// elements in a row.  GL lanes (a power of two) hold a head.
-template <int GL>
-__global__ void __launch_bounds__(256) k_rope(RopeArgs a, int split)
+// The largest magnitude of eight bf16 values, both halves (bf16 magnitudes
+// order as integers, a NaN above all).
+__device__ __forceinline__ uint32_t amax8(const uint4& u)
 {
-    pdl_wait();
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    return __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
+}
+
+// Heads whose loads a lane has in flight: 1, 2 and 4 took 69.4, 58.0 and 54.3 us
+// for the queries and keys of 16383 tokens (40 heads of 128), where the bytes
+// alone take 49.5 us.
+constexpr int kAhead = 4;
+
+// GL lanes (a power of two) hold a token's head, 16 elements a lane as two runs
+// of 8: with MOE_ROPE_HALF the rotated lanes hold a pair's halves (8 e and
+// rot / 2 + 8 e), all others 16 elements in a row; either way a lane needs the
+// same eight angles for every head, and computes them once.  The token's heads
+// (q, k, v one after another) are dealt to gridDim.y blocks.
+template <int GL>
+__global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a)
+{
     const int e = threadIdx.x & (GL - 1);
-    const long long g = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / GL;
-    const int t = (int)(g / split), u0 = (int)(g % split);
+    const int t = (int)(((size_t)blockIdx.x * 256 + threadIdx.x) / GL);
     const bool in = t < a.T && 16 * e < a.D;
-    const int pos = t < a.T ? a.pos[t] : -1;
-    // no shuffle crosses a group, and a group's lanes leave together
-    if (pos < 0) return;
     const bool rotated = a.freqs && 16 * e < a.rot;
     const bool half = rotated && a.layout == MOE_ROPE_HALF;
-    const int c0 = half ? 8 * e : 16 * e, c1 = half ? a.rot / 2 + 8 * e : 16 * e + 8;
+    const int units = a.hq + a.hk + a.hv, split = gridDim.y;
+    pdl_wait();
+    const int pos = t < a.T ? a.pos[t] : -1;
+    const int sq = a.append && a.seq && t < a.T ? a.seq[t] : t;
+    uint4 r0[kAhead], r1[kAhead];
+    // heads [0, hq) are q's, then k's, then v's: where unit u's lane elements lie in its head
+    auto turns = [&](int u) { return rotated && u < a.hq + a.hk; };
+    auto at0 = [&](int u) { return turns(u) && half ? 8 * e : 16 * e; };
+    auto at1 = [&](int u) { return turns(u) && half ? a.rot / 2 + 8 * e : 16 * e + 8; };
+    auto load = [&](int i, int u) {
+        r0[i] = r1[i] = make_uint4(0, 0, 0, 0);
+        if (u >= units || !in) return;
+        const uint16_t* src = u < a.hq          ? a.q + (size_t)t * a.ldq + (size_t)u * a.D
+                              : u < a.hq + a.hk ? a.k + (size_t)t * a.ldk + (size_t)(u - a.hq) * a.D
+                                                : a.v + (size_t)t * a.ldv + (size_t)(u - a.hq - a.hk) * a.D;
+        r0[i] = *reinterpret_cast<const uint4*>(src + at0(u));
+        r1[i] = *reinterpret_cast<const uint4*>(src + at1(u));
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) load(i, blockIdx.y + i * split);
+    uint64_t F[8];
+    if (rotated) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) F[i] = a.freqs[8 * e + i];
+    }
+    // a group's lanes share t and leave together; no shuffle crosses a group
+    if (pos < 0) return;
     Turn w[8];
     if (rotated) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = turn_of(a.freqs[8 * e + i], (uint32_t)pos, a.scale);
+        for (int i = 0; i < 8; i++) w[i] = turn_of(F[i], (uint32_t)pos, a.scale);
     }
-    long long slot = -1;                // (page, offset) of the token, as a row of the pool without its heads
-    int page = 0, off = 0;
+    bool placed = false;
+    size_t row = 0;             // the token's row in the pool, of head 0
     if (a.append) {
-        const int sq = a.seq ? a.seq[t] : t;
         const int pi = pos / a.page_size;
-        bool ok = sq >= 0 && sq < a.max_seqs && pi < a.row;
-        if (ok) {
-            page = a.table[(size_t)sq * a.row + pi];
-            ok = page >= 0 && page < a.num_pages;
-        }
-        off = pos - pi * a.page_size;
-        if (ok) slot = 0;
-        else if (e == 0 && u0 == 0) atomicOr(a.status, kStatusBadIndex);
+        int page = -1;
+        if (sq >= 0 && sq < a.max_seqs && pi < a.row) page = a.table[(size_t)sq * a.row + pi];
+        placed = page >= 0 && page < a.num_pages;
+        if (placed) row = (size_t)page * a.hk * a.page_size + (pos - pi * a.page_size);
+        else if (e == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadIndex);
     }
-    const int units = a.hq + a.hk + a.hv;
-    for (int u = u0; u < units; u += split) {
-        const int kind = u < a.hq ? 0 : u < a.hq + a.hk ? 1 : 2;
-        const int h = kind == 0 ? u : kind == 1 ? u - a.hq : u - a.hq - a.hk;
-        const uint16_t* src = kind == 0 ? a.q + (size_t)t * a.ldq : kind == 1 ? a.k + (size_t)t * a.ldk : a.v + (size_t)t * a.ldv;
-        src += (size_t)h * a.D;
-        const bool turn = rotated && kind != 2;
-        const int i0 = turn ? c0 : 16 * e, i1 = turn ? c1 : 16 * e + 8;
-        float x0[8] = {}, x1[8] = {};
-        uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-        if (in) {
-            r0 = *reinterpret_cast<const uint4*>(src + i0);
-            r1 = *reinterpret_cast<const uint4*>(src + i1);
-        }
-        if (turn) {
-            unpack8(r0, x0);
-            unpack8(r1, x1);
-            float y0[8], y1[8];
-            if (a.layout == MOE_ROPE_HALF) {
+    for (int u0 = blockIdx.y; u0 < units; u0 += kAhead * split) {
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    y0[i] = x0[i] * w[i].c - x1[i] * w[i].s;
-                    y1[i] = x1[i] * w[i].c + x0[i] * w[i].s;
+        for (int i = 0; i < kAhead; i++) {
+            const int u = u0 + i * split;
+            if (u >= units) break;
+            if (turns(u)) {
+                float x0[8], x1[8], y0[8], y1[8];
+                unpack8(r0[i], x0);
+                unpack8(r1[i], x1);
+                if (a.layout == MOE_ROPE_HALF) {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        y0[k] = x0[k] * w[k].c - x1[k] * w[k].s;
+                        y1[k] = x1[k] * w[k].c + x0[k] * w[k].s;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        y0[2 * k] = x0[2 * k] * w[k].c - x0[2 * k + 1] * w[k].s;
+                        y0[2 * k + 1] = x0[2 * k + 1] * w[k].c + x0[2 * k] * w[k].s;
+                        y1[2 * k] = x1[2 * k] * w[4 + k].c - x1[2 * k + 1] * w[4 + k].s;
+                        y1[2 * k + 1] = x1[2 * k + 1] * w[4 + k].c + x1[2 * k] * w[4 + k].s;
+                    }
                 }
-            } else {
+                r0[i] = pack8(y0);
+                r1[i] = pack8(y1);
+            }
+            const int i0 = at0(u), i1 = at1(u);
+            if (u < a.hq || !a.append) {
+                uint16_t* dst = u < a.hq ? a.q_out + (size_t)t * a.ldq_out + (size_t)u * a.D
+                                         : a.k_out + (size_t)t * a.ldk_out + (size_t)(u - a.hq) * a.D;
+                if (in) {
+                    *reinterpret_cast<uint4*>(dst + i0) = r0[i];
+                    *reinterpret_cast<uint4*>(dst + i1) = r1[i];
+                }
+            } else if (placed) {
+                const bool key = u < a.hq + a.hk;
+                const size_t prow = row + (size_t)(u - a.hq - (key ? 0 : a.hk)) * a.page_size;
+                uint8_t* pool = key ? a.pool.k : a.pool.v;
+                if (!a.e4m3) {
+                    uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + prow * a.D;
+                    if (in) {
+                        *reinterpret_cast<uint4*>(dst + i0) = r0[i];
+                        *reinterpret_cast<uint4*>(dst + i1) = r1[i];
+                    }
+                } else {
+                    // the bf16 row quantized: its largest magnitude over the head's lanes, then the codes
+                    uint32_t top = __vmaxu2(amax8(r0[i]), amax8(r1[i]));
+                    top = max(top & 0xFFFFu, top >> 16);
+                    const uint32_t group = ((1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    y0[2 * i] = x0[2 * i] * w[i].c - x0[2 * i + 1] * w[i].s;
-                    y0[2 * i + 1] = x0[2 * i + 1] * w[i].c + x0[2 * i] * w[i].s;
-                    y1[2 * i] = x1[2 * i] * w[4 + i].c - x1[2 * i + 1] * w[4 + i].s;
-                    y1[2 * i + 1] = x1[2 * i + 1] * w[4 + i].c + x1[2 * i] * w[4 + i].s;
+                    for (int o = GL / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+                    const int s = ue8m0_for_amax_bits(__uint_as_float(top << 16));
+                    uint2 q0 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), q1 = q0;
+                    if (s != 255) {
+                        const float down = __uint_as_float((uint32_t)(254 - s) << 23);       // 2^(127 - s)
+                        q0 = quant8(r0[i], down);
+                        q1 = quant8(r1[i], down);
+                    }
+                    if (in) {
+                        *reinterpret_cast<uint2*>(pool + prow * a.D + i0) = q0;
+                        *reinterpret_cast<uint2*>(pool + prow * a.D + i1) = q1;
+                    }
+                    if (e == 0) (key ? a.pool.ks : a.pool.vs)[prow] = (uint8_t)s;
                 }
             }
-            r0 = pack8(y0);
-            r1 = pack8(y1);
+            load(i, u + kAhead * split);        // the next round's
         }
-        if (kind == 0 || !a.append) {
-            uint16_t* dst = kind == 0 ? a.q_out + (size_t)t * a.ldq_out : a.k_out + (size_t)t * a.ldk_out;
-            dst += (size_t)h * a.D;
-            if (in) {
-                *reinterpret_cast<uint4*>(dst + i0) = r0;
-                *reinterpret_cast<uint4*>(dst + i1) = r1;
-            }
-            continue;
-        }
-        if (slot < 0) continue;
-        const size_t prow = ((size_t)page * a.hk + h) * a.page_size + off;
-        uint8_t* pool = kind == 1 ? a.pool.k : a.pool.v;
-        if (!a.e4m3) {
-            uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + prow * a.D;
-            if (in) {
-                *reinterpret_cast<uint4*>(dst + i0) = r0;
-                *reinterpret_cast<uint4*>(dst + i1) = r1;
-            }
-            continue;
-        }
-        // the bf16 row quantized: amax over the head's lanes, then 16 codes
-        unpack8(r0, x0);
-        unpack8(r1, x1);
-        float amax = 0.0f;
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            amax = fmaxf(amax, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
-            nan |= x0[i] != x0[i] || x1[i] != x1[i];
-        }
-        if (nan) amax = __int_as_float(0x7F800000);          // a non-finite maximum, like an infinite one
-        const uint32_t gmask = GL == 32 ? 0xFFFFFFFFu : ((1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
-#pragma unroll
-        for (int o = GL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
-        const int s = ue8m0_for_amax_bits(amax);
-        uint2 q0 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), q1 = q0;
-        if (s != 255) {
-            const float down = __uint_as_float((uint32_t)(254 - s) << 23);       // 2^(127 - s)
-            q0 = quant8(x0, down);
-            q1 = quant8(x1, down);
-        }
-        if (in) {
-            *reinterpret_cast<uint2*>(pool + prow * a.D + i0) = q0;
-            *reinterpret_cast<uint2*>(pool + prow * a.D + i1) = q1;
-        }
-        if (e == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[prow] = (uint8_t)s;
     }
 }
 
@@ -201,10 +221,17 @@ template <int GL>
 cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
 {
     const int units = a.hq + a.hk + a.hv;
-    const int split = units;
-    const long long threads = (long long)a.T * split * GL;
+    const long long lanes = (long long)a.T * GL;
+    // How many lanes share a token's heads.  Few tokens: enough for 512 lanes an
+    // SM, up to one head each (measured, 48 heads of 128: 8 tokens 2.2 us with 48
+    // sharers and 4.4 with 6; 900 tokens 5.7 us with 12, 9.6 with 48).  Many tokens:
+    // eight heads each, two rounds of loads on one set of angles (16383 tokens:
+    // 64 us with 6 sharers, 70 with 12, 79 with 1).
+    const long long fit = (long long)a.sms * 512 / lanes;
+    const int least = (units + 7) / 8;
+    const int split = (int)(fit < least ? least : fit > units ? units : fit);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
+    cfg.gridDim = dim3((unsigned)((lanes + 255) / 256), (unsigned)split);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -212,7 +239,7 @@ cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_rope<GL>, a, split);
+    return cudaLaunchKernelEx(&cfg, k_rope<GL>, a);
 }
 
 }  // namespace

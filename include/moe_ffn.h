@@ -584,6 +584,13 @@ int moe_attn_decode(moe_kv_t h, const moe_kv_pool* pool, const void* q, const in
  * pair is left out. */
 int moe_kv_copy_pages(moe_kv_t h, const moe_kv_pool* pools, int num_pools, const int32_t* pairs, int n, void* stream);
 
+/* The four calls above with their arguments as one array of 64-bit words, in
+ * their order (pointers and integers as they are, floating arguments as
+ * doubles): the same call, for language bindings that pay for every argument.
+ * INVALID_ARG: an unknown op, no array, an integer outside its type. */
+enum { MOE_KV_CALL_ROPE = 0, MOE_KV_CALL_APPEND = 1, MOE_KV_CALL_ATTN_DECODE = 2, MOE_KV_CALL_COPY_PAGES = 3 };
+int moe_kv_call(int op, const int64_t* words);
+
 /* The pages' bookkeeping (host code; needs no GPU and no other handle): which
  * page holds which tokens of which sequence, with pages shared by forked
  * sequences counted.  Deterministic: a new page is the lowest free one.

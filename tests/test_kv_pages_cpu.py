@@ -171,3 +171,18 @@ def test_cache_configs_and_null_handles_are_refused():
     assert L.moe_kv_copy_pages(None, None, 0, None, 0, None) == e
     assert L.moe_kv_status(None, None) == e
     L.moe_kv_destroy(None)
+
+
+def test_word_call_refusals():
+    """moe_kv_call takes the calls' arguments as 64-bit words and refuses what they would."""
+    L, e = moe.lib(), moe.MOE_ERR_INVALID_ARG
+    for op in (-1, 4):
+        assert L.moe_kv_call(op, bytes(8 * 16)) == e
+    for op in range(4):
+        assert L.moe_kv_call(op, None) == e
+        assert L.moe_kv_call(op, bytes(8 * 16)) == e                 # no handle
+    pool, rope = moe.kv_pool(0, 0), moe.rope(0, 16, 0)
+    for f in (lambda: moe.moe_rope(None, rope, None, 1), lambda: moe.moe_kv_append(None, pool, None, None, None, None, 1),
+              lambda: moe.moe_attn_decode(None, pool, None, None, None, 1, None),
+              lambda: moe.moe_kv_copy_pages(None, [pool], None, 1), lambda: moe.moe_kv_copy_pages(None, [], None, 0)):
+        assert _code(f) == e
