@@ -45,8 +45,11 @@ __host__ __device__ constexpr int stage_bytes(int DP, bool F8)
 __host__ __device__ constexpr int num_stages(int DP, bool F8) { return stage_bytes(DP, F8) < 6000 ? 5 : 3; }
 
 // A part of a row: NROW output rows (not divided by the sums), the powers of
-// two that they are multiples of, the sums of weights, and (E4M3) theirs.
-__host__ __device__ constexpr int part_floats(int DP, bool F8, int NROW) { return NROW * DP + (F8 ? 3 : 2) * NROW; }
+// two that they are multiples of, the sums of weights, and (E4M3) theirs.  The
+// rows are spaced so that a warp's stores of an MMA result (8 rows, 2 or 4
+// columns a lane) meet no bank twice.
+__host__ __device__ constexpr int part_row(int DP, bool F8) { return DP + (F8 ? 16 : 8); }
+__host__ __device__ constexpr int part_floats(int DP, bool F8, int NROW) { return NROW * part_row(DP, F8) + (F8 ? 3 : 2) * NROW; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
 {
@@ -175,6 +178,7 @@ __device__ __forceinline__ uint32_t at_chunk(uint32_t base, int r, int c)
 struct SplitArgs {
     AttnArgs a;
     int G, chunks, R;           // query heads per key head, groups of NROW of them, rows per sequence
+    int ps_shift;               // log2 of the page size, -1 if it is no power of two
     float* frags;               // [grid][kWarps] parts
     float* parts;               // [grid][2] parts
     int* tickets;               // [max_seqs * R], zero between launches
@@ -184,10 +188,11 @@ template <int DP, bool F8, int NROW>
 struct Kernel {
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
-    static constexpr int PART = part_floats(DP, F8, NROW);
+    static constexpr int PART = part_floats(DP, F8, NROW), PROW = part_row(DP, F8), PHEAD = NROW * PROW;
     static constexpr int SCALES = F8 ? 8 * TT : 0;           // a tile's scales as numbers
     static constexpr int REGION = STAGES * STAGE + SCALES;   // a warp's ring, and at the end its parts
-    static_assert(REGION % 16 == 0 && PART % 4 == 0 && 4 * 2 * PART <= REGION, "a warp's parts fit its ring");
+    static_assert(REGION % 16 == 0 && PART % 4 == 0 && 4 * (2 * PART + 4 * 2 * kWarps * NROW) <= REGION,
+                  "a warp's parts, and the merge's tables, fit its ring");
     static constexpr int QR = NROW == 8 ? 2 : 4;
 
     // ---- a row's state in one warp: lane 4 g + j holds row g (and g + 8 for
@@ -500,14 +505,21 @@ struct Kernel {
         const int g = lane >> 2, j = lane & 3;
 #pragma unroll
         for (int half = 0; half < NROW / 8; half++) {
+            float* r = p + (g + 8 * half) * PROW;
+            if (F8) {           // four columns in a row from an even and an odd MMA column block
 #pragma unroll
-            for (int i = 0; i < ND; i++)
+                for (int i = 0; i < ND; i += 2)
+                    *reinterpret_cast<float4*>(r + column(i, 0, j)) =
+                        make_float4(o[i][2 * half], o[i + 1][2 * half], o[i][2 * half + 1], o[i + 1][2 * half + 1]);
+            } else {
 #pragma unroll
-                for (int k = 0; k < 2; k++) p[(g + 8 * half) * DP + column(i, k, j)] = o[i][2 * half + k];
+                for (int i = 0; i < ND; i++)
+                    *reinterpret_cast<float2*>(r + column(i, 0, j)) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+            }
             if (j == 0) {
-                p[NROW * DP + g + 8 * half] = F8 ? mo[half] : m[half];
-                p[NROW * DP + NROW + g + 8 * half] = l[half];
-                if (F8) p[NROW * DP + 2 * NROW + g + 8 * half] = m[half];
+                p[PHEAD + g + 8 * half] = F8 ? mo[half] : m[half];
+                p[PHEAD + NROW + g + 8 * half] = l[half];
+                if (F8) p[PHEAD + 2 * NROW + g + 8 * half] = m[half];
             }
         }
     }
@@ -561,6 +573,7 @@ struct Kernel {
 
     static constexpr int VEC = DP / 32;         // columns a lane in a merge
 
+    // far: another CTA's
     __device__ __forceinline__ static void load_vec(float (&v)[VEC], const float* p, bool far)
     {
         if (VEC == 4) {
@@ -576,33 +589,96 @@ struct Kernel {
         }
     }
 
-    // A row's parts merged by one warp: lane i holds part i's numbers (mine: it
-    // has one), every lane VEC columns of all.  N parts' loads are in flight at a
-    // time; at(i) is part i, i < n.  Far: written by other CTAs.
-    template <int N, bool Far, class At>
-    struct Merge {
-        float acc[VEC], top, topo, sum;
-
-        __device__ __forceinline__ void reset()
-        {
-#pragma unroll
-            for (int k = 0; k < VEC; k++) acc[k] = 0.0f;
-            top = topo = -INFINITY;
-            sum = 0.0f;
+    // A merged row's VEC columns a lane, to its part `to` or as the row's output.
+    __device__ __forceinline__ static void finish(const SplitArgs& s, int b, int row, int g, int lane, const float (&acc)[VEC],
+                                                  float topo, float sum, float top, float* to)
+    {
+        const int d = lane * VEC;
+        if (to) {
+            if (VEC == 4) *reinterpret_cast<float4*>(to + g * PROW + d) = make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]);
+            else *reinterpret_cast<float2*>(to + g * PROW + d) = make_float2(acc[0], acc[1]);
+            if (lane == 0) {
+                to[PHEAD + g] = topo;
+                to[PHEAD + NROW + g] = sum;
+                if (F8) to[PHEAD + 2 * NROW + g] = top;
+            }
+            return;
         }
+        const int h = s.chunks == 1 ? row : row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
+        if (hg >= s.G) return;
+        const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
+        const float inv = quotient(sum, top, topo);
+        if (d < s.a.D) {
+            if (VEC == 4) put4(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv, acc[VEC - 2] * inv, acc[VEC - 1] * inv);
+            else put2(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv);
+        }
+        if (lane == 0) put_lse(s.a, out, top, sum);
+    }
 
-        // up to 32 more parts, of which `members` are there
-        __device__ __forceinline__ void add(unsigned members, At at, int g, int lane)
-        {
+    // A row's parts in this CTA, `mem`, at most one a warp (bit 2 w or 2 w + 1,
+    // at near(w, 1 or 2)): their weights to tab[bit][NROW], the row's references
+    // and sum to tab[16 ..][f][NROW].
+    template <class Near>
+    __device__ __forceinline__ static void weigh(unsigned mem, Near near, int f, int g, float* tab)
+    {
+        float mo[kWarps], l[kWarps], m[kWarps];
+        float top = -INFINITY, topo = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            // a place is read whether it holds a part or not, so that no load waits for a branch
+            const unsigned is = (mem >> (2 * w)) & 3u;
+            const float* e = near(w, is) + PHEAD + g;
+            const float a = e[0], b = e[NROW], c = F8 ? e[2 * NROW] : a;
+            mo[w] = is ? a : -INFINITY;
+            l[w] = is ? b : 0.0f;
+            m[w] = is ? c : -INFINITY;
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            topo = fmaxf(topo, mo[w]);
+            top = fmaxf(top, m[w]);
+        }
+        // -inf before the first key: nothing to bring to the new references
+        const float ro = topo == -INFINITY ? 0.0f : topo, rt = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const unsigned is = (mem >> (2 * w)) & 3u;
+            const float by = ex2(mo[w] - ro);
+            if (is) tab[(2 * w + (is >> 1)) * NROW + g] = by;
+            sum += ex2(m[w] - rt) * l[w];
+        }
+        float* t = tab + (2 * kWarps + f) * NROW + g;
+        t[0] = topo;
+        t[2 * kWarps * NROW] = sum;
+        t[4 * kWarps * NROW] = top;
+    }
+
+    // A row's parts of several CTAs merged by one warp: lane i holds part i's
+    // numbers, every lane VEC columns of all, and 16 parts' loads are in flight at a
+    // time.  at(i) is part i, i < n.
+    template <class At>
+    __device__ __forceinline__ static void join(const SplitArgs& s, int n, At at, int b, int row, int g, int lane)
+    {
+        constexpr int N = 16;
+        float acc[VEC], top = -INFINITY, topo = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VEC; k++) acc[k] = 0.0f;
+        for (int i0 = 0; i0 < n; i0 += 32) {
             float mo = -INFINITY, m = -INFINITY, l = 0.0f;
-            if ((members >> lane) & 1) {
-                const float* e = at(lane) + NROW * DP + g;
-                mo = Far ? __ldcg(e) : e[0];
-                l = Far ? __ldcg(e + NROW) : e[NROW];
-                m = !F8 ? mo : Far ? __ldcg(e + 2 * NROW) : e[2 * NROW];
+            if (i0 + lane < n) {
+                const float* e = at(i0 + lane) + PHEAD + g;
+                mo = __ldcg(e);
+                l = __ldcg(e + NROW);
+                m = F8 ? __ldcg(e + 2 * NROW) : mo;
+            }
+            float v[N][VEC];
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+#pragma unroll
+                for (int k = 0; k < VEC; k++) v[i][k] = 0.0f;
+                if (i0 + i < n) load_vec(v[i], at(i0 + i) + g * PROW + lane * VEC, true);
             }
             const float to_ = fmaxf(topo, warp_max(mo)), t = F8 ? fmaxf(top, warp_max(m)) : to_;
-            // -inf before the first key: nothing to bring to the new references
             const float rt = t == -INFINITY ? 0.0f : t, ro = to_ == -INFINITY ? 0.0f : to_;
             const float down = ex2(topo - ro), w = ex2(mo - ro);
             sum = sum * (F8 ? ex2(top - rt) : down) + warp_sum((F8 ? ex2(m - rt) : w) * l);
@@ -610,57 +686,27 @@ struct Kernel {
             topo = to_;
 #pragma unroll
             for (int k = 0; k < VEC; k++) acc[k] *= down;
-            while (members) {
-                float v[N][VEC], f[N];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
 #pragma unroll
                 for (int i = 0; i < N; i++) {
-                    const int x = members ? __ffs(members) - 1 : -1;
-                    members &= members - 1;
-                    f[i] = __shfl_sync(0xFFFFFFFFu, w, x & 31);
-                    if (x < 0) f[i] = 0.0f;
+                    const float f = __shfl_sync(0xFFFFFFFFu, w, N * h + i);
+                    if (i0 + N * h + i < n) {
 #pragma unroll
-                    for (int k = 0; k < VEC; k++) v[i][k] = 0.0f;
-                    if (x >= 0) load_vec(v[i], at(x) + g * DP + lane * VEC, Far);
+                        for (int k = 0; k < VEC; k++) acc[k] = fmaf(f, v[i][k], acc[k]);
+                    }
+                    if (h == 0 && i0 + N + i < n) load_vec(v[i], at(i0 + N + i) + g * PROW + lane * VEC, true);
                 }
-#pragma unroll
-                for (int i = 0; i < N; i++)
-#pragma unroll
-                    for (int k = 0; k < VEC; k++) acc[k] = fmaf(f[i], v[i][k], acc[k]);
             }
         }
-
-        // to the row's part `to`, or as the row's output
-        __device__ __forceinline__ void finish(const SplitArgs& s, int b, int row, int g, int lane, float* to) const
-        {
-            const int d = lane * VEC;
-            if (to) {
-                if (VEC == 4) *reinterpret_cast<float4*>(to + g * DP + d) = make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]);
-                else *reinterpret_cast<float2*>(to + g * DP + d) = make_float2(acc[0], acc[1]);
-                if (lane == 0) {
-                    to[NROW * DP + g] = topo;
-                    to[NROW * DP + NROW + g] = sum;
-                    if (F8) to[NROW * DP + 2 * NROW + g] = top;
-                }
-                return;
-            }
-            const int h = s.chunks == 1 ? row : row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
-            if (hg >= s.G) return;
-            const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
-            const float inv = quotient(sum, top, topo);
-            if (d < s.a.D) {
-                if (VEC == 4) put4(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv, acc[VEC - 2] * inv, acc[VEC - 1] * inv);
-                else put2(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv);
-            }
-            if (lane == 0) put_lse(s.a, out, top, sum);
-        }
-    };
+        finish(s, b, row, g, lane, acc, topo, sum, top, nullptr);
+    }
 };
 
 // A part that a warp leaves behind: 2 w + 0 from its first row, 2 w + 1 from its last.
 struct Frag {
     int b, row;                 // b < 0: none
     int from_start, to_end;     // the part holds the row's first tile, its last tile
-    int far;                    // it lies in global memory (s.frags)
 };
 
 // A place on the line of tiles.
@@ -686,38 +732,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
 
     // tiles before each sequence (of one row), by a scan over the lengths
     uint32_t base = 0;
-    for (int i0 = 0; i0 < B; i0 += kThreads) {
-        const int i = i0 + tid;
-        uint32_t v = 0;
-        if (i < B) {
-            int n = s.a.lens[i];
-            if ((n < 0 || n > cap) && blockIdx.x == 0) atomicOr(s.a.status, kStatusBadIndex);
-            n = min(max(n, 0), cap);
-            slen[i] = n;
-            const int first = s.a.window > 0 ? max(0, n - s.a.window) : 0;
-            v = (uint32_t)max(1, (n + TT - 1) / TT - first / TT);
-        }
-        uint32_t x = v;
+    auto tiles_of = [&](int i) {
+        if (i >= B) return 0u;
+        int n = s.a.lens[i];
+        if ((n < 0 || n > cap) && blockIdx.x == 0) atomicOr(s.a.status, kStatusBadIndex);
+        n = min(max(n, 0), cap);
+        slen[i] = n;
+        const int first = s.a.window > 0 ? max(0, n - s.a.window) : 0;
+        return (uint32_t)max(1, (n + TT - 1) / TT - first / TT);
+    };
+    auto scan = [&](uint32_t x) {
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
             if (lane >= d) x += y;
         }
-        if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
-        uint32_t before = base, all = base;
+        return x;
+    };
+    if (B <= 32) {              // every warp by itself, all writing the same
+        const uint32_t x = scan(tiles_of(lane));
+        if (lane < B) pre[lane + 1] = x;
+        if (lane == 0) pre[0] = 0;
+        base = __shfl_sync(0xFFFFFFFFu, x, 31);
+        __syncwarp();
+    } else {
+        for (int i0 = 0; i0 < B; i0 += kThreads) {
+            const uint32_t x = scan(tiles_of(i0 + tid));
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            uint32_t before = base, all = base;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            if (w < warp) before += s_warp[w];
-            all += s_warp[w];
+            for (int w = 0; w < kWarps; w++) {
+                if (w < warp) before += s_warp[w];
+                all += s_warp[w];
+            }
+            if (i0 + tid < B) pre[i0 + tid + 1] = before + x;
+            base = all;
+            __syncthreads();
         }
-        if (i < B) pre[i + 1] = before + x;
-        base = all;
+        if (tid == 0) pre[0] = 0;
         __syncthreads();
     }
-    if (tid == 0) pre[0] = 0;
-    if (tid < 2 * kWarps) s_frag[tid].b = -1;
-    __syncthreads();
     // the CTAs' stretches, equal to one tile, and the warps' within them; fewer
     // CTAs where they would not have a tile for every warp
     const uint32_t W = base * (uint32_t)s.R;
@@ -754,15 +809,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     };
     auto first_key = [&](int b) { return s.a.window > 0 ? max(0, slen[b] - s.a.window) : 0; };
 
+    if (lane < 2) s_frag[2 * warp + lane].b = -1;
+    __syncwarp();
     K k;
     if (u < end) {
         uint8_t* my = ring + warp * K::REGION;
         const uint32_t my32 = smem_u32(my);
-        // the producer's side: a window of 32 tiles' places in the pool, one a lane
-        // (in blocks of 16 rows of one head: a page is a whole number of them)
+        // The producer's side: a window of 32 tiles' places in the pool, one a lane
+        // (in blocks of 16 rows of one head: a page is a whole number of them), and
+        // the page ids of the window that comes next, on their way.
         const int hblk = ps / 16;
-        int wb = -1, wt = 0;
+        int wb = -1, wt = 0, nb = -1, nt = 0;
         uint32_t blk[TT / 16];
+        int ids[TT / 16];
+        auto page_of = [&](int key) { return s.ps_shift >= 0 ? key >> s.ps_shift : key / ps; };
+        auto fetch = [&](int b, int t) {
+            nb = b;
+            nt = t;
+#pragma unroll
+            for (int i = 0; i < TT / 16; i++) {
+                const int key = (t + lane) * TT + 16 * i;
+                ids[i] = key < slen[b] ? s.a.table[(size_t)b * s.a.row + page_of(key)] : 0;
+            }
+        };
+        auto install = [&]() {
+            wb = nb;
+            wt = nt;
+            const int n = slen[wb], first = first_key(wb);
+#pragma unroll
+            for (int i = 0; i < TT / 16; i++) {
+                const int key = (wt + lane) * TT + 16 * i;
+                const bool ok = ids[i] >= 0 && ids[i] < s.a.num_pages;
+                blk[i] = key < n && ok ? (uint32_t)ids[i] * (uint32_t)(s.a.hkv * hblk) + (uint32_t)((key - page_of(key) * ps) / 16)
+                                       : 0xFFFFFFFFu;
+                if (key < n && !ok && key + 16 > first) atomicOr(s.a.status, kStatusBadIndex);
+            }
+        };
         uint32_t badq = 0;                      // 2 bits a stage
         Place pp = place_of(u), cp = pp;
         uint32_t up = u;
@@ -777,22 +859,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         auto issue = [&](int stage) {
             const int n = slen[pp.b], first = first_key(pp.b), t0 = first / TT, tile = t0 + pp.t;
             if (pp.b != wb || tile < wt || tile >= wt + 32) {
-                wb = pp.b;
-                wt = tile;
-#pragma unroll
-                for (int i = 0; i < TT / 16; i++) {
-                    const int key = (tile + lane) * TT + 16 * i;
-                    uint32_t at = 0xFFFFFFFFu;
-                    if (key < n) {
-                        const int pi = key / ps;
-                        const int page = s.a.table[(size_t)pp.b * s.a.row + pi];
-                        if (page >= 0 && page < s.a.num_pages)
-                            at = (uint32_t)page * (uint32_t)(s.a.hkv * hblk) + (uint32_t)((key - pi * ps) / 16);
-                        else if (key + 16 > first)
-                            atomicOr(s.a.status, kStatusBadIndex);
-                    }
-                    blk[i] = at;
+                if (nb != pp.b || nt != tile) fetch(pp.b, tile);
+                install();
+                // what comes next: the rest of the row, else the next row's (or, where
+                // this window holds a whole row, the next sequence's) beginning
+                if (pp.t + 32 < pp.tiles) {
+                    fetch(pp.b, tile + 32);
+                } else if (pp.row + 1 < s.R && (pp.t > 0 || pp.tiles > 32)) {
+                    fetch(pp.b, t0);
+                } else if (pp.b + 1 < B) {
+                    fetch(pp.b + 1, first_key(pp.b + 1) / TT);
                 }
+            }
+            if (pp.t == 0 && up != u) {         // a row begins: its queries, for when the warp gets there
+                const int h = s.chunks == 1 ? pp.row : pp.row / s.chunks, g0 = (pp.row - h * s.chunks) * NROW;
+                const int bytes = min(NROW, s.G - g0) * s.a.D * 2;
+                if (lane * 128 < bytes)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                        reinterpret_cast<const uint8_t*>(s.a.q + ((size_t)pp.b * s.a.hq + h * s.G + g0) * s.a.D) + lane * 128));
             }
             const uint32_t st = my32 + stage * K::STAGE;
             const int h = s.chunks == 1 ? pp.row : pp.row / s.chunks;
@@ -868,21 +952,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             if (row_done && start == 0) {
                 k.store_out(s, cp.b, cp.row, lane);
             } else {
-                // a part: the last one of the stretch stays in the warp's ring, which
-                // is drained then; one that ends a row before goes to global memory
+                // A part: the last one of the stretch goes to the warp's ring, which is
+                // drained then; one that ends a row before waits in global memory.
                 const bool far = u != end;
                 k.store_part(far ? s.frags + ((size_t)blockIdx.x * kWarps + warp) * K::PART
                                  : reinterpret_cast<float*>(my) + (first_seg ? 0 : K::PART), lane);
                 if (lane == 0) {
                     Frag& f = s_frag[2 * warp + (first_seg ? 0 : 1)];
-                    f.far = far;
                     f.b = cp.b;
                     f.row = cp.row;
                     f.from_start = start == 0;
                     f.to_end = row_done;
                 }
             }
-            if (u == end) break;
+            if (u == end) {
+                if (!first_seg && s_frag[2 * warp].b >= 0) {
+                    // the first row's part comes to the ring, too
+                    const float* from = s.frags + ((size_t)blockIdx.x * kWarps + warp) * K::PART;
+                    for (int i = lane; i < K::PART / 4; i += 32) cp_async16(my32 + 16 * i, from + 4 * i, 16);
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                }
+                break;
+            }
             advance(cp);
             start = 0;
             first_seg = 0;
@@ -898,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     // parts' heads at once, a lane each, and finds the rows' first parts by votes.
     Frag fr;
     fr.b = -1;
-    fr.row = fr.from_start = fr.to_end = fr.far = 0;
+    fr.row = fr.from_start = fr.to_end = 0;
     if (lane < 2 * kWarps) fr = s_frag[lane];
     const unsigned there = __ballot_sync(0xFFFFFFFFu, fr.b >= 0);
     const unsigned before = there & ((1u << lane) - 1u);
@@ -906,38 +998,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     const int pb = __shfl_sync(0xFFFFFFFFu, fr.b, prev), pr = __shfl_sync(0xFFFFFFFFu, fr.row, prev);
     const unsigned heads = __ballot_sync(0xFFFFFFFFu, fr.b >= 0 && (!before || pb != fr.b || pr != fr.row));
     const unsigned starts = __ballot_sync(0xFFFFFFFFu, fr.from_start), ends = __ballot_sync(0xFFFFFFFFu, fr.to_end);
-    const unsigned far = __ballot_sync(0xFFFFFFFFu, fr.b >= 0 && fr.far);
-    // those in global memory come to their warps' rings first, all in one trip
-    if (far) {
-#pragma unroll 1
-        for (unsigned rest = far; rest; rest &= rest - 1) {
-            const int w = (__ffs(rest) - 1) >> 1;
-            const float* from = s.frags + ((size_t)blockIdx.x * kWarps + w) * K::PART;
-            const uint32_t to = smem_u32(ring + w * K::REGION);
-            for (int i = tid; i < K::PART / 4; i += kThreads) cp_async16(to + 16 * i, from + 4 * i, 16);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        __syncthreads();
-    }
-    // a warp a head, the rows side by side
     const int heads_in = min(NROW, s.G);
     auto last_of = [&](int f) {                 // the last part of the row whose first is f
         const unsigned after = heads & ~((2u << f) - 1u);
         return 31 - __clz(there & (after ? (after & -after) - 1u : 0xFFFFFFFFu));
     };
-    auto near = [&](int x) { return reinterpret_cast<const float*>(ring + (x >> 1) * K::REGION) + (x & 1) * K::PART; };
-    for (int e = warp; e < __popc(heads) * heads_in; e += kWarps) {
-        unsigned rest = heads;
-        for (int i = e / heads_in; i > 0; i--) rest &= rest - 1;
-        const int f = __ffs(rest) - 1, last = last_of(f), g = e % heads_in;
-        const int slot = (starts >> f) & 1;
-        const bool whole = slot && ((ends >> last) & 1);
-        typename K::template Merge<4, false, decltype(near)> m;
-        m.reset();
-        m.add(there & ((2u << last) - 1u) & ~((1u << f) - 1u), near, g, lane);
-        m.finish(s, s_frag[f].b, s_frag[f].row, g, lane, whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
-    }
+    auto members = [&](int f) { return there & ((2u << last_of(f)) - 1u) & ~((1u << f) - 1u); };
+    auto near = [&](int w, unsigned is) {
+        return reinterpret_cast<const float*>(ring + w * K::REGION) + (is == 1 ? 0 : K::PART);
+    };
+    float* tab = reinterpret_cast<float*>(ring) + 2 * K::PART;
     // rows that began before this CTA, that go on after it: their first parts here
     int open[2] = {-1, -1};
     if (heads) {
@@ -945,19 +1015,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         if (!((starts >> f) & 1)) open[0] = f;
         if (((starts >> l) & 1) && !((ends >> last_of(l)) & 1)) open[1] = l;
     }
-    if (open[0] < 0 && open[1] < 0) return;
-
-    // Rows that other CTAs hold parts of, too: the last CTA to finish joins them.
-    if (tid < 2) {
-        s_first[tid] = -1;
-        const int f = open[tid];
+    // first the weights, a thread a head of a row (and the last two threads find
+    // the CTAs that hold the open rows); then the sums, a warp a head
+    for (int i = tid; i < 2 * kWarps * heads_in; i += kThreads)
+        if ((heads >> (i % (2 * kWarps))) & 1) K::weigh(members(i % (2 * kWarps)), near, i % (2 * kWarps), i / (2 * kWarps), tab);
+    if (tid >= kThreads - 2) {
+        const int slot = tid - (kThreads - 2), f = open[slot];
+        s_first[slot] = -1;
         if (f >= 0) {
             const uint32_t tiles = pre[s_frag[f].b + 1] - pre[s_frag[f].b];
             const uint32_t r0 = pre[s_frag[f].b] * (uint32_t)s.R + (uint32_t)s_frag[f].row * tiles;
-            s_c0[tid] = (int)cta_of(r0);
-            s_count[tid] = (int)cta_of(r0 + tiles - 1) - s_c0[tid] + 1;
+            s_c0[slot] = (int)cta_of(r0);
+            s_count[slot] = (int)cta_of(r0 + tiles - 1) - s_c0[slot] + 1;
         }
     }
+    __syncthreads();
+    for (int e = warp; e < __popc(heads) * heads_in; e += kWarps) {
+        unsigned rest = heads;
+        for (int i = e / heads_in; i > 0; i--) rest &= rest - 1;
+        const int f = __ffs(rest) - 1, last = last_of(f), g = e % heads_in;
+        const int slot = (starts >> f) & 1;
+        const bool whole = slot && ((ends >> last) & 1);
+        const unsigned mem = members(f);
+        float acc[K::VEC];
+#pragma unroll
+        for (int k = 0; k < K::VEC; k++) acc[k] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const unsigned is = (mem >> (2 * w)) & 3u;
+            const float by = tab[(2 * w + (is >> 1)) * NROW + g];
+            float v[K::VEC];
+            K::load_vec(v, near(w, is) + g * K::PROW + lane * K::VEC, false);
+#pragma unroll
+            for (int k = 0; k < K::VEC; k++) acc[k] = is ? fmaf(by, v[k], acc[k]) : acc[k];
+        }
+        const float* t = tab + (2 * kWarps + f) * NROW + g;
+        K::finish(s, s_frag[f].b, s_frag[f].row, g, lane, acc, t[0], t[2 * kWarps * NROW], t[4 * kWarps * NROW],
+                  whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
+    }
+    if (open[0] < 0 && open[1] < 0) return;
+
+    // Rows that other CTAs hold parts of, too: the last CTA to finish joins them.
     __syncthreads();
     if (tid < 2 && open[tid] >= 0) {
         // the CTA's part was written before the barrier; its release and the
@@ -974,13 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     for (int e = warp; e < 2 * heads_in; e += kWarps) {
         const int slot = e >= heads_in, g = slot ? e - heads_in : e, c0 = s_first[slot], n = s_count[slot];
         if (c0 < 0) continue;
-        int i0 = 0;
         // c0 holds the row's beginning, in its slot 1; the others' parts are in slot 0
-        auto far_part = [&](int x) { return s.parts + ((size_t)(c0 + i0 + x) * 2 + (i0 + x == 0 ? 1 : 0)) * K::PART; };
-        typename K::template Merge<16, true, decltype(far_part)> m;
-        m.reset();
-        for (; i0 < n; i0 += 32) m.add(n - i0 >= 32 ? 0xFFFFFFFFu : (1u << (n - i0)) - 1u, far_part, g, lane);
-        m.finish(s, s_frag[open[slot]].b, s_frag[open[slot]].row, g, lane, nullptr);
+        K::join(s, n, [&](int x) { return s.parts + ((size_t)(c0 + x) * 2 + (x == 0 ? 1 : 0)) * K::PART; }, s_frag[open[slot]].b,
+                s_frag[open[slot]].row, g, lane);
     }
 }
 
@@ -1052,6 +1146,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
     s.G = a.hq / a.hkv;
     s.chunks = s.G <= 8 ? 1 : (s.G + 15) / 16;
     s.R = a.hkv * s.chunks;
+    s.ps_shift = a.page_size & (a.page_size - 1) ? -1 : __builtin_ctz((unsigned)a.page_size);
     const AttnWorkspace w = attn_workspace(a.max_seqs, a.hq, a.hkv, a.D, a.sms);
     s.tickets = reinterpret_cast<int*>(a.ws + w.tickets);
     s.frags = reinterpret_cast<float*>(a.ws + w.frags);
