@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         if (((starts >> l) & 1) && !((ends >> last_of(l)) & 1)) open[1] = l;
     }
     // first the weights, a thread a head of a row (and the last two threads find
-    // the CTAs that hold the open rows); then the sums, a warp a head
+    // the CTAs that hold the open rows); then the sums, a warp two heads
     for (int i = tid; i < 2 * kWarps * heads_in; i += kThreads)
         if ((heads >> (i % (2 * kWarps))) & 1) K::weigh(members(i % (2 * kWarps)), near, i % (2 * kWarps), i / (2 * kWarps), tab);
     if (tid >= kThreads - 2) {
@@ -1030,28 +1030,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         }
     }
     __syncthreads();
-    for (int e = warp; e < __popc(heads) * heads_in; e += kWarps) {
+    const int pairs = (heads_in + 1) / 2;
+    for (int e = warp; e < __popc(heads) * pairs; e += kWarps) {
         unsigned rest = heads;
-        for (int i = e / heads_in; i > 0; i--) rest &= rest - 1;
-        const int f = __ffs(rest) - 1, last = last_of(f), g = e % heads_in;
+        for (int i = e / pairs; i > 0; i--) rest &= rest - 1;
+        const int f = __ffs(rest) - 1, last = last_of(f), g = e % pairs * 2;
         const int slot = (starts >> f) & 1;
         const bool whole = slot && ((ends >> last) & 1);
         const unsigned mem = members(f);
-        float acc[K::VEC];
+        float acc[2][K::VEC];
 #pragma unroll
-        for (int k = 0; k < K::VEC; k++) acc[k] = 0.0f;
+        for (int k = 0; k < K::VEC; k++) acc[0][k] = acc[1][k] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; w++) {
             const unsigned is = (mem >> (2 * w)) & 3u;
-            const float by = tab[(2 * w + (is >> 1)) * NROW + g];
-            float v[K::VEC];
-            K::load_vec(v, near(w, is) + g * K::PROW + lane * K::VEC, false);
+            const float2 by = *reinterpret_cast<const float2*>(tab + (2 * w + (is >> 1)) * NROW + g);
+            float v[2][K::VEC];
 #pragma unroll
-            for (int k = 0; k < K::VEC; k++) acc[k] = is ? fmaf(by, v[k], acc[k]) : acc[k];
+            for (int r = 0; r < 2; r++) K::load_vec(v[r], near(w, is) + (g + r) * K::PROW + lane * K::VEC, false);
+#pragma unroll
+            for (int k = 0; k < K::VEC; k++) {
+                acc[0][k] = is ? fmaf(by.x, v[0][k], acc[0][k]) : acc[0][k];
+                acc[1][k] = is ? fmaf(by.y, v[1][k], acc[1][k]) : acc[1][k];
+            }
         }
-        const float* t = tab + (2 * kWarps + f) * NROW + g;
-        K::finish(s, s_frag[f].b, s_frag[f].row, g, lane, acc, t[0], t[2 * kWarps * NROW], t[4 * kWarps * NROW],
-                  whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART);
+        float* to = whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART;
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            const float* t = tab + (2 * kWarps + f) * NROW + g + r;
+            if (g + r < heads_in)
+                K::finish(s, s_frag[f].b, s_frag[f].row, g + r, lane, acc[r], t[0], t[2 * kWarps * NROW], t[4 * kWarps * NROW], to);
+        }
     }
     if (open[0] < 0 && open[1] < 0) return;
 
