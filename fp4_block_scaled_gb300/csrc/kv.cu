@@ -141,7 +141,7 @@ int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device)
     h->device = device;
     void* ws = nullptr;
     if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        attn_init_device() != cudaSuccess) {
+        attn_init_device() != cudaSuccess || rope_init_device() != cudaSuccess || copy_init_device() != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;
     }

@@ -75,6 +75,8 @@ struct CopyArgs {
     int sms;
 };
 
+cudaError_t rope_init_device();
+cudaError_t copy_init_device();
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_copy_pages(const CopyArgs& a, cudaStream_t s);

@@ -107,7 +107,7 @@ int moe_kv_pages_extend(moe_kv_pages_t m, int seq, int tokens, int32_t* copy)
     const bool split = inside && m->refs[(size_t)s.ids.back()] > 1;
     if (need - s.ids.size() + (split ? 1 : 0) > (size_t)m->free_count) return MOE_ERR_OOM;
     try {
-        s.ids.reserve(need);
+        if (s.ids.capacity() < need) s.ids.reserve(need > 2 * s.ids.capacity() ? need : 2 * s.ids.capacity());
     } catch (...) {
         return MOE_ERR_OOM;
     }

@@ -244,6 +244,16 @@ cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
 
 }  // namespace
 
+cudaError_t rope_init_device()
+{
+    cudaFuncAttributes at;                      // loads them, so that a first call may be captured
+    cudaError_t e = cudaFuncGetAttributes(&at, k_rope<1>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<2>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<4>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<8>);
+    return e;
+}
+
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
 {
     if (a.T == 0 || a.hq + a.hk + a.hv == 0) return cudaSuccess;

@@ -61,6 +61,12 @@ def test_heads_and_lengths(hq, hkv, kv):
     _run(LENS, hq, hkv, 128, 16, kv)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_very_many_query_heads(kv):
+    _run([0, 5, 40, 300], 512, 1, 64, 16, kv)
+    _run([33, 1], 512, 512, 32, 16, kv)
+
+
 @pytest.mark.parametrize("kv,D", [("bf16", d) for d in (16, 32, 48, 64, 80, 96, 112, 128)] +
                          [("e4m3", d) for d in (32, 64, 96, 128)])
 @pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])

@@ -20,7 +20,8 @@ def _cuda():
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("pages,n,layers,hkv,page,D", [
-    (2, 1, 1, 1, 16, 32), (40, 17, 3, 2, 16, 64), (9, 4, 70, 1, 32, 96), (300, 150, 2, 5, 48, 128), (6, 2, 2, 8, 1024, 128)])
+    (2, 1, 1, 1, 16, 32), (40, 17, 3, 2, 16, 64), (9, 4, 70, 1, 32, 96), (300, 150, 2, 5, 48, 128), (6, 2, 2, 8, 1024, 128),
+    (5, 2, 1, 3, 496, 96)])
 def test_copies_every_byte_of_every_layer(pages, n, layers, hkv, page, D, kv):
     rng = np.random.default_rng(pages + layers)
     pools = [Pool(pages, hkv, page, D, kv, rng) for _ in range(layers)]
