@@ -36,6 +36,8 @@
 // slower way to memory end later than others (dealing out the last eighth of
 // the line at run time evened that out, but the many parts it left cost the
 // join as much), and 2 to 6 us of merging.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv.h"
 
@@ -132,16 +134,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// p as two bf16 terms: hi = bf16(p), lo = bf16(p - hi), together 16
-// significant bits (bf16 alone would put an error of 2^-9 on every weight)
-__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo)
+// p as bf16 terms: hi = bf16(p), lo = bf16(p - hi), together 16 significant
+// bits (bf16 alone would put an error of 2^-9 on every weight), enough for a
+// bf16 output; the rest, bf16(p - hi - lo), brings 24 for an fp32 one, whose error
+// two terms would leave at 1.3e-6 of the output's norm.
+__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo, uint32_t& rest)
 {
     hi = pack_bf16(p0, p1);
-    lo = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+    const float r0 = p0 - __uint_as_float(hi << 16), r1 = p1 - __uint_as_float(hi & 0xFFFF0000u);
+    lo = pack_bf16(r0, r1);
+    rest = pack_bf16(r0 - __uint_as_float(lo << 16), r1 - __uint_as_float(lo & 0xFFFF0000u));
 }
 
 template <bool F8>
-__device__ __forceinline__ void split(float w0, float w1, uint32_t& hi, uint32_t& lo);
+__device__ __forceinline__ void split(float w0, float w1, uint32_t& hi, uint32_t& lo, uint32_t& rest);
 
 // Four E4M3 codes as two pairs of f16 (exact: 4 significant bits, exponents
 // -9 .. 8), bytes (0, 1) and (2, 3).
@@ -170,13 +176,13 @@ __device__ __forceinline__ void split_pair_f16(float w0, float w1, uint32_t& hi,
 }
 
 template <>
-__device__ __forceinline__ void split<false>(float w0, float w1, uint32_t& hi, uint32_t& lo)
+__device__ __forceinline__ void split<false>(float w0, float w1, uint32_t& hi, uint32_t& lo, uint32_t& rest)
 {
-    split_pair(w0, w1, hi, lo);
+    split_pair(w0, w1, hi, lo, rest);
 }
 
 template <>
-__device__ __forceinline__ void split<true>(float w0, float w1, uint32_t& hi, uint32_t& lo)
+__device__ __forceinline__ void split<true>(float w0, float w1, uint32_t& hi, uint32_t& lo, uint32_t&)
 {
     split_pair_f16(w0, w1, hi, lo);
 }
@@ -199,8 +205,10 @@ struct SplitArgs {
     int* tickets;               // [max_seqs * R], zero between launches
 };
 
-template <int DP, bool F8, int NROW>
+// FINE: a third bf16 term of the weights, for fp32 outputs over bf16 rows.
+template <int DP, bool F8, int NROW, bool FINE>
 struct Kernel {
+    static_assert(!(F8 && FINE), "the f16 terms hold 22 bits");
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
     static constexpr int PART = part_floats(DP, F8, NROW), PROW = part_row(DP, F8), PHEAD = NROW * PROW;
@@ -448,12 +456,12 @@ struct Kernel {
         const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
 #pragma unroll
         for (int n2 = 0; n2 < NT / 2; n2++) {
-            uint32_t h0, l0, h2, l2, h1 = 0, l1 = 0, h3 = 0, l3 = 0;
-            split<F8>(x[2 * n2][0], x[2 * n2][1], h0, l0);
-            split<F8>(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2);
+            uint32_t h0, l0, h2, l2, h1 = 0, l1 = 0, h3 = 0, l3 = 0, t0 = 0, t1 = 0, t2 = 0, t3 = 0;
+            split<F8>(x[2 * n2][0], x[2 * n2][1], h0, l0, t0);
+            split<F8>(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2, t2);
             if (NROW == 16) {
-                split<F8>(x[2 * n2][2], x[2 * n2][3], h1, l1);
-                split<F8>(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3);
+                split<F8>(x[2 * n2][2], x[2 * n2][3], h1, l1, t1);
+                split<F8>(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3, t3);
             }
             auto mma_p = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
                 if (NROW == 8) {
@@ -462,6 +470,7 @@ struct Kernel {
                     mma<F8>(d, h0, h1, h2, h3, b0, b1);
                     mma<F8>(d, l0, l1, l2, l3, b0, b1);
                 }
+                if (FINE) mma<F8>(d, t0, t1, t2, t3, b0, b1);
             };
 #pragma unroll
             for (int c2 = 0; c2 < CPR / 2; c2++) {
@@ -729,10 +738,10 @@ struct Place {
     int b, row, t, tiles;
 };
 
-template <int DP, bool F8, int NROW>
+template <int DP, bool F8, int NROW, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ SplitArgs s)
 {
-    using K = Kernel<DP, F8, NROW>;
+    using K = Kernel<DP, F8, NROW, FINE>;
     constexpr int TT = K::TT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t s_warp[kWarps];
@@ -1104,10 +1113,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     }
 }
 
-template <int DP, bool F8, int NROW>
+template <int DP, bool F8, int NROW, bool FINE>
 cudaError_t launch(const SplitArgs& s, cudaStream_t st)
 {
-    using K = Kernel<DP, F8, NROW>;
+    using K = Kernel<DP, F8, NROW, FINE>;
     const size_t smem = (size_t)kWarps * K::REGION + (2 * (size_t)s.a.B + 1) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.a.sms);
@@ -1119,15 +1128,23 @@ cudaError_t launch(const SplitArgs& s, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn<DP, F8, NROW>, s);
+    return cudaLaunchKernelEx(&cfg, k_attn<DP, F8, NROW, FINE>, s);
 }
 
-template <int DP, bool F8, int NROW>
-cudaError_t allow()
+// The kernel of a handle's configuration: f(its template parameters).
+template <class F>
+cudaError_t dispatch(int D, bool e4m3, int G, bool f32, F f)
 {
-    using K = Kernel<DP, F8, NROW>;
-    return cudaFuncSetAttribute(k_attn<DP, F8, NROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kWarps * K::REGION + (2 * kAttnMaxSeqs + 1) * 4);
+    using std::bool_constant;
+    using std::integral_constant;
+    auto rows = [&](auto dp, auto f8, auto fine) {
+        return G <= 8 ? f(dp, f8, integral_constant<int, 8>(), fine) : f(dp, f8, integral_constant<int, 16>(), fine);
+    };
+    auto type = [&](auto dp) {
+        if (e4m3) return rows(dp, bool_constant<true>(), bool_constant<false>());
+        return f32 ? rows(dp, bool_constant<false>(), bool_constant<true>()) : rows(dp, bool_constant<false>(), bool_constant<false>());
+    };
+    return D <= 64 ? type(integral_constant<int, 64>()) : type(integral_constant<int, 128>());
 }
 
 int rows_of(int hq, int hkv)
@@ -1151,17 +1168,13 @@ AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms)
     return w;
 }
 
-cudaError_t attn_init_device()
+cudaError_t attn_init_device(int hq, int hkv, int D, bool e4m3, bool f32)
 {
-    cudaError_t e = allow<64, false, 8>();
-    if (e == cudaSuccess) e = allow<64, false, 16>();
-    if (e == cudaSuccess) e = allow<128, false, 8>();
-    if (e == cudaSuccess) e = allow<128, false, 16>();
-    if (e == cudaSuccess) e = allow<64, true, 8>();
-    if (e == cudaSuccess) e = allow<64, true, 16>();
-    if (e == cudaSuccess) e = allow<128, true, 8>();
-    if (e == cudaSuccess) e = allow<128, true, 16>();
-    return e;
+    return dispatch(D, e4m3, hq / hkv, f32, [](auto dp, auto f8, auto nrow, auto fine) {
+        using K = Kernel<dp(), f8(), nrow(), fine()>;
+        return cudaFuncSetAttribute(k_attn<dp(), f8(), nrow(), fine()>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kWarps * K::REGION + (2 * kAttnMaxSeqs + 1) * 4);
+    });
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
@@ -1177,12 +1190,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
     s.tickets = reinterpret_cast<int*>(a.ws + w.tickets);
     s.frags = reinterpret_cast<float*>(a.ws + w.frags);
     s.parts = reinterpret_cast<float*>(a.ws + w.parts);
-    if (a.D <= 64) {
-        if (a.e4m3) return s.G <= 8 ? launch<64, true, 8>(s, st) : launch<64, true, 16>(s, st);
-        return s.G <= 8 ? launch<64, false, 8>(s, st) : launch<64, false, 16>(s, st);
-    }
-    if (a.e4m3) return s.G <= 8 ? launch<128, true, 8>(s, st) : launch<128, true, 16>(s, st);
-    return s.G <= 8 ? launch<128, false, 8>(s, st) : launch<128, false, 16>(s, st);
+    return dispatch(a.D, a.e4m3, s.G, a.out_f32, [&](auto dp, auto f8, auto nrow, auto fine) {
+        return launch<dp(), f8(), nrow(), fine()>(s, st);
+    });
 }
 
 }  // namespace moe

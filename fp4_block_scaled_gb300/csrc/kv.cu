@@ -141,7 +141,9 @@ int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device)
     h->device = device;
     void* ws = nullptr;
     if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        attn_init_device() != cudaSuccess || rope_init_device() != cudaSuccess || copy_init_device() != cudaSuccess) {
+        attn_init_device(cfg->num_q_heads, cfg->num_kv_heads, cfg->head_dim, cfg->kv_dtype != MOE_KV_BF16,
+                         cfg->out_dtype == MOE_OUT_F32) != cudaSuccess ||
+        rope_init_device() != cudaSuccess || copy_init_device() != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;
     }

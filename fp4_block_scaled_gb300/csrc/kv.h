@@ -62,7 +62,7 @@ struct AttnWorkspace {
 };
 constexpr int kAttnMaxSeqs = 2048;
 AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms);
-cudaError_t attn_init_device();
+cudaError_t attn_init_device(int hq, int hkv, int D, bool e4m3, bool f32);
 
 constexpr int kCopyLayers = 64;
 struct CopyArgs {

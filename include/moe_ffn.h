@@ -563,8 +563,9 @@ int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long 
  *   scale      finite; 0: 1 / sqrt(D).  softcap >= 0 and finite (0: none);
  *              window >= 0
  * Scores, softmax and sums are fp32; the weights enter the product with v as
- * two 16-bit terms: 16 significant bits (E4M3: the weight times v's scale,
- * to 2^-22 of itself or 2^-31 of the sequence's largest).  A key or value that is not finite
+ * 16-bit terms: 16 significant bits for a bf16 output, 24 for an fp32 one
+ * (E4M3: the weight times v's scale, to 2^-22 of itself or 2^-31 of the
+ * sequence's largest).  A key or value that is not finite
  * makes the outputs it enters not finite; pool contents outside the keys
  * above are never used, whatever they are.  A page id outside
  * [0, num_pages) sets MOE_ERR_BAD_INDEX and its keys are left out; so does a
