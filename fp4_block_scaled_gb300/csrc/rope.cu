@@ -86,18 +86,19 @@ __device__ __forceinline__ uint32_t amax8(const uint4& u)
     return __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
 }
 
-// Heads whose loads a lane has in flight: 1, 2 and 4 took 69.4, 58.0 and 54.3 us
-// for the queries and keys of 16383 tokens (40 heads of 128), where the bytes
-// alone take 49.5 us.
-constexpr int kAhead = 4;
-
 // GL lanes (a power of two) hold a token's head, 16 elements a lane as two runs
 // of 8: with MOE_ROPE_HALF the rotated lanes hold a pair's halves (8 e and
 // rot / 2 + 8 e), all others 16 elements in a row; either way a lane needs the
 // same eight angles for every head, and computes them once.  The token's heads
 // (q, k, v one after another) are dealt to gridDim.y blocks.
-template <int GL>
-__global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a)
+// AHEAD: heads whose loads a lane has in flight.  BLOCKS: blocks of an SM.  For the
+// queries and keys of 16383 tokens (40 heads of 128), whose bytes alone take
+// 49.5 us: 53.9 us with four heads and three blocks, 58.4 with two, 69 with one,
+// 55.1 with two heads and four blocks, 68 with four.  The E4M3 append, with more
+// to compute per byte, is the other way round: 16000 tokens 66.3 us with four
+// heads and three blocks, 63.9 with two and four (bytes 53.2).
+template <int GL, int AHEAD, int BLOCKS>
+__global__ void __launch_bounds__(256, BLOCKS) k_rope(const __grid_constant__ RopeArgs a)
 {
     const int e = threadIdx.x & (GL - 1);
     const int t = (int)(((size_t)blockIdx.x * 256 + threadIdx.x) / GL);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
     pdl_wait();
     const int pos = t < a.T ? a.pos[t] : -1;
     const int sq = a.append && a.seq && t < a.T ? a.seq[t] : t;
-    uint4 r0[kAhead], r1[kAhead];
+    uint4 r0[AHEAD], r1[AHEAD];
     // heads [0, hq) are q's, then k's, then v's: where unit u's lane elements lie in its head
     auto turns = [&](int u) { return rotated && u < a.hq + a.hk; };
     auto at0 = [&](int u) { return turns(u) && half ? 8 * e : 16 * e; };
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
         r1[i] = *reinterpret_cast<const uint4*>(src + at1(u));
     };
 #pragma unroll
-    for (int i = 0; i < kAhead; i++) load(i, blockIdx.y + i * split);
+    for (int i = 0; i < AHEAD; i++) load(i, blockIdx.y + i * split);
     uint64_t F[8];
     if (rotated) {
 #pragma unroll
@@ -146,9 +147,9 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
         if (placed) row = (size_t)page * a.hk * a.page_size + (pos - pi * a.page_size);
         else if (e == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadIndex);
     }
-    for (int u0 = blockIdx.y; u0 < units; u0 += kAhead * split) {
+    for (int u0 = blockIdx.y; u0 < units; u0 += AHEAD * split) {
 #pragma unroll
-        for (int i = 0; i < kAhead; i++) {
+        for (int i = 0; i < AHEAD; i++) {
             const int u = u0 + i * split;
             if (u >= units) break;
             if (turns(u)) {
@@ -212,12 +213,12 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
                     if (e == 0) (key ? a.pool.ks : a.pool.vs)[prow] = (uint8_t)s;
                 }
             }
-            load(i, u + kAhead * split);        // the next round's
+            load(i, u + AHEAD * split);        // the next round's
         }
     }
 }
 
-template <int GL>
+template <int GL, int AHEAD, int BLOCKS>
 cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
 {
     const int units = a.hq + a.hk + a.hv;
@@ -239,7 +240,7 @@ cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_rope<GL>, a);
+    return cudaLaunchKernelEx(&cfg, k_rope<GL, AHEAD, BLOCKS>, a);
 }
 
 }  // namespace
@@ -247,20 +248,23 @@ cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
 cudaError_t rope_init_device()
 {
     cudaFuncAttributes at;                      // loads them, so that a first call may be captured
-    cudaError_t e = cudaFuncGetAttributes(&at, k_rope<1>);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<2>);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<4>);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_rope<8>);
+    const void* all[] = {(const void*)k_rope<1, 4, 3>, (const void*)k_rope<2, 4, 3>, (const void*)k_rope<4, 4, 3>,
+                         (const void*)k_rope<8, 4, 3>, (const void*)k_rope<2, 2, 4>, (const void*)k_rope<4, 2, 4>,
+                         (const void*)k_rope<8, 2, 4>};
+    cudaError_t e = cudaSuccess;
+    for (const void* k : all)
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k);
     return e;
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
 {
     if (a.T == 0 || a.hq + a.hk + a.hv == 0) return cudaSuccess;
-    if (a.D <= 16) return launch_gl<1>(a, s);
-    if (a.D <= 32) return launch_gl<2>(a, s);
-    if (a.D <= 64) return launch_gl<4>(a, s);
-    return launch_gl<8>(a, s);
+    if (a.append && a.e4m3)                     // D is a multiple of 32
+        return a.D <= 32 ? launch_gl<2, 2, 4>(a, s) : a.D <= 64 ? launch_gl<4, 2, 4>(a, s) : launch_gl<8, 2, 4>(a, s);
+    if (a.D <= 16) return launch_gl<1, 4, 3>(a, s);
+    if (a.D <= 32) return launch_gl<2, 4, 3>(a, s);
+    return a.D <= 64 ? launch_gl<4, 4, 3>(a, s) : launch_gl<8, 4, 3>(a, s);
 }
 
 }  // namespace moe
