@@ -91,6 +91,21 @@ def test_many_short_sequences(hq):
     _run([(i * 37) % 50 for i in range(300)], hq, 2, 64, 16)
 
 
+def test_no_keys_at_all():
+    out, lse = _run([0, 0, 0], 8, 2, 64, 16)
+    assert not out.any() and np.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,D", [(16, 128), (48, 64)])
+def test_short_rows_stay_whole_between_long_ones(hq, D, kv):
+    """Enough short sequences that none of them is split, with long ones that
+    are between them, at the ends and next to each other."""
+    lens = [(i * 37) % 131 for i in range(330)]
+    lens[0], lens[100], lens[101], lens[200], lens[329] = 3000, 2100, 129, 128, 2500
+    _run(lens, hq, 4, D, 32, kv, window=0)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 1000])
 def test_window(window, kv):
