@@ -198,11 +198,17 @@ __device__ __forceinline__ uint32_t at_chunk(uint32_t base, int r, int c)
 
 // Rows of up to kWhole keys stay with one warp where every warp has a tile and
 // the rows are short on the average (at most kShort tiles): a part costs more
-// than the few tiles it moves.  256 sequences of up to 30 and 100 keys: 15.9 and
-// 26.1 us when split, 11.7 and 22.0 when not; E4M3 of 100: 21.3 and 17.5.  Where
+// than the few tiles it moves.  256 sequences of up to 30 and 100 keys: 13.4 and
+// 21.3 us when split, 10.4 and 19.2 when not; E4M3 of 100: 18.7 and 16.6.  Where
 // warps would idle splitting wins: one E4M3 sequence of 100 keys 6.7 us, 9.7 whole.
 constexpr int kWhole = 128;
 constexpr int kShort = 16;
+
+// What a row itself (queries, output, places) costs a warp, in tiles, when the
+// line is shared out: without it the warps with many short rows end last (128
+// E4M3 sequences of up to 8000 keys, some of one key: 189 us, 181 with 1 to 4; 256 of
+// up to 1000: 72 and 54.5; 48 windows of 1000 keys: 43.8 and 36.8).
+constexpr uint32_t kRowCost = 2;
 
 struct SplitArgs {
     AttnArgs a;
@@ -805,30 +811,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         if (tid == 0) pre[0] = 0;
         __syncthreads();
     }
-    // the CTAs' stretches, equal to one tile, and the warps' within them; fewer
-    // CTAs where they would not have a tile for every warp
-    const uint32_t W = base * (uint32_t)s.R;
+    // The line in units: a row's tiles, and kRowCost for the row itself where warps
+    // have several rows.  The CTAs' stretches are equal to one unit, and the warps'
+    // within them; fewer CTAs where they would not have a tile for every warp.
+    const uint32_t R = (uint32_t)s.R, tiles_all = base * R;
+    const bool full = tiles_all >= gridDim.x * kWarps;
+    const uint32_t V = full ? kRowCost : 0, W = tiles_all + V * (uint32_t)B * R;
     const uint32_t grid = min(gridDim.x, (W + kWarps - 1) / kWarps);
     if (blockIdx.x >= grid) return;
     const uint32_t wq = W / grid, wr = W - wq * grid;
     const uint32_t mine = wq + (blockIdx.x < wr ? 1u : 0u), per = mine / kWarps, left = mine % kWarps;
-    uint32_t u = blockIdx.x * wq + min((uint32_t)blockIdx.x, wr) + warp * per + min((uint32_t)warp, left);
-    uint32_t end = u + per + ((uint32_t)warp < left ? 1u : 0u);
+    const uint32_t from = blockIdx.x * wq + min((uint32_t)blockIdx.x, wr) + warp * per + min((uint32_t)warp, left);
+    const uint32_t to = from + per + ((uint32_t)warp < left ? 1u : 0u);
     auto cta_of = [&](uint32_t at) { return at < wr * (wq + 1) ? at / (wq + 1) : wr + (at - wr * (wq + 1)) / wq; };
+    auto units_before = [&](int b) { return (pre[b] + V * (uint32_t)b) * R; };
 
-    auto place_of = [&](uint32_t at) {
+    // The place where a stretch that ends or begins at unit `at` is cut, and the
+    // tiles before it.  The units of the row itself come first and hold no tile; a
+    // cut inside a row that is not split moves to its end.
+    const bool whole_rows = full && base <= (uint32_t)B * kShort;
+    auto cut = [&](uint32_t at, uint32_t& tiles) {
         int lo = 0, hi = B - 1;
         while (lo < hi) {                       // the last sequence that begins at or before `at`
             const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] * (uint32_t)s.R <= at) lo = mid;
+            if (units_before(mid) <= at) lo = mid;
             else hi = mid - 1;
         }
         Place p;
         p.b = lo;
         p.tiles = (int)(pre[lo + 1] - pre[lo]);
-        const uint32_t in = at - pre[lo] * (uint32_t)s.R;
-        p.row = (int)(in / (uint32_t)p.tiles);
-        p.t = (int)(in - (uint32_t)p.row * (uint32_t)p.tiles);
+        const uint32_t units = (uint32_t)p.tiles + V, in = at - units_before(lo);
+        p.row = (int)(in / units);
+        const uint32_t t = in - (uint32_t)p.row * units;
+        p.t = (int)(t - min(t, V));
+        tiles = at - V * ((uint32_t)p.b * R + (uint32_t)p.row) - min(t, V);
+        if (whole_rows && p.tiles <= kWhole / TT && p.t > 0) {
+            tiles += (uint32_t)(p.tiles - p.t);
+            p.t = 0;
+            if (++p.row == s.R) {
+                p.row = 0;
+                p.b++;
+                p.tiles = p.b < B ? (int)(pre[p.b + 1] - pre[p.b]) : 0;
+            }
+        }
         return p;
     };
     auto advance = [&](Place& p) {
@@ -839,16 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         p.b++;
         if (p.b < B) p.tiles = (int)(pre[p.b + 1] - pre[p.b]);
     };
-    // a boundary of two stretches inside a row that is not split moves to its end
-    if (base <= (uint32_t)B * kShort && W >= gridDim.x * kWarps) {
-        auto whole = [&](uint32_t at) {
-            if (at >= W) return at;
-            const Place p = place_of(at);
-            return p.tiles <= kWhole / TT && p.t > 0 ? at + (uint32_t)(p.tiles - p.t) : at;
-        };
-        u = whole(u);
-        end = whole(end);
-    }
+    uint32_t u = tiles_all, end = to;           // in tiles from here on
+    Place begin = {};
+    if (from < to) begin = cut(from, u);
+    if (to >= W) end = tiles_all;
+    else if (full) cut(to, end);
     auto first_key = [&](int b) { return s.a.window > 0 ? max(0, slen[b] - s.a.window) : 0; };
 
     if (lane < 2) s_frag[2 * warp + lane].b = -1;
@@ -888,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             }
         };
         uint32_t badq = 0;                      // 2 bits a stage
-        Place pp = place_of(u), cp = pp;
+        Place pp = begin, cp = begin;
         uint32_t up = u;
         const int rb = s.a.D * (F8 ? 1 : 2);    // bytes of a cached row
         const int c = lane % K::CPR, r0 = lane / K::CPR;
@@ -1068,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         s_first[slot] = -1;
         if (f >= 0) {
             const uint32_t tiles = pre[s_frag[f].b + 1] - pre[s_frag[f].b];
-            const uint32_t r0 = pre[s_frag[f].b] * (uint32_t)s.R + (uint32_t)s_frag[f].row * tiles;
+            const uint32_t r0 = units_before(s_frag[f].b) + (uint32_t)s_frag[f].row * (tiles + V) + V;
             s_c0[slot] = (int)cta_of(r0);
             s_count[slot] = (int)cta_of(r0 + tiles - 1) - s_c0[slot] + 1;
         }

@@ -53,8 +53,8 @@ int check_kv_cfg(const moe_kv_config* c)
         return MOE_ERR_UNSUPPORTED;
     const long long cap = (long long)c->max_pages_per_seq * c->page_size;      // tokens of a sequence: int32 positions
     if (cap > INT32_MAX - 4096) return MOE_ERR_UNSUPPORTED;
-    // the attention counts a batch's tiles of 16 keys, in all rows, in 32 bits
-    if ((double)((cap + 15) / 16) * c->max_seqs * c->num_q_heads > 4294967294.0) return MOE_ERR_UNSUPPORTED;
+    // the attention counts a batch's tiles of 16 keys, in all rows, in 32 bits (with some for each row)
+    if ((double)((cap + 15) / 16) * c->max_seqs * c->num_q_heads > 4280000000.0) return MOE_ERR_UNSUPPORTED;
     // and pool places in blocks of 16 rows
     if ((double)c->num_pages * c->num_kv_heads * (c->page_size / 16) > 4294967294.0) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
