@@ -27,15 +27,15 @@
 // Measured (GPU time, back to back; 6783 GB/s is the rate of a plain copy):
 //   64 sequences of up to 8000 keys, 8 x 128, bf16:   166 us, 6.36 TB/s
 //   2 of up to 131071:                                138 us, 6.45 TB/s
-//   128 of up to 8000, E4M3, 8 query heads a key head: 188 us, 5.53 TB/s
-//   48 windows of 1000 keys, 16 x 64, capped scores:   42 us, 4.13 TB/s
-//   one sequence of 1000 keys:                        8.0 us (a launch of an empty
-//     kernel 2.1; lengths, page ids, keys: three round trips to memory; the join)
+//   128 of up to 8000, E4M3, 8 query heads a key head: 181 us, 5.74 TB/s
+//   48 windows of 1000 keys, 16 x 64, capped scores:   37 us, 4.65 TB/s
+//   one sequence of 1000 keys:                        8.2 us (a launch takes 2.1;
+//     then lengths, page ids, keys, the ticket and the join: five round trips)
 // While the rings are full the SMs take in 25 bytes a cycle each, the memory's
-// rate; what is lost is 3.4 us before them, the 10 to 20 % by which SMs with a
+// rate; what is lost is 3.4 us before them, the tenth by which SMs with a
 // slower way to memory end later than others (dealing out the last eighth of
 // the line at run time evened that out, but the many parts it left cost the
-// join as much), and 2 to 6 us of merging.
+// join as much), and 2 to 5 us of merging.
 #include <type_traits>
 
 #include "common.cuh"
