@@ -18,16 +18,16 @@
 // 16 bytes a lane, two of three 8 KB tiles in flight: 128 KB an SM), with no
 // barrier between warps, and fetches ahead what a tile's address needs (the
 // page ids of the next 32 tiles) and what the next row begins with (its
-// queries).  The products are mma.sync m16n8k16, which are busy 15 to 22 % of the
+// queries).  The products are mma.sync m16n8k16, which are busy 14 to 31 % of the
 // time: a tile of one token's 8 query heads fills half of an MMA's 16 rows (the
 // other half carries the weights' low terms), and a tcgen05 MMA would want 128
 // keys in one place and a round trip through tensor memory per tile for the
 // same bytes.
 //
 // Measured (GPU time, back to back; 6783 GB/s is the rate of a plain copy):
-//   64 sequences of up to 8000 keys, 8 x 128, bf16:   166 us, 6.36 TB/s
+//   64 sequences of up to 8000 keys, 8 x 128, bf16:   164 us, 6.43 TB/s
 //   2 of up to 131071:                                138 us, 6.45 TB/s
-//   128 of up to 8000, E4M3, 8 query heads a key head: 181 us, 5.74 TB/s
+//   128 of up to 8000, E4M3, 8 query heads a key head: 179 us, 5.81 TB/s
 //   48 windows of 1000 keys, 16 x 64, capped scores:   37 us, 4.65 TB/s
 //   one sequence of 1000 keys:                        8.2 us (a launch takes 2.1;
 //     then lengths, page ids, keys, the ticket and the join: five round trips)
@@ -35,7 +35,7 @@
 // rate; what is lost is 3.4 us before them, the tenth by which SMs with a
 // slower way to memory end later than others (dealing out the last eighth of
 // the line at run time evened that out, but the many parts it left cost the
-// join as much), and 2 to 5 us of merging.
+// join as much), and 2 to 4 us of merging.
 #include <type_traits>
 
 #include "common.cuh"
@@ -135,7 +135,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 // p as bf16 terms: hi = bf16(p), lo = bf16(p - hi), together 16 significant
-// bits (bf16 alone would put an error of 2^-9 on every weight), enough for a
+// bits (bf16 alone would put an error of up to 2^-8 on every weight), enough for a
 // bf16 output; the rest, bf16(p - hi - lo), brings 24 for an fp32 one, whose error
 // two terms would leave at 1.3e-6 of the output's norm.
 __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo, uint32_t& rest)
@@ -1105,18 +1105,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         float acc[2][K::VEC];
 #pragma unroll
         for (int k = 0; k < K::VEC; k++) acc[0][k] = acc[1][k] = 0.0f;
+        for (unsigned rest = mem; rest;) {      // four parts' loads at a time
+            float2 by[4];
+            float v[4][2][K::VEC];
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            const unsigned is = (mem >> (2 * w)) & 3u;
-            const float2 by = *reinterpret_cast<const float2*>(tab + (2 * w + (is >> 1)) * NROW + g);
-            float v[2][K::VEC];
+            for (int i = 0; i < 4; i++) {
+                // past the last part: the first one again, without weight
+                const int x = rest ? __ffs(rest) - 1 : f;
+                by[i] = *reinterpret_cast<const float2*>(tab + x * NROW + g);
+                if (!rest) by[i] = make_float2(0.0f, 0.0f);
+                rest &= rest - 1;
 #pragma unroll
-            for (int r = 0; r < 2; r++) K::load_vec(v[r], near(w, is) + (g + r) * K::PROW + lane * K::VEC, false);
-#pragma unroll
-            for (int k = 0; k < K::VEC; k++) {
-                acc[0][k] = is ? fmaf(by.x, v[0][k], acc[0][k]) : acc[0][k];
-                acc[1][k] = is ? fmaf(by.y, v[1][k], acc[1][k]) : acc[1][k];
+                for (int r = 0; r < 2; r++)
+                    K::load_vec(v[i][r], near(x >> 1, 1u + (x & 1)) + (g + r) * K::PROW + lane * K::VEC, false);
             }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int k = 0; k < K::VEC; k++) {
+                    acc[0][k] = fmaf(by[i].x, v[i][0][k], acc[0][k]);
+                    acc[1][k] = fmaf(by[i].y, v[i][1][k], acc[1][k]);
+                }
         }
         float* to = whole ? nullptr : s.parts + ((size_t)blockIdx.x * 2 + slot) * K::PART;
 #pragma unroll

@@ -564,7 +564,7 @@ int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long 
  *              window >= 0
  * Scores, softmax and sums are fp32; the weights enter the product with v as
  * 16-bit terms: 16 significant bits for a bf16 output, 24 for an fp32 one
- * (E4M3: the weight times v's scale, to 2^-22 of itself or 2^-31 of the
+ * (E4M3: the weight times v's scale, to 2^-21 of itself or 2^-31 of the
  * sequence's largest).  A key or value that is not finite
  * makes the outputs it enters not finite; pool contents outside the keys
  * above are never used, whatever they are.  A page id outside
