@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ Copy
     uint4 v[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; i++)
-        if (i * 256 + (int)threadIdx.x < n) v[i] = ldg_stream_v4(s + i * 256 + threadIdx.x);
+        if (i * 256 + (int)threadIdx.x < n) v[i] = __ldcg(s + i * 256 + threadIdx.x);
 #pragma unroll
     for (int i = 0; i < VEC; i++)
         if (i * 256 + (int)threadIdx.x < n) d[i * 256 + threadIdx.x] = v[i];
