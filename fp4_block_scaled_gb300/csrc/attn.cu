@@ -52,7 +52,10 @@ constexpr int kThreads = 32 * kWarps;
 // (in powers of two): weights stay below 2^8, and most tiles rescale nothing.
 constexpr float kSlack = 8.0f;
 
-__host__ __device__ constexpr int tile_keys(int DP, bool F8) { return F8 || DP <= 64 ? 32 : 16; }
+// Keys of a tile: 8 KB of k and v rows, or less (E4M3 rows of 32 elements); tiles of
+// half the keys took 35.7 us where E4M3 rows of 64 now take 33.0 (32 sequences of up
+// to 8000).
+__host__ __device__ constexpr int tile_keys(int DP, bool F8) { return F8 && DP <= 64 ? 64 : F8 || DP <= 64 ? 32 : 16; }
 __host__ __device__ constexpr int row_bytes(int DP, bool F8) { return DP * (F8 ? 1 : 2); }
 // a tile in the ring: k rows, v rows, then (E4M3) their scale bytes
 __host__ __device__ constexpr int stage_bytes(int DP, bool F8)
@@ -219,11 +222,13 @@ struct SplitArgs {
     int* tickets;               // [max_seqs * R], zero between launches
 };
 
-// FINE: a third bf16 term of the weights, for fp32 outputs over bf16 rows.
-template <int DP, bool F8, int NROW, bool FINE>
+// DP: the elements of a row's place in the ring, CW <= DP those that are computed
+// with.  FINE: a third bf16 term of the weights, for fp32 outputs over bf16 rows.
+template <int DP, int CW, bool F8, int NROW, bool FINE>
 struct Kernel {
     static_assert(!(F8 && FINE), "the f16 terms hold 22 bits");
-    static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = DP / 16, ND = DP / 8;
+    static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = CW / 16, ND = CW / 8;
+    static constexpr int C2 = row_bytes(CW, F8) / 32;        // pairs of chunks computed with
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
     static constexpr int PART = part_floats(DP, F8, NROW), PROW = part_row(DP, F8), PHEAD = NROW * PROW;
     static constexpr int SCALES = F8 ? 8 * TT : 0;           // a tile's scales as numbers
@@ -331,10 +336,12 @@ struct Kernel {
         if (F8) {
             // a key a lane: k's scale as a number (byte 0 as zero: below 2^-117 with any
             // code), v's as an exponent; a NaN row has NaN codes
-            static_assert(!F8 || TT == 32, "a key a lane");
-            const uint8_t* b = stp + 2 * TT * ROWB + lane;
-            sc[lane] = __uint_as_float((uint32_t)b[0] << 23);
-            sc[TT + lane] = __uint_as_float(0x4B000000u | b[TT]) - 8388735.0f;      // 2^23 + byte, less 2^23 + 127
+#pragma unroll
+            for (int i = lane; i < TT; i += 32) {
+                const uint8_t* b = stp + 2 * TT * ROWB + i;
+                sc[i] = __uint_as_float((uint32_t)b[0] << 23);
+                sc[TT + i] = __uint_as_float(0x4B000000u | b[TT]) - 8388735.0f;     // 2^23 + byte, less 2^23 + 127
+            }
             __syncwarp();
         }
         const uint32_t kb = st, vb = st + TT * ROWB;
@@ -346,7 +353,7 @@ struct Kernel {
         // scores: 16 keys x 32 bytes of their rows per load
         const int kr = (lane & 7) + ((lane >> 4) & 1) * 8, kc = (lane >> 3) & 1;
 #pragma unroll
-        for (int c2 = 0; c2 < CPR / 2; c2++) {
+        for (int c2 = 0; c2 < C2; c2++) {
 #pragma unroll
             for (int n2 = 0; n2 < NT / 2; n2++) {
                 uint32_t r[4];
@@ -487,7 +494,7 @@ struct Kernel {
                 if (FINE) mma<F8>(d, t0, t1, t2, t3, b0, b1);
             };
 #pragma unroll
-            for (int c2 = 0; c2 < CPR / 2; c2++) {
+            for (int c2 = 0; c2 < C2; c2++) {
                 uint32_t r[4];
                 ldsm4t(r, at_chunk<ROWB>(vb, 16 * n2 + vr, 2 * c2 + vc));
                 if (F8) {
@@ -752,10 +759,10 @@ struct Place {
     int b, row, t, tiles;
 };
 
-template <int DP, bool F8, int NROW, bool FINE>
+template <int DP, int CW, bool F8, int NROW, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ SplitArgs s)
 {
-    using K = Kernel<DP, F8, NROW, FINE>;
+    using K = Kernel<DP, CW, F8, NROW, FINE>;
     constexpr int TT = K::TT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t s_warp[kWarps];
@@ -907,7 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
                 if (key < n && !ok && key + 16 > first) atomicOr(s.a.status, kStatusBadIndex);
             }
         };
-        uint32_t badq = 0;                      // 2 bits a stage
+        constexpr int BB = TT / 16;             // a tile's bits of badq
+        uint32_t badq = 0;
         Place pp = begin, cp = begin;
         uint32_t up = u;
         const int rb = s.a.D * (F8 ? 1 : 2);    // bytes of a cached row
@@ -980,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
                     if (F8 && lane < 2) cp_async16(st + 2 * TT * K::ROWB + lane * TT + 16 * i, slane + row, ok ? 16 : 0);
                 }
             }
-            badq = (badq & ~(3u << (2 * stage))) | (bad << (2 * stage));
+            badq = (badq & ~(((1u << BB) - 1u) << (BB * stage))) | (bad << (BB * stage));
             up++;
             if (up < end) advance(pp);
         };
@@ -1003,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             __syncwarp();
             const int n = slen[cp.b], first = first_key(cp.b), at = (first / TT + cp.t) * TT;
             k.tile(s, my32 + stage * K::STAGE, my + stage * K::STAGE, reinterpret_cast<float*>(my + K::STAGES * K::STAGE), lane, max(0, first - at), min(TT, n - at),
-                   (badq >> (2 * stage)) & 3u);
+                   (badq >> (BB * stage)) & ((1u << BB) - 1u));
             __syncwarp();
             stage = stage + 1 == K::STAGES ? 0 : stage + 1;
             u++;
@@ -1160,10 +1168,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     }
 }
 
-template <int DP, bool F8, int NROW, bool FINE>
+template <int DP, int CW, bool F8, int NROW, bool FINE>
 cudaError_t launch(const SplitArgs& s, cudaStream_t st)
 {
-    using K = Kernel<DP, F8, NROW, FINE>;
+    using K = Kernel<DP, CW, F8, NROW, FINE>;
     const size_t smem = (size_t)kWarps * K::REGION + (2 * (size_t)s.a.B + 1) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.a.sms);
@@ -1175,7 +1183,7 @@ cudaError_t launch(const SplitArgs& s, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn<DP, F8, NROW, FINE>, s);
+    return cudaLaunchKernelEx(&cfg, k_attn<DP, CW, F8, NROW, FINE>, s);
 }
 
 // The kernel of a handle's configuration: f(its template parameters).
@@ -1184,14 +1192,21 @@ cudaError_t dispatch(int D, bool e4m3, int G, bool f32, F f)
 {
     using std::bool_constant;
     using std::integral_constant;
-    auto rows = [&](auto dp, auto f8, auto fine) {
-        return G <= 8 ? f(dp, f8, integral_constant<int, 8>(), fine) : f(dp, f8, integral_constant<int, 16>(), fine);
+    auto rows = [&](auto dp, auto cw, auto f8, auto fine) {
+        return G <= 8 ? f(dp, cw, f8, integral_constant<int, 8>(), fine) : f(dp, cw, f8, integral_constant<int, 16>(), fine);
     };
-    auto type = [&](auto dp) {
-        if (e4m3) return rows(dp, bool_constant<true>(), bool_constant<false>());
-        return f32 ? rows(dp, bool_constant<false>(), bool_constant<true>()) : rows(dp, bool_constant<false>(), bool_constant<false>());
+    auto type = [&](auto dp, auto cw) {
+        if (e4m3) return rows(dp, cw, bool_constant<true>(), bool_constant<false>());
+        return f32 ? rows(dp, cw, bool_constant<false>(), bool_constant<true>()) : rows(dp, cw, bool_constant<false>(), bool_constant<false>());
     };
-    return D <= 64 ? type(integral_constant<int, 64>()) : type(integral_constant<int, 128>());
+    using C64 = integral_constant<int, 64>;
+    using C96 = integral_constant<int, 96>;
+    using C128 = integral_constant<int, 128>;
+    if (D <= 64) return type(C64(), C64());
+    // E4M3 rows of up to 96 are computed 96 wide (32 sequences of up to 8000: 45.8 us, 52.7
+    // with 128); for bf16, which waits for memory, it makes no difference (71.3, 72.5)
+    if (e4m3 && D <= 96) return rows(C128(), C96(), bool_constant<true>(), bool_constant<false>());
+    return type(C128(), C128());
 }
 
 int rows_of(int hq, int hkv)
@@ -1217,9 +1232,9 @@ AttnWorkspace attn_workspace(int max_seqs, int hq, int hkv, int D, int sms)
 
 cudaError_t attn_init_device(int hq, int hkv, int D, bool e4m3, bool f32)
 {
-    return dispatch(D, e4m3, hq / hkv, f32, [](auto dp, auto f8, auto nrow, auto fine) {
-        using K = Kernel<dp(), f8(), nrow(), fine()>;
-        return cudaFuncSetAttribute(k_attn<dp(), f8(), nrow(), fine()>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return dispatch(D, e4m3, hq / hkv, f32, [](auto dp, auto cw, auto f8, auto nrow, auto fine) {
+        using K = Kernel<dp(), cw(), f8(), nrow(), fine()>;
+        return cudaFuncSetAttribute(k_attn<dp(), cw(), f8(), nrow(), fine()>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kWarps * K::REGION + (2 * kAttnMaxSeqs + 1) * 4);
     });
 }
@@ -1237,8 +1252,8 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
     s.tickets = reinterpret_cast<int*>(a.ws + w.tickets);
     s.frags = reinterpret_cast<float*>(a.ws + w.frags);
     s.parts = reinterpret_cast<float*>(a.ws + w.parts);
-    return dispatch(a.D, a.e4m3, s.G, a.out_f32, [&](auto dp, auto f8, auto nrow, auto fine) {
-        return launch<dp(), f8(), nrow(), fine()>(s, st);
+    return dispatch(a.D, a.e4m3, s.G, a.out_f32, [&](auto dp, auto cw, auto f8, auto nrow, auto fine) {
+        return launch<dp(), cw(), f8(), nrow(), fine()>(s, st);
     });
 }
 
