@@ -223,10 +223,10 @@ struct SplitArgs {
 };
 
 // DP: the elements of a row's place in the ring, CW <= DP those that are computed
-// with.  FINE: a third bf16 term of the weights, for fp32 outputs over bf16 rows.
+// with.  FINE: for fp32 outputs, a third term of the weights over bf16 rows, and a
+// tile's sums rounded into the row's.
 template <int DP, int CW, bool F8, int NROW, bool FINE>
 struct Kernel {
-    static_assert(!(F8 && FINE), "the f16 terms hold 22 bits");
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = CW / 16, ND = CW / 8;
     static constexpr int C2 = row_bytes(CW, F8) / 32;        // pairs of chunks computed with
     static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
@@ -325,6 +325,55 @@ struct Kernel {
     {
         if (NROW == 8) mma<F8>(d, q[ks][0], 0u, q[ks][1], 0u, b0, b1);
         else mma<F8>(d, q[ks][0], q[ks][1], q[ks][2], q[ks][3], b0, b1);
+    }
+
+    // The weights of 16 keys as A operands: high terms, low terms and (FINE, bf16)
+    // the rest, rows g and g + 8 of the first and the last 8 keys.
+    struct Terms {
+        uint32_t h[4], l[4], t[4];
+
+        __device__ __forceinline__ void make(const float (&a)[4], const float (&b)[4])
+        {
+            h[1] = h[3] = l[1] = l[3] = t[1] = t[3] = 0;
+            split<F8>(a[0], a[1], h[0], l[0], t[0]);
+            split<F8>(b[0], b[1], h[2], l[2], t[2]);
+            if (NROW == 16) {
+                split<F8>(a[2], a[3], h[1], l[1], t[1]);
+                split<F8>(b[2], b[3], h[3], l[3], t[3]);
+            }
+        }
+
+        __device__ __forceinline__ void times(float (&d)[4], uint32_t b0, uint32_t b1) const
+        {
+            if (NROW == 8) {
+                mma<F8>(d, h[0], l[0], h[2], l[2], b0, b1);
+            } else {
+                mma<F8>(d, h[0], h[1], h[2], h[3], b0, b1);
+                mma<F8>(d, l[0], l[1], l[2], l[3], b0, b1);
+            }
+            if (FINE && !F8) mma<F8>(d, t[0], t[1], t[2], t[3], b0, b1);
+        }
+    };
+
+    // Weights times 16 keys' values, the 32 bytes of their rows at `addr`.
+    __device__ __forceinline__ static void values(float (&d)[F8 ? 4 : 2][4], const Terms& w, uint32_t addr)
+    {
+        uint32_t r[4];
+        ldsm4t(r, addr);
+        if (F8) {
+            // chunk 2 c2 (r0, r1) and 2 c2 + 1 (r2, r3), 16 columns each: even ones, odd ones
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t e0, d0, e1, d1;
+                e4m3_to_f16(__byte_perm(r[2 * c], 0, 0x3120), e0, d0);
+                e4m3_to_f16(__byte_perm(r[2 * c + 1], 0, 0x3120), e1, d1);
+                w.times(d[F8 ? 2 * c : 0], e0, e1);
+                w.times(d[F8 ? 2 * c + 1 : 1], d0, d1);
+            }
+        } else {
+            w.times(d[0], r[0], r[1]);
+            w.times(d[1], r[2], r[3]);
+        }
     }
 
     // One tile: `lo`, `hi` are the first and one past the last key of it that
@@ -475,42 +524,34 @@ struct Kernel {
         // the A operand hold the weights' high terms and rows 8..15 their low
         // terms, so one MMA multiplies both; NROW 16 takes two.
         const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+        Terms w[FINE ? NT / 2 : 1];
+        if (FINE) {
+            // The tensor core cuts the sums it keeps to 24 bits, so a long row's would
+            // drift by 2^-25 a product of 16 keys (up to 6e-6 of a row's norm): a
+            // tile's sums are made alone and added, rounded, to the row's.
 #pragma unroll
-        for (int n2 = 0; n2 < NT / 2; n2++) {
-            uint32_t h0, l0, h2, l2, h1 = 0, l1 = 0, h3 = 0, l3 = 0, t0 = 0, t1 = 0, t2 = 0, t3 = 0;
-            split<F8>(x[2 * n2][0], x[2 * n2][1], h0, l0, t0);
-            split<F8>(x[2 * n2 + 1][0], x[2 * n2 + 1][1], h2, l2, t2);
-            if (NROW == 16) {
-                split<F8>(x[2 * n2][2], x[2 * n2][3], h1, l1, t1);
-                split<F8>(x[2 * n2 + 1][2], x[2 * n2 + 1][3], h3, l3, t3);
-            }
-            auto mma_p = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
-                if (NROW == 8) {
-                    mma<F8>(d, h0, l0, h2, l2, b0, b1);
-                } else {
-                    mma<F8>(d, h0, h1, h2, h3, b0, b1);
-                    mma<F8>(d, l0, l1, l2, l3, b0, b1);
-                }
-                if (FINE) mma<F8>(d, t0, t1, t2, t3, b0, b1);
-            };
+            for (int n2 = 0; n2 < NT / 2; n2++) w[n2].make(x[2 * n2], x[2 * n2 + 1]);
 #pragma unroll
             for (int c2 = 0; c2 < C2; c2++) {
-                uint32_t r[4];
-                ldsm4t(r, at_chunk<ROWB>(vb, 16 * n2 + vr, 2 * c2 + vc));
-                if (F8) {
-                    // chunk 2 c2 (r0, r1) and 2 c2 + 1 (r2, r3), 16 columns each: even ones, odd ones
+                constexpr int M = F8 ? 4 : 2;
+                float d[M][4];
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        uint32_t e0, d0, e1, d1;
-                        e4m3_to_f16(__byte_perm(r[2 * c], 0, 0x3120), e0, d0);
-                        e4m3_to_f16(__byte_perm(r[2 * c + 1], 0, 0x3120), e1, d1);
-                        mma_p(o[2 * (2 * c2 + c)], e0, e1);
-                        mma_p(o[2 * (2 * c2 + c) + 1], d0, d1);
-                    }
-                } else {
-                    mma_p(o[2 * c2], r[0], r[1]);
-                    mma_p(o[2 * c2 + 1], r[2], r[3]);
-                }
+                for (int i = 0; i < M; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
+#pragma unroll
+                for (int n2 = 0; n2 < NT / 2; n2++) values(d, w[n2], at_chunk<ROWB>(vb, 16 * n2 + vr, 2 * c2 + vc));
+#pragma unroll
+                for (int i = 0; i < M; i++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) o[M * c2 + i][k] += d[i][k];
+            }
+        } else {
+#pragma unroll
+            for (int n2 = 0; n2 < NT / 2; n2++) {
+                w[0].make(x[2 * n2], x[2 * n2 + 1]);
+#pragma unroll
+                for (int c2 = 0; c2 < C2; c2++)
+                    values(*reinterpret_cast<float(*)[F8 ? 4 : 2][4]>(&o[(F8 ? 4 : 2) * c2]), w[0],
+                           at_chunk<ROWB>(vb, 16 * n2 + vr, 2 * c2 + vc));
             }
         }
     }
@@ -1192,21 +1233,30 @@ cudaError_t dispatch(int D, bool e4m3, int G, bool f32, F f)
 {
     using std::bool_constant;
     using std::integral_constant;
-    auto rows = [&](auto dp, auto cw, auto f8, auto fine) {
-        return G <= 8 ? f(dp, cw, f8, integral_constant<int, 8>(), fine) : f(dp, cw, f8, integral_constant<int, 16>(), fine);
-    };
-    auto type = [&](auto dp, auto cw) {
-        if (e4m3) return rows(dp, cw, bool_constant<true>(), bool_constant<false>());
-        return f32 ? rows(dp, cw, bool_constant<false>(), bool_constant<true>()) : rows(dp, cw, bool_constant<false>(), bool_constant<false>());
-    };
     using C64 = integral_constant<int, 64>;
     using C96 = integral_constant<int, 96>;
     using C128 = integral_constant<int, 128>;
-    if (D <= 64) return type(C64(), C64());
+    using N8 = integral_constant<int, 8>;
+    using N16 = integral_constant<int, 16>;
+    using E4m3 = bool_constant<true>;
+    using Bf16 = bool_constant<false>;
+    using Fine = bool_constant<true>;
+    using Plain = bool_constant<false>;
+    auto type = [&](auto dp, auto cw, auto f8, auto rows) {
+        return f32 ? f(dp, cw, f8, rows, Fine()) : f(dp, cw, f8, rows, Plain());
+    };
+    if (D <= 64) {
+        if (e4m3) return G <= 8 ? type(C64(), C64(), E4m3(), N8()) : type(C64(), C64(), E4m3(), N16());
+        return G <= 8 ? type(C64(), C64(), Bf16(), N8()) : type(C64(), C64(), Bf16(), N16());
+    }
+    if (!e4m3) return G <= 8 ? type(C128(), C128(), Bf16(), N8()) : type(C128(), C128(), Bf16(), N16());
     // E4M3 rows of up to 96 are computed 96 wide (32 sequences of up to 8000: 45.8 us, 52.7
     // with 128); for bf16, which waits for memory, it makes no difference (71.3, 72.5)
-    if (e4m3 && D <= 96) return rows(C128(), C96(), bool_constant<true>(), bool_constant<false>());
-    return type(C128(), C128());
+    if (D <= 96) return G <= 8 ? type(C128(), C96(), E4m3(), N8()) : type(C128(), C96(), E4m3(), N16());
+    // the order of the finer sums is the faster one for E4M3 rows of 128 and up to 8 heads
+    // (128 sequences of up to 8000: 171 us, 180 without), and the slower one for more heads
+    // (32 sequences: 71 and 66 us) and shorter rows (96: 50.4 and 45.8)
+    return G <= 8 ? f(C128(), C128(), E4m3(), N8(), Fine()) : type(C128(), C128(), E4m3(), N16());
 }
 
 int rows_of(int hq, int hkv)

@@ -77,8 +77,9 @@ def check_attention(pool, q, lens, tab, page, out, lse, scale, softcap=0.0, wind
     4 sqrt(D) 2^-24 of the sum of the products' sizes, times scale, and a
     relative 2^-21 for scaling, tanh cap and exponent (max(1, |s|) of them);
     the weights are off by the same relative amounts, twice (numerator and
-    denominator); weights enter the product with 16 significant bits (2^-17),
-    and n fp32 additions are taken as 4 sqrt(n) 2^-24.  All of it applies to
+    denominator); weights enter the product with 16 significant bits for a bf16
+    output (2^-17), 22 at least for an fp32 one (2^-21), and n fp32 additions are
+    taken as 4 sqrt(n) 2^-24.  All of it applies to
     sum_j p_j |v_j|.  A bf16 output is off by half a step more.
 
     An E4M3 row's weight is w_j = p_j s_j (s_j its scale) times codes c_j, held
@@ -105,7 +106,7 @@ def check_attention(pool, q, lens, tab, page, out, lse, scale, softcap=0.0, wind
             ref, rl, size, prod, big, p = okv.attention(q[b, g], k, v, seen, scale, softcap)
             ds = 4 * np.sqrt(D) * 2.0 ** -24 * prod + 2.0 ** -21 * max(1.0, big)
             sums = 4 * np.sqrt(max(1, n)) * 2.0 ** -24
-            tol = (2 * ds + 2.0 ** -16 + sums)[:, None] * size + 1e-37
+            tol = (2 * ds + (2.0 ** -16 if out_bf16 else 2.0 ** -20) + sums)[:, None] * size + 1e-37
             if pool.ks is not None and p.size:
                 f = np.concatenate([okv.scale_of(pool.vs[i, h]) if i is not None else np.zeros(page) for i in ids])[:n][seen]
                 codes = np.abs(v[seen] / f[:, None]).sum(0)

@@ -86,6 +86,45 @@ def test_long_caches_are_split_and_joined(lens, kv):
     _run(lens, 8, 2, 128, 64, kv)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,D", [(8, 128), (32, 64)])
+def test_fp32_outputs_of_long_rows_do_not_drift(hq, D, kv):
+    """Rows of 6000 keys that one warp sums nearly alone (more rows than the
+    machine has warps), against fp64 on the device.
+
+    Bound on a row's relative norm: scores off by sqrt(D) 2^-24 of the products'
+    size (scale sum |q k| is about 1.5 sqrt(D) 2 / pi < 11 here) and 2^-21, twice; weights
+    2^-21; the tiles' sums added to the row's, 188 roundings at most, sqrt(188) 2^-24:
+    below 2^-18 in all, where sums cut to 24 bits at every product of 16 keys
+    would drift by up to 375 * 2^-24 = 2^-15.4."""
+    B, n, hkv, page = 160, 6000, 8, 64
+    row = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(D + hq)
+    pages = 200                                                      # all sequences share them, in different orders
+    k, v = (torch.randn((pages, hkv, page, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    v = v + 1.0                                                      # sums that grow
+    tab = torch.stack([torch.randperm(pages, generator=g, device="cuda")[:row] for _ in range(B)]).to(torch.int32)
+    q = (1.5 * torch.randn((B, hq, D), generator=g, device="cuda")).to(torch.bfloat16)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    if kv == "bf16":
+        pool, kd, vd = moe.kv_pool(k, v), k.double(), v.double()
+    else:
+        kc, vc = k.float().to(torch.float8_e4m3fn), v.float().to(torch.float8_e4m3fn)
+        s = torch.full((pages, hkv, page), 127, dtype=torch.uint8, device="cuda")
+        pool, kd, vd = moe.kv_pool(kc, vc, s, s), kc.double(), vc.double()
+    out = torch.empty((B, hq, D), dtype=torch.float32, device="cuda")
+    with handle(hq, hkv, D, page, pages, B, row, kv, "f32") as h:
+        moe.moe_attn_decode(h, pool, q, lens, tab, B, out)
+        assert moe.moe_kv_status(h) == moe.MOE_OK
+    worst = 0.0
+    for b in range(0, B, 7):
+        kb, vb = (x[tab[b].long()].transpose(0, 1).reshape(hkv, -1, D)[:, :n] for x in (kd, vd))
+        z = q[b].double().view(hkv, hq // hkv, D) @ kb.transpose(1, 2) / D ** 0.5
+        ref = (torch.softmax(z, -1) @ vb).view(hq, D)
+        worst = max(worst, float(((out[b].double() - ref).norm(dim=-1) / ref.norm(dim=-1)).max()))
+    assert worst <= 2.0 ** -18, worst
+
+
 @pytest.mark.parametrize("hq", [8, 16])
 def test_many_short_sequences(hq):
     _run([(i * 37) % 50 for i in range(300)], hq, 2, 64, 16)
