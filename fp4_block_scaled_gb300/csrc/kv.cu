@@ -105,8 +105,20 @@ struct Span {
         : lo((const char*)p), hi(p ? lo + ((size_t)(T - 1) * ld + (size_t)heads * D) * 2 : lo)
     {
     }
+    Span(const void* p, size_t bytes) : lo((const char*)p), hi(p ? lo + bytes : lo) {}
     bool overlaps(const Span& o) const { return lo < o.hi && o.lo < hi; }
 };
+
+// Whether a token of x (`heads` heads of D, every ld elements) may share an
+// element with one of y.  Parts of one projection's rows interleave: with one
+// stride they are apart if they are so within a row.
+bool clash(const Span& x, int hx, long long ldx, const Span& y, int hy, long long ldy, int D)
+{
+    if (!x.overlaps(y)) return false;
+    if (ldx != ldy) return true;
+    const long long off = ((y.lo - x.lo) / 2 % ldx + ldx) % ldx;       // where y's part of a row begins, from x's
+    return off < (long long)hx * D || off + (long long)hy * D > ldx;
+}
 
 constexpr int kMaxTokens = 1 << 24;     // of one moe_rope or moe_kv_append call
 
@@ -248,13 +260,13 @@ int moe_rope(moe_kv_t h, const moe_rope_desc* rope, const int32_t* pos, int T, c
     a.ldq_out = q == q_out ? lq : (long long)c.num_q_heads * c.head_dim;
     a.ldk_out = k == k_out ? lk : (long long)c.num_kv_heads * c.head_dim;
     a.sms = h->sms;
-    // an output overlaps no input but the one it is; rows of one projection
-    // rotated in place interleave, and are told apart by their first elements
+    // an output overlaps no input but the one it is
     const Span sq(q, lq, a.hq, a.D, T), sk(k, lk, a.hk, a.D, T);
     const Span oq(q_out, a.ldq_out, a.hq, a.D, T), ok(k_out, a.ldk_out, a.hk, a.D, T);
     if (q != q_out && (oq.overlaps(sq) || oq.overlaps(sk))) return MOE_ERR_INVALID_ARG;
     if (k != k_out && (ok.overlaps(sk) || ok.overlaps(sq))) return MOE_ERR_INVALID_ARG;
     if (q && k && (q != q_out || k != k_out) && oq.overlaps(ok)) return MOE_ERR_INVALID_ARG;
+    if ((q == q_out || k == k_out) && clash(sq, a.hq, lq, sk, a.hk, lk, a.D)) return MOE_ERR_INVALID_ARG;
     KvGuard guard(h->device);
     return cuda_rc(launch_rope(a, (cudaStream_t)stream));
 }
@@ -311,6 +323,8 @@ int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long 
     a.sms = h->sms;
     const Span sq(q, lq, a.hq, a.D, T), sk(k, lk, a.hk, a.D, T), sv(v, lv, a.hv, a.D, T), oq(q_out, a.ldq_out, a.hq, a.D, T);
     if (q && q != q_out && (oq.overlaps(sq) || oq.overlaps(sk) || oq.overlaps(sv))) return MOE_ERR_INVALID_ARG;
+    if (q && q == q_out && (clash(sq, a.hq, lq, sk, a.hk, lk, a.D) || clash(sq, a.hq, lq, sv, a.hv, lv, a.D)))
+        return MOE_ERR_INVALID_ARG;
     KvGuard guard(h->device);
     return cuda_rc(launch_rope(a, (cudaStream_t)stream));
 }
@@ -319,15 +333,19 @@ int moe_attn_decode(moe_kv_t h, const moe_kv_pool* pool, const void* q, const in
                     const int32_t* page_table, int B, float scale, float softcap, int window, void* out, float* lse,
                     void* stream)
 {
-    if (!h || B < 0 || B > h->cfg.max_seqs || window < 0 || !isfinite(scale) || !isfinite(softcap) || softcap < 0.0f)
+    if (!h || B < 0 || B > h->cfg.max_seqs || window < 0 || !(fabsf(scale) <= 0x1p32f) ||
+        (softcap != 0.0f && !(softcap >= 0x1p-32f && softcap <= 0x1p32f)))
         return MOE_ERR_INVALID_ARG;
     const int rc = check_pool(h, pool);
     if (rc) return rc;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
         return MOE_ERR_INVALID_ARG;
     if (B == 0) return MOE_OK;
-    if (!q || !seq_lens || !page_table || !out || q == out) return MOE_ERR_INVALID_ARG;
+    if (!q || !seq_lens || !page_table || !out) return MOE_ERR_INVALID_ARG;
     const moe_kv_config& c = h->cfg;
+    const size_t heads = (size_t)B * c.num_q_heads, n = heads * c.head_dim;
+    const Span sq(q, n * 2), so(out, n * (c.out_dtype == MOE_OUT_F32 ? 4 : 2)), sl(lse, heads * 4);
+    if (so.overlaps(sq) || sl.overlaps(sq) || sl.overlaps(so)) return MOE_ERR_INVALID_ARG;
     AttnArgs a{};
     a.pool = pool_of(*pool);
     a.q = (const uint16_t*)q;

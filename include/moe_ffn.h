@@ -526,7 +526,8 @@ int moe_rope_table(int rot_dim, double base, int kind, double factor, int traine
  *   q_out    device bf16 [T][Hq][D], contiguous -- or q itself, rotated in
  *            place with the stride ldq; k_out likewise
  * A stride is 0 or a multiple of 8 that holds a token's heads.  An output may
- * overlap no input other than by being it. */
+ * overlap no input other than by being it; a tensor rotated in place and
+ * another that lies between its rows have one stride. */
 int moe_rope(moe_kv_t h, const moe_rope_desc* rope, const int32_t* pos, int T, const void* q, long long ldq,
              void* q_out, const void* k, long long ldk, void* k_out, void* stream);
 
@@ -560,13 +561,15 @@ int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long 
  *   page_table device int32; row b is sequence b's
  *   out        device [B][Hq][D], bf16 or fp32 per cfg.out_dtype
  *   lse        device fp32 [B][Hq], or NULL
- *   scale      finite; 0: 1 / sqrt(D).  softcap >= 0 and finite (0: none);
- *              window >= 0
+ *   scale      within +-2^32; 0: 1 / sqrt(D).  softcap 0 (none) or 2^-32 ..
+ *              2^32; window >= 0
+ * out and lse overlap neither each other nor q.
  * Scores, softmax and sums are fp32; the weights enter the product with v as
  * 16-bit terms: 16 significant bits for a bf16 output, 24 for an fp32 one
  * (E4M3: the weight times v's scale, to 2^-21 of itself or 2^-31 of the
  * sequence's largest).  A key or value that is not finite
- * makes the outputs it enters not finite; pool contents outside the keys
+ * makes the outputs it enters not finite, but a score of -inf is a weight of
+ * zero (of all keys: as no keys); pool contents outside the keys
  * above are never used, whatever they are.  A page id outside
  * [0, num_pages) sets MOE_ERR_BAD_INDEX and its keys are left out; so does a
  * length below 0 (taken as 0) or above the row's capacity (taken as that).

@@ -263,6 +263,59 @@ def test_refusals():
         assert moe.moe_kv_status(h) == moe.MOE_OK
 
 
+def test_refuses_overlaps_and_extreme_factors():
+    B, hq, hkv, D, page = 2, 4, 2, 64, 16
+    lens, tab = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((B,), (B, 1)))
+    p = torch.zeros(1, hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    n = B * hq * D * 2                              # bytes of q; out takes twice that, lse 32
+    at = torch.zeros(8 * n, dtype=torch.uint8, device="cuda").data_ptr() + 2 * n
+    with handle(hq, hkv, D, page, 1, B, 1) as h:
+        def run(q, o, lse=None, **kw):
+            moe.moe_attn_decode(h, moe.kv_pool(p, p), at + q, lens, tab, B, at + o, None if lse is None else at + lse, **kw)
+
+        def refused(*a, **kw):
+            with pytest.raises(moe.MoeError) as e:
+                run(*a, **kw)
+            assert e.value.code == moe.MOE_ERR_INVALID_ARG, (a, kw)
+        refused(0, n - 16), refused(2 * n - 16, 0), refused(0, -2 * n + 16)
+        refused(0, n, lse=n - 16), refused(0, n, lse=3 * n - 16), refused(0, n, lse=-16)
+        for kw in dict(scale=2.0 ** 33), dict(scale=-2.0 ** 33), dict(softcap=2.0 ** -33), dict(softcap=2.0 ** 33), dict(scale=1e300):
+            refused(0, n, **kw)
+        run(0, n, lse=3 * n), run(2 * n, 0, lse=3 * n), run(0, n, lse=-32)
+        run(0, n, scale=2.0 ** 32, softcap=2.0 ** -32), run(0, n, scale=-2.0 ** 32, softcap=2.0 ** 32)
+        assert moe.moe_kv_status(h) == moe.MOE_OK
+
+
+def test_keys_whose_score_is_minus_infinity_weigh_nothing():
+    """q of ones against keys with one element of -inf: those keys alone drop
+    out; a sequence of none other ends like one without keys."""
+    hq, hkv, D, page = 4, 2, 64, 16
+    rng = np.random.default_rng(5)
+    lens = np.array([40, 5], np.int32)
+    p = Pool(4, hkv, page, D, "bf16", rng)
+    tab = np.array([[0, 1, 2], [3, -1, -1]], np.int32)
+    keep = np.ones((4, page), bool)
+    for page_id, off in (0, 0), (0, 7), (1, 15), (2, 3):
+        keep[page_id, off] = False
+    keep[3, :5] = False
+    i, off = np.nonzero(~keep)
+    p.k[i, :, off, 9] = np.int16(-128)                               # 0xFF80, -inf
+    p.upload()
+    q = torch.ones(2, hq, D, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.empty(2, hq, D, device="cuda"), torch.empty(2, hq, device="cuda")
+    with handle(hq, hkv, D, page, 4, 2, 3) as h:
+        moe.moe_attn_decode(h, p.struct, q, torch.from_numpy(lens).cuda(), torch.from_numpy(tab).cuda(), 2, o, lse=lse)
+        assert moe.moe_kv_status(h) == moe.MOE_OK
+    assert not o[1].any() and torch.isneginf(lse[1]).all()
+    # the same sequence with those keys taken out
+    rows = [(int(tab[0, j // page]), j % page) for j in range(40)]
+    rows = [r for r in rows if keep[r]]
+    c = Pool(4, hkv, page, D, "bf16", rng)
+    for j, (i, off) in enumerate(rows):
+        c.k[j // page, :, j % page], c.v[j // page, :, j % page] = p.k[i, :, off], p.v[i, :, off]
+    check_attention(c, np.ones((1, hq, D)), [len(rows)], np.array([[0, 1, 2]], np.int32), page, f64(o[:1]), f64(lse[:1]), D ** -0.5)
+
+
 def test_allocation_failure_and_next_call():
     moe.moe_ffn_test_fail_allocs(1)
     try:

@@ -256,6 +256,43 @@ def test_append_bad_places_are_left_out_and_reported():
         _check_rope(f64(qo), f64(x[0]), pos, f, m, "half")
 
 
+def test_in_place_beside_other_parts_of_the_rows():
+    """q in place: k and v may lie between its rows, with its stride, and nowhere on them."""
+    T, hq, hkv, D, page = 3, 4, 2, 64, 16
+    desc, keep, _, _ = _desc(64, "half")
+    ld = (hq + 2 * hkv) * D
+    x = torch.zeros(2 * T * ld, dtype=torch.bfloat16, device="cuda")
+    at = lambda e: x.data_ptr() + 2 * e                               # noqa: E731
+    other = torch.zeros(T, hkv, D, dtype=torch.bfloat16, device="cuda")
+    pos, seq = (torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2))
+    pos += torch.arange(T, device="cuda", dtype=torch.int32)
+    tab = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    p = torch.zeros(2, 1, hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    good = moe.kv_pool(p[0], p[1])
+    with handle(hq, hkv, D, page, 1, 2, 1) as h:
+        def rope(k, ldk, T=T, q=0):
+            moe.moe_rope(h, desc, pos, T, q=at(q), q_out=at(q), ldq=ld, k=k, k_out=k, ldk=ldk)
+
+        def append(k, v, ldk, ldv):
+            moe.moe_kv_append(h, good, k, v, pos, tab, T, seq=seq, rope=desc, q=at(0), q_out=at(0), ldq=ld, ldk=ldk, ldv=ldv)
+
+        def refused(f, *a, **kw):
+            with pytest.raises(moe.MoeError) as e:
+                f(*a, **kw)
+            assert e.value.code == moe.MOE_ERR_INVALID_ARG, a
+        end = ld - hkv * D
+        for k, ldk in (at(0), ld), (at(hq * D - 8), ld), (at(hq * D), ld - 8), (at(end + 8), ld), (at(ld), ld):
+            refused(rope, k, ldk)
+            refused(append, k, other, ldk, 0)
+            refused(append, other, k, 0, ldk)
+        refused(rope, at(hq * D - 8), ld, T=1)
+        refused(rope, at(0), ld, q=hkv * D - 8)
+        rope(at(hq * D), ld), rope(at(end), ld), rope(at(T * ld), hkv * D), rope(at(0), ld, q=hkv * D)
+        rope(at(hq * D), hkv * D, T=1)
+        append(at(hq * D), at(end), ld, ld), append(at(T * ld), at(T * ld), 0, 0)
+        assert moe.moe_kv_status(h) == moe.MOE_OK
+
+
 def test_append_refusals():
     T, hq, hkv, D, page = 3, 4, 2, 64, 16
     desc, keep, _, _ = _desc(64, "half")
