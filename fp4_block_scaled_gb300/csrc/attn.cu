@@ -217,6 +217,7 @@ struct SplitArgs {
     AttnArgs a;
     int G, chunks, R;           // query heads per key head, groups of NROW of them, rows per sequence
     int ps_shift;               // log2 of the page size, -1 if it is no power of two
+    int pair_shift;             // 2^it pairs of heads hold a row's
     float* frags;               // [grid][kWarps] parts
     float* parts;               // [grid][2] parts
     int* tickets;               // [max_seqs * R], zero between launches
@@ -268,7 +269,7 @@ struct Kernel {
     __device__ __forceinline__ void load_q(const SplitArgs& s, int b, int row, int lane)
     {
         const int g = lane >> 2, j = lane & 3, D = s.a.D;
-        const int h = row / s.chunks, c = row - h * s.chunks;
+        const int h = s.chunks == 1 ? row : row / s.chunks, c = row - h * s.chunks;
 #pragma unroll
         for (int half = 0; half < NROW / 8; half++) {
             const int hg = c * NROW + g + 8 * half;
@@ -613,7 +614,7 @@ struct Kernel {
     __device__ __forceinline__ void store_out(const SplitArgs& s, int b, int row, int lane) const
     {
         const int g = lane >> 2, j = lane & 3;
-        const int h = row / s.chunks, c = row - h * s.chunks;
+        const int h = s.chunks == 1 ? row : row / s.chunks, c = row - h * s.chunks;
 #pragma unroll
         for (int half = 0; half < NROW / 8; half++) {
             const int hg = c * NROW + g + 8 * half;
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t s_warp[kWarps];
     __shared__ Frag s_frag[2 * kWarps];
-    __shared__ int s_first[2], s_c0[2], s_count[2];
+    __shared__ int s_first[2], s_count[2];
     uint8_t* ring = smem;
     uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kWarps * K::REGION);   // [B + 1]
     int* slen = reinterpret_cast<int*>(pre + s.a.B + 1);                               // [B]
@@ -827,9 +828,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         const int first = s.a.window > 0 ? max(0, n - s.a.window) : 0;
         return (uint32_t)max(1, (n + TT - 1) / TT - first / TT);
     };
-    auto scan = [&](uint32_t x) {
+    auto scan = [&](uint32_t x) {               // over B lanes, if they are fewer than a warp's
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
+            if (d >= B) break;
             const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
             if (lane >= d) x += y;
         }
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         const uint32_t x = scan(tiles_of(lane));
         if (lane < B) pre[lane + 1] = x;
         if (lane == 0) pre[0] = 0;
-        base = __shfl_sync(0xFFFFFFFFu, x, 31);
+        base = __shfl_sync(0xFFFFFFFFu, x, B - 1);
         __syncwarp();
     } else {
         for (int i0 = 0; i0 < B; i0 += kThreads) {
@@ -1128,26 +1130,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         if (!((starts >> f) & 1)) open[0] = f;
         if (((starts >> l) & 1) && !((ends >> last_of(l)) & 1)) open[1] = l;
     }
-    // first the weights, a thread a head of a row (and the last two threads find
-    // the CTAs that hold the open rows); then the sums, a warp two heads
+    // first the weights, a thread a head of a row; then the sums, a warp two heads
     for (int i = tid; i < 2 * kWarps * heads_in; i += kThreads)
         if ((heads >> (i % (2 * kWarps))) & 1) K::weigh(members(i % (2 * kWarps)), near, i % (2 * kWarps), i / (2 * kWarps), tab);
-    if (tid >= kThreads - 2) {
-        const int slot = tid - (kThreads - 2), f = open[slot];
-        s_first[slot] = -1;
-        if (f >= 0) {
-            const uint32_t tiles = pre[s_frag[f].b + 1] - pre[s_frag[f].b];
-            const uint32_t r0 = units_before(s_frag[f].b) + (uint32_t)s_frag[f].row * (tiles + V) + V;
-            s_c0[slot] = (int)cta_of(r0);
-            s_count[slot] = (int)cta_of(r0 + tiles - 1) - s_c0[slot] + 1;
-        }
-    }
     __syncthreads();
-    const int pairs = (heads_in + 1) / 2;
-    for (int e = warp; e < __popc(heads) * pairs; e += kWarps) {
+    for (int e = warp; e < __popc(heads) << s.pair_shift; e += kWarps) {
+        const int g = 2 * (e & ((1 << s.pair_shift) - 1));
+        if (g >= heads_in) continue;
         unsigned rest = heads;
-        for (int i = e / pairs; i > 0; i--) rest &= rest - 1;
-        const int f = __ffs(rest) - 1, last = last_of(f), g = e % pairs * 2;
+        for (int i = e >> s.pair_shift; i > 0; i--) rest &= rest - 1;
+        const int f = __ffs(rest) - 1, last = last_of(f);
         const int slot = (starts >> f) & 1;
         const bool whole = slot && ((ends >> last) & 1);
         const unsigned mem = members(f);
@@ -1188,16 +1180,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
 
     // Rows that other CTAs hold parts of, too: the last CTA to finish joins them.
     __syncthreads();
-    if (tid < 2 && open[tid] >= 0) {
-        // the CTA's part was written before the barrier; its release and the
-        // others' acquisition are the ticket's
-        int* ticket = s.tickets + (size_t)s_frag[open[tid]].b * s.R + s_frag[open[tid]].row;
-        int old;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
-        if (old == s_count[tid] - 1) {
-            *ticket = 0;
-            s_first[tid] = s_c0[tid];
+    if (tid < 2) {
+        const int f = tid ? open[1] : open[0];
+        int first = -1, count = 0;
+        if (f >= 0) {
+            // the CTA's part was written before the barrier; its release and the
+            // others' acquisition are the ticket's
+            const int b = s_frag[f].b, row = s_frag[f].row;
+            int* ticket = s.tickets + (size_t)b * s.R + row;
+            int old;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+            // meanwhile, the CTAs that hold the row
+            const uint32_t tiles = pre[b + 1] - pre[b], r0 = units_before(b) + (uint32_t)row * (tiles + V) + V;
+            const int c0 = (int)cta_of(r0);
+            count = (int)cta_of(r0 + tiles - 1) - c0 + 1;
+            if (old == count - 1) {
+                *ticket = 0;
+                first = c0;
+            }
         }
+        s_first[tid] = first;
+        s_count[tid] = count;
     }
     __syncthreads();
     for (int e = warp; e < 2 * heads_in; e += kWarps) {
@@ -1298,6 +1301,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st)
     s.chunks = s.G <= 8 ? 1 : (s.G + 15) / 16;
     s.R = a.hkv * s.chunks;
     s.ps_shift = a.page_size & (a.page_size - 1) ? -1 : __builtin_ctz((unsigned)a.page_size);
+    s.pair_shift = s.G <= 2 ? 0 : s.G <= 4 ? 1 : s.G <= 8 ? 2 : 3;
     const AttnWorkspace w = attn_workspace(a.max_seqs, a.hq, a.hkv, a.D, a.sms);
     s.tickets = reinterpret_cast<int*>(a.ws + w.tickets);
     s.frags = reinterpret_cast<float*>(a.ws + w.frags);
