@@ -17,20 +17,20 @@
 // warp streams its tiles through a ring of its own in shared memory (cp.async,
 // 16 bytes a lane, two of three 8 KB tiles in flight: 128 KB an SM), with no
 // barrier between warps, and fetches ahead what a tile's address needs (the
-// page ids of the next 32 tiles) and what the next row begins with (its
-// queries).  The products are mma.sync m16n8k16, which are busy 14 to 31 % of the
-// time: a tile of one token's 8 query heads fills half of an MMA's 16 rows (the
-// other half carries the weights' low terms), and a tcgen05 MMA would want 128
-// keys in one place and a round trip through tensor memory per tile for the
-// same bytes.
+// page ids of the next 32 tiles; prefetching the next row's queries too gains
+// nothing, and its instructions cost one sequence 0.1 us).  The products are
+// mma.sync m16n8k16, which are busy 14 to 31 % of the time: a tile of one
+// token's 8 query heads fills half of an MMA's 16 rows (the other half carries
+// the weights' low terms), and a tcgen05 MMA would want 128 keys in one place and
+// a round trip through tensor memory per tile for the same bytes.
 //
 // Measured (GPU time, back to back; 6783 GB/s is the rate of a plain copy):
 //   64 sequences of up to 8000 keys, 8 x 128, bf16:   164 us, 6.43 TB/s
 //   2 of up to 131071:                                138 us, 6.45 TB/s
 //   128 of up to 8000, E4M3, 8 query heads a key head: 175 us, 5.94 TB/s
 //   48 windows of 1000 keys, 16 x 64, capped scores:   37 us, 4.65 TB/s
-//   one sequence of 1000 keys:                        8.2 us (a launch takes 2.1;
-//     then lengths, page ids, keys, the ticket and the join: five round trips)
+//   one sequence of 1000 keys:                        8.0 us (of 16: 4.7; a launch
+//     takes 2.1; then lengths, page ids, keys, the ticket and the join: five round trips)
 // While the rings are full the SMs take in 25 bytes a cycle each, the memory's
 // rate; what is lost is 3.4 us before them, the tenth by which SMs with a
 // slower way to memory end later than others (dealing out the last eighth of
@@ -983,13 +983,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
                 } else if (pp.b + 1 < B) {
                     fetch(pp.b + 1, first_key(pp.b + 1) / TT);
                 }
-            }
-            if (pp.t == 0 && up != u) {         // a row begins: its queries, for when the warp gets there
-                const int h = s.chunks == 1 ? pp.row : pp.row / s.chunks, g0 = (pp.row - h * s.chunks) * NROW;
-                const int bytes = min(NROW, s.G - g0) * s.a.D * 2;
-                if (lane * 128 < bytes)
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(
-                        reinterpret_cast<const uint8_t*>(s.a.q + ((size_t)pp.b * s.a.hq + h * s.G + g0) * s.a.D) + lane * 128));
             }
             const uint32_t st = my32 + stage * K::STAGE;
             const int h = s.chunks == 1 ? pp.row : pp.row / s.chunks;
