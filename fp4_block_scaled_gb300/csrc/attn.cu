@@ -5,7 +5,8 @@
 // key head, group of up to NROW query heads); the rows' tiles in order are one
 // line, and every warp of the grid takes an equal stretch of it, so the split
 // along the cache follows the lengths by itself: a long sequence spreads over
-// many warps, short ones share one.  A warp keeps the running maximum and sum
+// many warps, short ones share one (where warps would idle, short rows are kept in
+// one CTA instead).  A warp keeps the running maximum and sum
 // of the softmax and its output rows in registers while it stays in a row
 // (softmax(s)_j v_j summed with weights 2^(s_j - m), rescaled when m moves), and
 // writes the rows that lie inside its stretch itself.  What is left of a row
@@ -29,7 +30,7 @@
 //   2 of up to 131071:                                138 us, 6.45 TB/s
 //   128 of up to 8000, E4M3, 8 query heads a key head: 175 us, 5.94 TB/s
 //   48 windows of 1000 keys, 16 x 64, capped scores:   37 us, 4.65 TB/s
-//   one sequence of 1000 keys:                        8.0 us (of 16: 4.7; a launch
+//   one sequence of 1000 keys:                        7.9 us (of 16: 4.2, 100: 5.4; a launch
 //     takes 2.1; then lengths, page ids, keys, the ticket and the join: five round trips)
 // While the rings are full the SMs take in 25 bytes a cycle each, the memory's
 // rate; what is lost is 3.4 us before them, the tenth by which SMs with a
@@ -206,6 +207,18 @@ __device__ __forceinline__ uint32_t at_chunk(uint32_t base, int r, int c)
 // warps would idle splitting wins: one E4M3 sequence of 100 keys 6.7 us, 9.7 whole.
 constexpr int kWhole = 128;
 constexpr int kShort = 16;
+
+// A join across CTAs takes 2.3 us, so where CTAs would idle, rows of up to this many
+// tiles have one to themselves: 32 (E4M3, whose tiles take twice the instructions:
+// 16), and twice that where more than half the CTAs have a row anyway (8 key heads
+// of 128, bf16, sequences x keys, without and with it: 1 x 100 7.8 and 5.3 us,
+// 1 x 512 7.8 and 7.7, 8 x 500 9.1 and 8.0, 16 x 600 14.4 and 11.5, 18 x 1000 20.5 and
+// 17.2; beyond it, 1 x 600 would take 8.4 for 7.7 and one E4M3 sequence of 1000 11.6
+// for 8.9; ragged batches gain less, 16 of up to 1000 11.7 and 11.1, or lose, 10 of
+// up to 1000 10.1 and 10.8).  More rows than CTAs: see snap (20 x 100 8.7 and 7.9, 40 x 48
+// 8.9 and 7.3, 30 x 30, which had no join, 6.0 and 6.2).  The choice costs a line that
+// is full 0.2 us (1 x 3000: 9.0 and 9.2).
+__device__ __forceinline__ uint32_t one_cta_tiles(bool f8, uint32_t rows) { return (f8 ? 16u : 32u) << (2 * rows > gridDim.x ? 1 : 0); }
 
 // What a row itself (queries, output, places) costs a warp, in tiles, when the
 // line is shared out: without it the warps with many short rows end last (128
@@ -796,6 +809,13 @@ struct Frag {
     int from_start, to_end;     // the part holds the row's first tile, its last tile
 };
 
+// A CTA's sequence, where every row has CTAs of its own: the tiles and the CTAs of
+// each of its rows, and the CTAs before its first.
+struct Apart {
+    int b;
+    uint32_t tiles, ctas, before;
+};
+
 // A place on the line of tiles.
 struct Place {
     int b, row, t, tiles;
@@ -807,7 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
     using K = Kernel<DP, CW, F8, NROW, FINE>;
     constexpr int TT = K::TT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t s_warp[kWarps];
+    __shared__ uint32_t s_warp[2][kWarps];
+    __shared__ Apart s_own;
+    __shared__ int s_apart[2];                  // apart: the first of this row's CTAs and their number, else -1
     __shared__ Frag s_frag[2 * kWarps];
     __shared__ int s_first[2], s_count[2];
     uint8_t* ring = smem;
@@ -837,61 +859,131 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         }
         return x;
     };
+    // Few rows: CTAs of their own, one for a row of up to one_cta tiles, else one for
+    // every kWarps tiles; `own` is this CTA's sequence.
+    const uint32_t R = (uint32_t)s.R, one_cta = one_cta_tiles(F8, (uint32_t)B * R);
+    auto ctas_of = [&](uint32_t tiles) { return tiles <= one_cta ? min(tiles, 1u) : (tiles + kWarps - 1) / kWarps; };
+    bool apart = false;
+    uint32_t ctas = 0;          // of all rows
+    Apart own = {};
     if (B <= 32) {              // every warp by itself, all writing the same
-        const uint32_t x = scan(tiles_of(lane));
+        const uint32_t mine = tiles_of(lane), x = scan(mine), n = ctas_of(mine), y = scan(n);
         if (lane < B) pre[lane + 1] = x;
         if (lane == 0) pre[0] = 0;
         base = __shfl_sync(0xFFFFFFFFu, x, B - 1);
+        ctas = __shfl_sync(0xFFFFFFFFu, y, B - 1) * R;
+        apart = ctas <= gridDim.x;
+        if (apart) {
+            own.b = min(__popc(__ballot_sync(0xFFFFFFFFu, lane < B && y * R <= blockIdx.x)), B - 1);
+            own.tiles = __shfl_sync(0xFFFFFFFFu, mine, own.b);
+            own.ctas = __shfl_sync(0xFFFFFFFFu, n, own.b);
+            own.before = (__shfl_sync(0xFFFFFFFFu, y, own.b) - own.ctas) * R;
+        }
         __syncwarp();
     } else {
+        const bool few = (uint32_t)B * R <= gridDim.x;          // so that B < kThreads
         for (int i0 = 0; i0 < B; i0 += kThreads) {
-            const uint32_t x = scan(tiles_of(i0 + tid));
-            if (lane == 31) s_warp[warp] = x;
+            const uint32_t mine = tiles_of(i0 + tid), n = ctas_of(mine), x = scan(mine), y = few ? scan(n) : 0u;
+            if (lane == 31) {
+                s_warp[0][warp] = x;
+                s_warp[1][warp] = y;
+            }
             __syncthreads();
-            uint32_t before = base, all = base;
+            uint32_t before = base, all = base, ctas_before = 0;
+            ctas = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; w++) {
-                if (w < warp) before += s_warp[w];
-                all += s_warp[w];
+                if (w < warp) {
+                    before += s_warp[0][w];
+                    ctas_before += s_warp[1][w];
+                }
+                all += s_warp[0][w];
+                ctas += s_warp[1][w];
             }
             if (i0 + tid < B) pre[i0 + tid + 1] = before + x;
             base = all;
+            ctas *= R;
+            apart = few && ctas <= gridDim.x;
+            const uint32_t end = (ctas_before + y) * R, begin = end - n * R;
+            if (apart && begin <= blockIdx.x && blockIdx.x < end) s_own = Apart{tid, mine, n, begin};
             __syncthreads();
         }
         if (tid == 0) pre[0] = 0;
         __syncthreads();
+        if (apart && blockIdx.x < ctas) own = s_own;
     }
     // The line in units: a row's tiles, and kRowCost for the row itself where warps
     // have several rows.  The CTAs' stretches are equal to one unit, and the warps'
     // within them; fewer CTAs where they would not have a tile for every warp.
-    const uint32_t R = (uint32_t)s.R, tiles_all = base * R;
-    const bool full = tiles_all >= gridDim.x * kWarps;
+    const uint32_t tiles_all = base * R;
+    const bool full = !apart && tiles_all >= gridDim.x * kWarps;
     const uint32_t V = full ? kRowCost : 0, W = tiles_all + V * (uint32_t)B * R;
-    const uint32_t grid = min(gridDim.x, (W + kWarps - 1) / kWarps);
+    const uint32_t grid = apart ? ctas : min(gridDim.x, (W + kWarps - 1) / kWarps);
     if (blockIdx.x >= grid) return;
-    const uint32_t wq = W / grid, wr = W - wq * grid;
-    const uint32_t mine = wq + (blockIdx.x < wr ? 1u : 0u), per = mine / kWarps, left = mine % kWarps;
-    const uint32_t from = blockIdx.x * wq + min((uint32_t)blockIdx.x, wr) + warp * per + min((uint32_t)warp, left);
-    const uint32_t to = from + per + ((uint32_t)warp < left ? 1u : 0u);
+    // a / b; of small numbers (a line that is not full has below 2^14 units) by way
+    // of floats: (a + 1/2) / b is 1 / 2b or more from an integer, and off by far less
+    auto div = [&](uint32_t a, uint32_t b) {
+        return full ? a / b : (uint32_t)__fdividef((float)a + 0.5f, (float)b);
+    };
+    const uint32_t wq = div(W, grid), wr = W - wq * grid;
     auto cta_of = [&](uint32_t at) { return at < wr * (wq + 1) ? at / (wq + 1) : wr + (at - wr * (wq + 1)) / wq; };
     auto units_before = [&](int b) { return (pre[b] + V * (uint32_t)b) * R; };
+    auto seq_of = [&](uint32_t at) {            // the last sequence that begins at or before `at`
+        if (B <= 32) return __popc(__ballot_sync(0xFFFFFFFFu, lane < B - 1 && units_before(lane + 1) <= at));
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (units_before(mid) <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    // A CTA's stretch; where warps would idle it does not begin or end inside a
+    // row of up to one_cta tiles, but at its end (cta_of still holds for longer rows).
+    auto snap = [&](uint32_t at) {
+        if (at >= W) return at;
+        const int b = seq_of(at);
+        const uint32_t tiles = pre[b + 1] - pre[b], in = at - units_before(b), t = in - div(in, tiles) * tiles;
+        return tiles <= one_cta && t ? at + tiles - t : at;
+    };
+    Place begin = {};
+    uint32_t lo, hi, row0 = 0;
+    if (apart) {
+        const uint32_t in = blockIdx.x - own.before, row = div(in, own.ctas);
+        const uint32_t piece = in - row * own.ctas;
+        if (tid == 0) {
+            s_apart[0] = (int)(blockIdx.x - piece);
+            s_apart[1] = (int)own.ctas;
+        }
+        row0 = pre[own.b] * R + row * own.tiles;
+        lo = row0 + piece * kWarps;
+        hi = own.ctas == 1 ? row0 + own.tiles : min(lo + kWarps, row0 + own.tiles);
+        begin.b = own.b;
+        begin.row = (int)row;
+        begin.tiles = (int)own.tiles;
+    } else {
+        if (tid == 0) s_apart[0] = -1;
+        lo = blockIdx.x * wq + min((uint32_t)blockIdx.x, wr);
+        hi = lo + wq + (blockIdx.x < wr ? 1u : 0u);
+        if (!full) {
+            lo = snap(lo);
+            hi = snap(hi);
+        }
+    }
+    const uint32_t per = (hi - lo) / kWarps, left = (hi - lo) % kWarps;
+    const uint32_t from = lo + warp * per + min((uint32_t)warp, left);
+    const uint32_t to = from + per + ((uint32_t)warp < left ? 1u : 0u);
 
     // The place where a stretch that ends or begins at unit `at` is cut, and the
     // tiles before it.  The units of the row itself come first and hold no tile; a
     // cut inside a row that is not split moves to its end.
     const bool whole_rows = full && base <= (uint32_t)B * kShort;
     auto cut = [&](uint32_t at, uint32_t& tiles) {
-        int lo = 0, hi = B - 1;
-        while (lo < hi) {                       // the last sequence that begins at or before `at`
-            const int mid = (lo + hi + 1) >> 1;
-            if (units_before(mid) <= at) lo = mid;
-            else hi = mid - 1;
-        }
         Place p;
-        p.b = lo;
-        p.tiles = (int)(pre[lo + 1] - pre[lo]);
-        const uint32_t units = (uint32_t)p.tiles + V, in = at - units_before(lo);
-        p.row = (int)(in / units);
+        p.b = seq_of(at);
+        p.tiles = (int)(pre[p.b + 1] - pre[p.b]);
+        const uint32_t units = (uint32_t)p.tiles + V, in = at - units_before(p.b);
+        p.row = (int)div(in, units);
         const uint32_t t = in - (uint32_t)p.row * units;
         p.t = (int)(t - min(t, V));
         tiles = at - V * ((uint32_t)p.b * R + (uint32_t)p.row) - min(t, V);
@@ -915,9 +1007,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
         if (p.b < B) p.tiles = (int)(pre[p.b + 1] - pre[p.b]);
     };
     uint32_t u = tiles_all, end = to;           // in tiles from here on
-    Place begin = {};
-    if (from < to) begin = cut(from, u);
-    if (to >= W) end = tiles_all;
+    if (apart) {
+        begin.t = (int)(from - row0);
+        if (from < to) u = from;
+    } else if (from < to) {
+        begin = cut(from, u);
+    }
+    if (to >= W) end = tiles_all;       // (apart: the last CTA's last warp, where W is tiles_all)
     else if (full) cut(to, end);
     auto first_key = [&](int b) { return s.a.window > 0 ? max(0, slen[b] - s.a.window) : 0; };
 
@@ -1185,8 +1281,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ Sp
             asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
             // meanwhile, the CTAs that hold the row
             const uint32_t tiles = pre[b + 1] - pre[b], r0 = units_before(b) + (uint32_t)row * (tiles + V) + V;
-            const int c0 = (int)cta_of(r0);
-            count = (int)cta_of(r0 + tiles - 1) - c0 + 1;
+            int c0 = s_apart[0];
+            if (c0 >= 0) {
+                count = s_apart[1];
+            } else {
+                c0 = (int)cta_of(r0);
+                count = (int)cta_of(r0 + tiles - 1) - c0 + 1;
+            }
             if (old == count - 1) {
                 *ticket = 0;
                 first = c0;

@@ -145,6 +145,25 @@ def test_short_rows_stay_whole_between_long_ones(hq, D, kv):
     _run(lens, hq, 4, D, 32, kv, window=0)
 
 
+FEW = {  # rows with CTAs of their own, on both sides of what one takes; more rows than CTAs with little to do
+    "two_heads": ([511, 512, 513, 1, 0, 1023, 1024, 1025, 256, 257], 2),
+    "one_sequence": ([1300], 8),
+    "past_a_warp": ([(i * 97) % 500 for i in range(40)] + [1030, 1024, 1025], 2),
+    "most_rows": ([(i * 89) % 300 for i in range(147)] + [513, 0, 1040], 1),
+    "between": ([(i * 37) % 60 for i in range(60)] + [700, 0, 33, 515, 1], 4),
+    "between_in_a_warp": ([(i * 37) % 60 for i in range(29)] + [700, 0, 515], 8),
+}
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name", list(FEW))
+def test_few_rows(name, D, kv):
+    lens, hkv = FEW[name]
+    _run(lens, 4 * hkv, hkv, D, 32, kv)
+    _run(lens, 4 * hkv, hkv, D, 32, kv, window=200)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 1000])
 def test_window(window, kv):
