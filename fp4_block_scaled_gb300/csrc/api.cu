@@ -255,6 +255,17 @@ cudaError_t moe::lib_host_alloc(void** p, size_t bytes, unsigned flags)
     return cudaHostAlloc(p, bytes, flags);
 }
 
+cudaError_t moe::lib_zero(void* p, size_t bytes)
+{
+    cudaStream_t s;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(p, 0, bytes, s);
+    const cudaError_t done = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
+    return e == cudaSuccess ? done : e;
+}
+
 extern "C" {
 
 size_t moe_ffn_packed_expert_bytes(const moe_ffn_config* cfg)

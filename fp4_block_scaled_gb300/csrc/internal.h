@@ -75,6 +75,10 @@ cudaError_t gemv_init_device();   // per device, before the first launch
 // so that a test can make them fail (moe_ffn_test_fail_allocs).
 cudaError_t lib_malloc(void** p, size_t bytes);
 cudaError_t lib_host_alloc(void** p, size_t bytes, unsigned flags);
+
+// Sets device memory of the current device to zero before it returns: on a stream
+// of its own, so that no stream has to be ordered after it, nor it after any.
+cudaError_t lib_zero(void* p, size_t bytes);
 size_t gemv_stream_smem();
 
 // Optional per-phase event recorder (moe_ffn_profile_*); nullptr = off.

@@ -165,8 +165,8 @@ int moe_kv_create(moe_kv_t* out, const moe_kv_config* cfg, int device)
         delete h;
         return MOE_ERR_OOM;
     }
-    // the status word and the attention's tickets start at zero
-    if (cudaMemset(ws, 0, 256 + w.frags) != cudaSuccess) {
+    // the status word and the attention's tickets are zero before any stream can use them
+    if (lib_zero(ws, 256 + w.frags) != cudaSuccess) {
         cudaFree(ws);
         delete h;
         return MOE_ERR_CUDA;

@@ -108,3 +108,31 @@ def test_the_largest_batch(kv):
         torch.cuda.synchronize()
         assert moe.moe_kv_status(h) == moe.MOE_OK
     st.check(list(range(0, 2048, 29)) + [699, 700, 701, 2047])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_new_handle_works_at_once_on_a_stream_beside_a_busy_default_one(kv):
+    """The tickets of rows split among CTAs are zero when the handle is there,
+    whatever the memory held before and whatever the default stream has to do
+    (torch's other streams do not wait for it)."""
+    st = Step([5000, 300, 44], 8, 2, 64, 16, kv, 5)
+    s = torch.cuda.Stream()
+    with handle(8, 2, 64, 16, st.pages, st.B, st.row, kv) as h:     # kernels loaded
+        st.run(h, s)
+        torch.cuda.synchronize()
+    for _ in range(3):
+        dirt = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+        st.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        del dirt
+        torch.cuda.empty_cache()                                     # memory that the workspace may come from
+        torch.cuda._sleep(1 << 30)                                   # half a second of the default stream
+        busy = torch.cuda.Event()
+        busy.record()
+        with handle(8, 2, 64, 16, st.pages, st.B, st.row, kv) as h:
+            for _ in range(4):
+                st.run(h, s)
+            s.synchronize()
+            assert not busy.query(), "the default stream ended first: nothing was shown"
+            assert moe.moe_kv_status(h, s) == moe.MOE_OK
+        st.check()
