@@ -339,7 +339,7 @@ int moe_ffn_create(moe_ffn_t* out, const moe_ffn_config* cfg, int device)
         delete h;
         return MOE_ERR_OOM;
     }
-    if (cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess ||
+    if (lib_zero(h->ws, h->ws_bytes) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->cap_stream, cudaStreamNonBlocking) != cudaSuccess) {
         cudaFree(h->ws);
         delete h;

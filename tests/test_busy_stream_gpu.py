@@ -1,0 +1,67 @@
+"""Handles made and used while torch's default stream is busy: torch's other
+streams do not wait for it, and nothing of a handle may."""
+import contextlib
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_block_scaled_gb300 as moe
+from moe_setup import Layer, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    moe.lib()
+    yield
+
+
+@contextlib.contextmanager
+def busy_default_stream():
+    """Half a second of work on the default stream, which outlasts the block."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1 << 30)
+    end = torch.cuda.Event()
+    end.record()
+    yield
+    assert not end.query(), "the default stream ended first: nothing was shown"
+    torch.cuda.synchronize()
+
+
+def freed_memory_of_ones():
+    """Memory that the next handle's workspace may come from holds no zeros."""
+    dirt = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirt
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("path,T", [("slot", 1), ("slot", 4), ("group", 20)])
+def test_a_new_ffn_handle_works_at_once(path, T):
+    """The counters of the layer kernels are zero when the handle is there."""
+    L = Layer(E=16, H=1024, I=448, k=6, max_tokens=32, path=path)
+    s = torch.cuda.Stream()
+    try:
+        x, idx, w = inputs(T, 16, 1024, 6, seed=3)
+        want = L.run(x, idx, w)
+        xd = torch.from_numpy(x.view(np.int16)).cuda()
+        it, wt = torch.from_numpy(np.ascontiguousarray(idx, np.int32)).cuda(), torch.from_numpy(np.ascontiguousarray(w, np.float32)).cuda()
+        y = torch.empty_like(want)
+        for _ in range(3):
+            y.fill_(float("nan"))
+            freed_memory_of_ones()
+            with busy_default_stream():
+                h = moe.moe_ffn_create(L.cfg, 0)
+                for _ in range(3):
+                    moe.moe_ffn_forward(h, xd, it, wt, L.es.table, y, T, stream=s)
+                s.synchronize()
+            assert moe.moe_ffn_status(h, s) == moe.MOE_OK
+            moe.moe_ffn_destroy(h)
+            assert torch.equal(y, want)
+    finally:
+        torch.cuda.synchronize()
+        L.close()
