@@ -266,6 +266,16 @@ cudaError_t moe::lib_zero(void* p, size_t bytes)
     return e == cudaSuccess ? done : e;
 }
 
+cudaError_t moe::lib_take_status(int* word, cudaStream_t s, int* v)
+{
+    *v = 0;
+    cudaError_t e = cudaMemcpyAsync(v, word, sizeof(int), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *v == 0) return e;
+    e = cudaMemsetAsync(word, 0, sizeof(int), s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
+
 extern "C" {
 
 size_t moe_ffn_packed_expert_bytes(const moe_ffn_config* cfg)

@@ -79,6 +79,10 @@ cudaError_t lib_host_alloc(void** p, size_t bytes, unsigned flags);
 // Sets device memory of the current device to zero before it returns: on a stream
 // of its own, so that no stream has to be ordered after it, nor it after any.
 cudaError_t lib_zero(void* p, size_t bytes);
+
+// Waits for s, then reads a status word and clears it, both on s: before the next
+// call there can set it again, and without the default stream.
+cudaError_t lib_take_status(int* word, cudaStream_t s, int* v);
 size_t gemv_stream_smem();
 
 // Optional per-phase event recorder (moe_ffn_profile_*); nullptr = off.

@@ -182,9 +182,7 @@ int moe_kv_status(moe_kv_t h, void* stream)
     if (!h) return MOE_ERR_INVALID_ARG;
     KvGuard guard(h->device);
     int v = 0;
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
-    if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-    if (v && cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
+    if (lib_take_status(h->status, (cudaStream_t)stream, &v) != cudaSuccess) return MOE_ERR_CUDA;
     return v & kStatusBadIndex ? MOE_ERR_BAD_INDEX : MOE_OK;
 }
 

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import fp4_block_scaled_gb300 as moe
+from kv_setup import Pool, handle
 from moe_setup import Layer, inputs
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,25 @@ def test_a_new_ffn_handle_works_at_once(path, T):
     finally:
         torch.cuda.synchronize()
         L.close()
+
+
+def test_the_cache_status_is_read_and_cleared_on_its_stream():
+    """Errors set right after a status call are kept, and it waits for its own
+    stream alone."""
+    D, page = 64, 16
+    p = Pool(1, 1, page, D, "bf16", np.random.default_rng(0))
+    x = torch.zeros((1, 1, D), dtype=torch.bfloat16, device="cuda")
+    good, bad = (torch.tensor([n], dtype=torch.int32, device="cuda") for n in (0, page))     # beyond the row
+    tab = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    with handle(1, 1, D, page, 1, 1, 1) as h:
+        def append(pos):
+            moe.moe_kv_append(h, p.struct, x, x, pos, tab, 1, stream=s)
+        append(good)
+        assert moe.moe_kv_status(h, s) == moe.MOE_OK
+        with busy_default_stream():
+            for _ in range(50):
+                append(bad)
+                assert moe.moe_kv_status(h, s) == moe.MOE_ERR_BAD_INDEX
+            append(good)
+            assert moe.moe_kv_status(h, s) == moe.MOE_OK
