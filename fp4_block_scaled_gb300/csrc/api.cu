@@ -835,12 +835,8 @@ int moe_ffn_status(moe_ffn_t h, void* stream)
 {
     if (!h) return MOE_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    cudaStream_t s = (cudaStream_t)stream;
     int v = 0;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
-    if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    if (v && cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
+    if (lib_take_status(h->status, (cudaStream_t)stream, &v) != cudaSuccess) return MOE_ERR_CUDA;
     if (v & kStatusTimeout) return MOE_ERR_DEVICE_TIMEOUT;
     if (v & kStatusBadIndex) return MOE_ERR_BAD_INDEX;
     return MOE_OK;

@@ -88,3 +88,29 @@ def test_the_cache_status_is_read_and_cleared_on_its_stream():
                 assert moe.moe_kv_status(h, s) == moe.MOE_ERR_BAD_INDEX
             append(good)
             assert moe.moe_kv_status(h, s) == moe.MOE_OK
+
+
+def test_the_ffn_status_is_read_and_cleared_on_its_stream():
+    L = Layer(E=8, H=256, I=128, k=2, max_tokens=2)
+    s = torch.cuda.Stream()
+    try:
+        x, idx, w = inputs(1, 8, 256, 2, seed=1)
+        xd, wt = torch.from_numpy(x.view(np.int16)).cuda(), torch.from_numpy(np.ascontiguousarray(w, np.float32)).cuda()
+        good = torch.from_numpy(np.ascontiguousarray(idx, np.int32)).cuda()
+        bad = torch.full_like(good, 99)                              # no such expert
+        y = torch.zeros((1, 256), dtype=torch.float32, device="cuda")
+
+        def run(it):
+            moe.moe_ffn_forward(L.h, xd, it, wt, L.es.table, y, 1, stream=s)
+        torch.cuda.synchronize()
+        run(good)
+        assert moe.moe_ffn_status(L.h, s) == moe.MOE_OK
+        with busy_default_stream():
+            for _ in range(50):
+                run(bad)
+                assert moe.moe_ffn_status(L.h, s) == moe.MOE_ERR_BAD_INDEX
+            run(good)
+            assert moe.moe_ffn_status(L.h, s) == moe.MOE_OK
+    finally:
+        torch.cuda.synchronize()
+        L.close()
