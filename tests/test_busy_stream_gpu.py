@@ -1,12 +1,11 @@
 """Handles made and used while torch's default stream is busy: torch's other
 streams do not wait for it, and nothing of a handle may."""
-import contextlib
-
 import numpy as np
 import pytest
 import torch
 
 import fp4_block_scaled_gb300 as moe
+from busy_stream import busy_default_stream
 from kv_setup import Pool, handle
 from moe_setup import Layer, inputs
 
@@ -19,26 +18,6 @@ def _cuda():
         pytest.skip("no CUDA device")
     moe.lib()
     yield
-
-
-@contextlib.contextmanager
-def busy_default_stream():
-    """Half a second of work on the default stream, which outlasts the block."""
-    torch.cuda.synchronize()
-    torch.cuda._sleep(1 << 30)
-    end = torch.cuda.Event()
-    end.record()
-    yield
-    assert not end.query(), "the default stream ended first: nothing was shown"
-    torch.cuda.synchronize()
-
-
-def freed_memory_of_ones():
-    """Memory that the next handle's workspace may come from holds no zeros."""
-    dirt = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
-    torch.cuda.synchronize()
-    del dirt
-    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("path,T", [("slot", 1), ("slot", 4), ("group", 20)])
@@ -54,7 +33,6 @@ def test_a_new_ffn_handle_works_at_once(path, T):
         y = torch.empty_like(want)
         for _ in range(3):
             y.fill_(float("nan"))
-            freed_memory_of_ones()
             with busy_default_stream():
                 h = moe.moe_ffn_create(L.cfg, 0)
                 for _ in range(3):

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import fp4_block_scaled_gb300 as moe
+from busy_stream import busy_default_stream
 from kv_setup import Pool, bf16_of, check_attention, f64, handle, table
 from oracle import kv as okv
 
@@ -117,22 +118,18 @@ def test_a_new_handle_works_at_once_on_a_stream_beside_a_busy_default_one(kv):
     (torch's other streams do not wait for it)."""
     st = Step([5000, 300, 44], 8, 2, 64, 16, kv, 5)
     s = torch.cuda.Stream()
+    cfg = moe.kv_config(8, 2, 64, 16, st.pages, st.B, st.row, kv_dtype=moe.MOE_KV_E4M3_UE8M0 if kv == "e4m3" else moe.MOE_KV_BF16,
+                        out_dtype=moe.MOE_OUT_F32)
     with handle(8, 2, 64, 16, st.pages, st.B, st.row, kv) as h:     # kernels loaded
         st.run(h, s)
         torch.cuda.synchronize()
     for _ in range(3):
-        dirt = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
         st.out.fill_(float("nan"))
-        torch.cuda.synchronize()
-        del dirt
-        torch.cuda.empty_cache()                                     # memory that the workspace may come from
-        torch.cuda._sleep(1 << 30)                                   # half a second of the default stream
-        busy = torch.cuda.Event()
-        busy.record()
-        with handle(8, 2, 64, 16, st.pages, st.B, st.row, kv) as h:
+        with busy_default_stream():
+            h = moe.moe_kv_create(cfg, 0)
             for _ in range(4):
                 st.run(h, s)
             s.synchronize()
-            assert not busy.query(), "the default stream ended first: nothing was shown"
-            assert moe.moe_kv_status(h, s) == moe.MOE_OK
+        assert moe.moe_kv_status(h, s) == moe.MOE_OK
+        moe.moe_kv_destroy(h)
         st.check()
