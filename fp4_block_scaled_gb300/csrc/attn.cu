@@ -66,7 +66,8 @@ __host__ __device__ constexpr int stage_bytes(int DP, bool F8)
 __host__ __device__ constexpr int num_stages(int DP, bool F8) { return stage_bytes(DP, F8) < 6000 ? 5 : 3; }
 
 // A part of a row: NROW output rows (not divided by the sums), the powers of
-// two that they are multiples of, the sums of weights, and (E4M3) theirs.  The
+// two that the sums of weights are multiples of, the sums, and (E4M3) the whole
+// powers of two by which the output's lie above theirs.  The
 // rows are spaced so that a warp's stores of an MMA result (8 rows, 2 or 4
 // columns a lane) meet no bank twice.
 __host__ __device__ constexpr int part_row(int DP, bool F8) { return DP + (F8 ? 16 : 8); }
@@ -253,11 +254,14 @@ struct Kernel {
 
     // ---- a row's state in one warp: lane 4 g + j holds row g (and g + 8 for
     // NROW 16), columns 2j, 2j + 1 of every 8
-    // o 2^mo is the row's sum of weights times values, l 2^m its sum of weights.
-    // E4M3: the values' scales 2^(s - 127) enter o's weights as exponents, so o
-    // has a reference of its own; bf16: mo is m.
+    // o 2^m is the row's sum of weights times values, l 2^m its sum of weights.
+    // E4M3: the values' scales 2^(s - 127) enter o's weights as exponents, so o's
+    // reference is m + whole(up): apart from m by a whole number, so that a score
+    // less m is rounded once, for o and l alike.  (With a reference of its own,
+    // rounded like the scores, one key's output came out off by 2.6e-6 of itself
+    // at scores of tens and by 1e-5 at hundreds; now it is the value.)
     float o[ND][4];
-    float m[2], l[2], mo[2];
+    float m[2], l[2], up[2];
     uint32_t q[KS][QR];
     float qf[2];                // score factor of a row: E4M3 queries are scaled
 
@@ -267,13 +271,16 @@ struct Kernel {
         for (int i = 0; i < ND; i++)
 #pragma unroll
             for (int k = 0; k < 4; k++) o[i][k] = 0.0f;
-        m[0] = m[1] = mo[0] = mo[1] = -INFINITY;
+        m[0] = m[1] = up[0] = up[1] = -INFINITY;
         l[0] = l[1] = 0.0f;
     }
 
     // (scores pass the references by at most kSlack; o's lies 2^7 lower, so that
-    // its weights, below 2^15, use f16's range)
+    // its weights, up to 2^15, use f16's range)
     static constexpr float kLift = 7.0f;
+
+    // up as o's reference has it; -inf before the first key
+    __device__ __forceinline__ static float whole(float up) { return up == -INFINITY ? 0.0f : floorf(up); }
 
     // Query rows as the A operand.  E4M3: the contraction index runs as
     // e4m3_to_f16 yields the keys' elements, (4j, 4j + 1), (4j + 2, 4j + 3) of 16, and a
@@ -390,22 +397,78 @@ struct Kernel {
         }
     }
 
+    // o times `down`, a factor a row
+    __device__ __forceinline__ void shrink(const float (&down)[2])
+    {
+#pragma unroll
+        for (int i = 0; i < ND; i++) {
+            o[i][0] *= down[0];
+            o[i][1] *= down[0];
+            o[i][2] *= NROW == 8 ? down[0] : down[1];                // NROW 8: the low terms' sums
+            o[i][3] *= NROW == 8 ? down[0] : down[1];
+        }
+    }
+
+    // E4M3: new references m and up, and x, the scores less the old one, r, less the
+    // new one; w0 is the old whole(up) and then the new; t: the largest of a row's x.
+    __device__ __forceinline__ void rebase(float (&x)[NT][4], const float (&t)[2], const float (&r)[2], float (&w0)[2], const float* sc,
+                                           int j)
+    {
+        constexpr int NV = NROW == 8 ? 2 : 4;
+        float d[2] = {0.0f, 0.0f}, ty[2] = {-INFINITY, -INFINITY}, down[2] = {1.0f, 1.0f};
+        bool none[2] = {true, true};            // no key yet: nothing to bring along
+#pragma unroll
+        for (int k = 0; k < NV / 2; k++) {
+            none[k] = m[k] == -INFINITY;
+            m[k] = fmaxf(m[k], r[k] + t[k]);
+            d[k] = r[k] - (m[k] == -INFINITY ? 0.0f : m[k]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const float2 e = *reinterpret_cast<const float2*>(sc + TT + 8 * n + 2 * j);
+#pragma unroll
+            for (int k = 0; k < NV; k++) {
+                x[n][k] += d[k >> 1];
+                ty[k >> 1] = fmaxf(ty[k >> 1], x[n][k] + ((k & 1) ? e.y : e.x));
+            }
+        }
+#pragma unroll
+        for (int i = 1; i <= 2; i++)
+#pragma unroll
+            for (int k = 0; k < NV / 2; k++) ty[k] = fmaxf(ty[k], __shfl_xor_sync(0xFFFFFFFFu, ty[k], i));
+#pragma unroll
+        for (int k = 0; k < NV / 2; k++) {
+            const float w = w0[k];
+            up[k] = fmaxf(up[k] + d[k], ty[k] - kLift);
+            w0[k] = whole(up[k]);
+            // (the sum rounds by 2^-24 of itself, which counts for little where it is large:
+            // what it is the exponent of is small beside the new keys' then)
+            l[k] *= none[k] ? 0.0f : ex2(d[k]);
+            down[k] = none[k] ? 0.0f : ex2(d[k] + (w - w0[k]));
+        }
+        shrink(down);
+    }
+
     // One tile: `lo`, `hi` are the first and one past the last key of it that
     // count; bad: a bit per 16 keys left out.
     __device__ __forceinline__ void tile(const SplitArgs& s, uint32_t st, const uint8_t* stp, float* sc, int lane, int lo, int hi,
                                          uint32_t bad)
     {
         const int j = lane & 3;
+        float top_scale = 0.0f;                 // E4M3: log2 of the largest of v's scales
         if (F8) {
             // a key a lane: k's scale as a number (byte 0 as zero: below 2^-117 with any
             // code), v's as an exponent; a NaN row has NaN codes
+            uint32_t top = 0;
 #pragma unroll
             for (int i = lane; i < TT; i += 32) {
                 const uint8_t* b = stp + 2 * TT * ROWB + i;
                 sc[i] = __uint_as_float((uint32_t)b[0] << 23);
                 sc[TT + i] = __uint_as_float(0x4B000000u | b[TT]) - 8388735.0f;     // 2^23 + byte, less 2^23 + 127
+                top = max(top, (uint32_t)b[TT]);
             }
             __syncwarp();
+            top_scale = (float)(int)__reduce_max_sync(0xFFFFFFFFu, top) - 127.0f;
         }
         const uint32_t kb = st, vb = st + TT * ROWB;
         float x[NT][4];
@@ -437,11 +500,9 @@ struct Kernel {
                 }
             }
         }
-        // the softmax works in powers of two: x = s log2(e); y: the same with the
-        // value's scale, the exponent of o's weight
+        // the softmax works in powers of two: x = s log2(e)
         constexpr float kLog2e = 1.4426950408889634f;
         constexpr int NV = NROW == 8 ? 2 : 4;
-        float y[F8 ? NT : 1][4];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             float2 f = make_float2(1.0f, 1.0f);
@@ -456,13 +517,18 @@ struct Kernel {
 #pragma unroll
                 for (int k = 0; k < NV; k++) x[n][k] = cap * tanhf(x[n][k]);
         }
+        // E4M3: x less the reference from here on
+        float r[2] = {0.0f, 0.0f}, w0[2] = {0.0f, 0.0f};
         if (F8) {
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                const float2 e = *reinterpret_cast<const float2*>(sc + TT + 8 * n + 2 * j);
-#pragma unroll
-                for (int k = 0; k < NV; k++) y[n][k] = x[n][k] + ((k & 1) ? e.y : e.x);
+            for (int k = 0; k < NV / 2; k++) {
+                r[k] = m[k] == -INFINITY ? 0.0f : m[k];
+                w0[k] = whole(up[k]);
             }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < NV; k++) x[n][k] -= r[k >> 1];
         }
         if (lo > 0 || hi < TT || bad) {
 #pragma unroll
@@ -470,70 +536,60 @@ struct Kernel {
 #pragma unroll
                 for (int k = 0; k < NV; k++) {
                     const int at = 8 * n + 2 * j + (k & 1);
-                    if (at < lo || at >= hi || ((bad >> (n / 2)) & 1)) {
-                        x[n][k] = -INFINITY;
-                        if (F8) y[n][k] = -INFINITY;
-                    }
+                    if (at < lo || at >= hi || ((bad >> (n / 2)) & 1)) x[n][k] = -INFINITY;
                 }
         }
-        float t[2] = {-INFINITY, -INFINITY}, ty[2] = {-INFINITY, -INFINITY};
+        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int k = 0; k < NV; k++) {
-                t[k >> 1] = fmaxf(t[k >> 1], x[n][k]);
-                if (F8) ty[k >> 1] = fmaxf(ty[k >> 1], y[n][k]);
-            }
+            for (int k = 0; k < NV; k++) t[k >> 1] = fmaxf(t[k >> 1], x[n][k]);
 #pragma unroll
         for (int d = 1; d <= 2; d++)
 #pragma unroll
-            for (int k = 0; k < NV / 2; k++) {
-                t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], d));
-                if (F8) ty[k] = fmaxf(ty[k], __shfl_xor_sync(0xFFFFFFFFu, ty[k], d));
-            }
-        bool move = t[0] > m[0] + kSlack || (NROW == 16 && t[1] > m[1] + kSlack);
+            for (int k = 0; k < NV / 2; k++) t[k] = fmaxf(t[k], __shfl_xor_sync(0xFFFFFFFFu, t[k], d));
         if (F8) {
-            // o's references lie kLift lower
-            ty[0] -= kLift;
-            ty[1] -= kLift;
-            move = move || ty[0] > mo[0] + kSlack || (NROW == 16 && ty[1] > mo[1] + kSlack);
-        }
-        if (__any_sync(0xFFFFFFFFu, move)) {
-            float down[2] = {1.0f, 1.0f};
+            // o's weights stay below 2^(kLift + kSlack) if even the largest scale meets
+            // the largest score, which only now and then moves a reference for nothing
+            bool move = false;
 #pragma unroll
-            for (int k = 0; k < NV / 2; k++) {
-                const float to = fmaxf(m[k], t[k]);
-                if (to != m[k]) down[k] = ex2(m[k] - to);            // 0 from -inf
-                m[k] = to;
-                l[k] *= down[k];
-                if (F8) {
-                    const float too = fmaxf(mo[k], ty[k]);
-                    down[k] = too != mo[k] ? ex2(mo[k] - too) : 1.0f;
-                    mo[k] = too;
+            for (int k = 0; k < NV / 2; k++)
+                move = move || t[k] > (m[k] == -INFINITY ? -INFINITY : kSlack) || t[k] + (top_scale - w0[k]) > kLift + kSlack;
+            if (__any_sync(0xFFFFFFFFu, move)) rebase(x, t, r, w0, sc, j);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const float2 e = *reinterpret_cast<const float2*>(sc + TT + 8 * n + 2 * j);
+#pragma unroll
+                for (int k = 0; k < NV; k++) {
+                    const float y = x[n][k] + (((k & 1) ? e.y : e.x) - w0[k >> 1]);
+                    l[k >> 1] += ex2(x[n][k]);
+                    x[n][k] = ex2(y);
                 }
             }
+        } else {
+            const bool move = t[0] > m[0] + kSlack || (NROW == 16 && t[1] > m[1] + kSlack);
+            if (__any_sync(0xFFFFFFFFu, move)) {
+                float down[2] = {1.0f, 1.0f};
 #pragma unroll
-            for (int i = 0; i < ND; i++) {
-                o[i][0] *= down[0];
-                o[i][1] *= down[0];
-                o[i][2] *= NROW == 8 ? down[0] : down[1];            // NROW 8: the low terms' sums
-                o[i][3] *= NROW == 8 ? down[0] : down[1];
+                for (int k = 0; k < NV / 2; k++) {
+                    const float to = fmaxf(m[k], t[k]);
+                    if (to != m[k]) down[k] = ex2(m[k] - to);        // 0 from -inf
+                    m[k] = to;
+                    l[k] *= down[k];
+                }
+                shrink(down);
             }
+#pragma unroll
+            for (int k = 0; k < 2; k++)         // before the first key the reference is -inf, and every x as well
+                r[k] = m[k] == -INFINITY ? 0.0f : m[k];
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < NV; k++) {
+                    x[n][k] = ex2(x[n][k] - r[k >> 1]);
+                    l[k >> 1] += x[n][k];
+                }
         }
-        float r[2], ro[2];                      // before the first key the references are -inf, and every x as well
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            r[k] = m[k] == -INFINITY ? 0.0f : m[k];
-            ro[k] = mo[k] == -INFINITY ? 0.0f : mo[k];
-        }
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int k = 0; k < NV; k++) {
-                x[n][k] = ex2(x[n][k] - r[k >> 1]);
-                l[k >> 1] += x[n][k];
-                if (F8) x[n][k] = ex2(y[n][k] - ro[k >> 1]);
-            }
         // values: 16 keys x 32 bytes of their rows per load.  NROW 8: rows 0..7 of
         // the A operand hold the weights' high terms and rows 8..15 their low
         // terms, so one MMA multiplies both; NROW 16 takes two.
@@ -587,11 +643,14 @@ struct Kernel {
         }
     }
 
-    // 2^mo / (l 2^m), the factor from o to the output; 0 for a row without keys
-    __device__ __forceinline__ static float quotient(float l, float m, float mo)
+    // 2^k / l, the factor from o to the output (k within +-160, in two factors: l may
+    // be what brings it into range); 0 for a row without keys
+    __device__ __forceinline__ static float quotient(float l, float k)
     {
         if (l == 0.0f) return 0.0f;
-        return F8 ? ex2(mo - m) / l : 1.0f / l;
+        if (!F8) return 1.0f / l;
+        const int e = (int)k, a = e >> 1;
+        return 1.0f / l * exp2i(a) * exp2i(e - a);
     }
 
     // Column of o[i][k] (k = 0, 1), and of the pair (i, k), (i + 1, k) in E4M3.
@@ -617,9 +676,9 @@ struct Kernel {
                     *reinterpret_cast<float2*>(r + column(i, 0, j)) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
             }
             if (j == 0) {
-                p[PHEAD + g + 8 * half] = F8 ? mo[half] : m[half];
+                p[PHEAD + g + 8 * half] = m[half];
                 p[PHEAD + NROW + g + 8 * half] = l[half];
-                if (F8) p[PHEAD + 2 * NROW + g + 8 * half] = m[half];
+                if (F8) p[PHEAD + 2 * NROW + g + 8 * half] = whole(up[half]);
             }
         }
     }
@@ -633,7 +692,7 @@ struct Kernel {
             const int hg = c * NROW + g + 8 * half;
             if (hg >= s.G) continue;
             const size_t at = (size_t)b * s.a.hq + h * s.G + hg;
-            const float inv = quotient(l[half], m[half], F8 ? mo[half] : m[half]);
+            const float inv = quotient(l[half], F8 ? whole(up[half]) : 0.0f);
             const size_t out = at * s.a.D;
             if (F8) {           // four columns in a row from an even and an odd MMA column block
 #pragma unroll
@@ -691,23 +750,23 @@ struct Kernel {
 
     // A merged row's VEC columns a lane, to its part `to` or as the row's output.
     __device__ __forceinline__ static void finish(const SplitArgs& s, int b, int row, int g, int lane, const float (&acc)[VEC],
-                                                  float topo, float sum, float top, float* to)
+                                                  float top, float sum, float k, float* to)
     {
         const int d = lane * VEC;
         if (to) {
             if (VEC == 4) *reinterpret_cast<float4*>(to + g * PROW + d) = make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]);
             else *reinterpret_cast<float2*>(to + g * PROW + d) = make_float2(acc[0], acc[1]);
             if (lane == 0) {
-                to[PHEAD + g] = topo;
+                to[PHEAD + g] = top;
                 to[PHEAD + NROW + g] = sum;
-                if (F8) to[PHEAD + 2 * NROW + g] = top;
+                if (F8) to[PHEAD + 2 * NROW + g] = k;
             }
             return;
         }
         const int h = s.chunks == 1 ? row : row / s.chunks, hg = (row - h * s.chunks) * NROW + g;
         if (hg >= s.G) return;
         const size_t out = (size_t)b * s.a.hq + h * s.G + hg;
-        const float inv = quotient(sum, top, topo);
+        const float inv = quotient(sum, k);
         if (d < s.a.D) {
             if (VEC == 4) put4(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv, acc[VEC - 2] * inv, acc[VEC - 1] * inv);
             else put2(s.a, out * s.a.D + d, acc[0] * inv, acc[1] * inv);
@@ -721,36 +780,38 @@ struct Kernel {
     template <class Near>
     __device__ __forceinline__ static void weigh(unsigned mem, Near near, int f, int g, float* tab)
     {
-        float mo[kWarps], l[kWarps], m[kWarps];
-        float top = -INFINITY, topo = -INFINITY, sum = 0.0f;
+        float m[kWarps], l[kWarps], k[kWarps];
+        float top = -INFINITY, above = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; w++) {
             // a place is read whether it holds a part or not, so that no load waits for a branch
             const unsigned is = (mem >> (2 * w)) & 3u;
             const float* e = near(w, is) + PHEAD + g;
-            const float a = e[0], b = e[NROW], c = F8 ? e[2 * NROW] : a;
-            mo[w] = is ? a : -INFINITY;
+            const float a = e[0], b = e[NROW], c = F8 ? e[2 * NROW] : 0.0f;
+            m[w] = is ? a : -INFINITY;
             l[w] = is ? b : 0.0f;
-            m[w] = is ? c : -INFINITY;
+            k[w] = is ? c : 0.0f;
         }
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            topo = fmaxf(topo, mo[w]);
-            top = fmaxf(top, m[w]);
-        }
+        for (int w = 0; w < kWarps; w++) top = fmaxf(top, m[w]);
         // -inf before the first key: nothing to bring to the new references
-        const float ro = topo == -INFINITY ? 0.0f : topo, rt = top == -INFINITY ? 0.0f : top;
+        const float rt = top == -INFINITY ? 0.0f : top;
+        if (F8) {
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) above = fmaxf(above, m[w] + k[w]);
+        }
+        const float kt = F8 ? whole(above - rt) : 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; w++) {
             const unsigned is = (mem >> (2 * w)) & 3u;
-            const float by = ex2(mo[w] - ro);
-            if (is) tab[(2 * w + (is >> 1)) * NROW + g] = by;
-            sum += ex2(m[w] - rt) * l[w];
+            const float by = ex2(m[w] - rt);
+            if (is) tab[(2 * w + (is >> 1)) * NROW + g] = F8 ? ex2(m[w] - rt + (k[w] - kt)) : by;
+            sum += by * l[w];
         }
         float* t = tab + (2 * kWarps + f) * NROW + g;
-        t[0] = topo;
+        t[0] = top;
         t[2 * kWarps * NROW] = sum;
-        t[4 * kWarps * NROW] = top;
+        t[4 * kWarps * NROW] = kt;
     }
 
     // A row's parts of several CTAs merged by one warp: lane i holds part i's
@@ -760,16 +821,16 @@ struct Kernel {
     __device__ __forceinline__ static void join(const SplitArgs& s, int n, At at, int b, int row, int g, int lane)
     {
         constexpr int N = 16;
-        float acc[VEC], top = -INFINITY, topo = -INFINITY, sum = 0.0f;
+        float acc[VEC], top = -INFINITY, kt = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < VEC; k++) acc[k] = 0.0f;
         for (int i0 = 0; i0 < n; i0 += 32) {
-            float mo = -INFINITY, m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, pk = 0.0f;
             if (i0 + lane < n) {
                 const float* e = at(i0 + lane) + PHEAD + g;
-                mo = __ldcg(e);
+                m = __ldcg(e);
                 l = __ldcg(e + NROW);
-                m = F8 ? __ldcg(e + 2 * NROW) : mo;
+                if (F8) pk = __ldcg(e + 2 * NROW);
             }
             float v[N][VEC];
 #pragma unroll
@@ -778,12 +839,24 @@ struct Kernel {
                 for (int k = 0; k < VEC; k++) v[i][k] = 0.0f;
                 if (i0 + i < n) load_vec(v[i], at(i0 + i) + g * PROW + lane * VEC, true);
             }
-            const float to_ = fmaxf(topo, warp_max(mo)), t = F8 ? fmaxf(top, warp_max(m)) : to_;
-            const float rt = t == -INFINITY ? 0.0f : t, ro = to_ == -INFINITY ? 0.0f : to_;
-            const float down = ex2(topo - ro), w = ex2(mo - ro);
-            sum = sum * (F8 ? ex2(top - rt) : down) + warp_sum((F8 ? ex2(m - rt) : w) * l);
+            float t = m, above = m + pk;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+                if (F8) above = fmaxf(above, __shfl_xor_sync(0xFFFFFFFFu, above, o));
+            }
+            t = fmaxf(t, top);
+            above = fmaxf(above, top + kt);
+            const float rt = t == -INFINITY ? 0.0f : t;
+            float down = ex2(top - rt), w = ex2(m - rt);
+            sum = sum * down + warp_sum(w * l);
+            if (F8) {
+                const float k = whole(above - rt);
+                down = ex2(top - rt + (kt - k));
+                w = ex2(m - rt + (pk - k));
+                kt = k;
+            }
             top = t;
-            topo = to_;
 #pragma unroll
             for (int k = 0; k < VEC; k++) acc[k] *= down;
 #pragma unroll
@@ -799,7 +872,7 @@ struct Kernel {
                 }
             }
         }
-        finish(s, b, row, g, lane, acc, topo, sum, top, nullptr);
+        finish(s, b, row, g, lane, acc, top, sum, kt, nullptr);
     }
 };
 
