@@ -442,7 +442,8 @@ typedef struct moe_kv_s* moe_kv_t;
 
 enum {
     MOE_KV_BF16 = 0,        /* bf16 rows                                       */
-    MOE_KV_E4M3_UE8M0 = 1   /* E4M3 codes, one ue8m0 byte per row of one head:
+    MOE_KV_E4M3_UE8M0 = 1   /* E4M3 codes, one ue8m0 byte per row of one head
+                               (2^(byte - 127); 255: a row of NaN):
                                moe_ffn_act_quant's rule with n = D             */
 };
 

@@ -125,3 +125,31 @@ def test_value_scales_over_the_whole_range(hq, hkv, D):
         q = bf16_of(qscale * rng.standard_normal((len(lens), hq, D)))
         got, lse = _attend(p, q, lens, tab, page)
         check_attention(p, okv.bf16(q), lens, tab, page, got, lse, D ** -0.5)
+
+
+@pytest.mark.parametrize("hq,hkv,D", HEADS)
+def test_a_scale_byte_of_255_is_nan(hq, hkv, D):
+    """With codes that are numbers: a key's makes its scores NaN, a value's the
+    output; outside the keys that count it is never used."""
+    rng = np.random.default_rng(D)
+    page, lens = 16, [40, 40, 40, 3000, 3000, 40, 33]
+    row = -(-max(lens) // page)
+    pages = sum(-(-n // page) for n in lens)
+    p = Pool(pages, hkv, page, D, "e4m3", rng)
+    tab = table(lens, page, pages, row, rng)
+    at = lambda b, j: (tab[b, j // page], slice(None), j % page)     # noqa: E731
+    q = np.ones((len(lens), hq, D))
+    p.k[at(0, 19)] = 0xB8                                            # ones, negative: a score of -inf were the byte infinity
+    p.ks[at(0, 19)] = 255
+    p.vs[at(1, 7)] = p.vs[at(3, 2999)] = 255
+    p.ks[at(4, 0)] = 255
+    p.vs[at(5, 3)] = p.ks[at(5, 4)] = 255                            # before the window of 30
+    p.vs[at(6, 40)] = p.ks[at(6, 47)] = 255                          # behind the last key
+    got, lse = _attend(p, bf16_of(q), lens, tab, page)
+    assert np.isnan(got[[0, 1, 3, 4]]).all() and np.isnan(lse[[0, 4]]).all()
+    assert np.isfinite(got[[2, 6]]).all() and np.isfinite(lse[[1, 2, 3, 6]]).all()
+    keep = [2, 6]
+    check_attention(p, q[keep], [lens[b] for b in keep], tab[keep], page, got[keep], lse[keep], D ** -0.5)
+    got, lse = _attend(p, bf16_of(q), [40] * 7, tab, page, window=30)
+    assert np.isfinite(got[[2, 5]]).all() and np.isfinite(lse[[2, 5]]).all()
+    check_attention(p, q[[5]], [40], tab[[5]], page, got[[5]], lse[[5]], D ** -0.5, window=30)
