@@ -457,17 +457,16 @@ struct Kernel {
         const int j = lane & 3;
         float top_scale = 0.0f;                 // E4M3: log2 of the largest of v's scales
         if (F8) {
-            // a key a lane: k's scale as a number (byte 0 as zero: below 2^-117 with any
-            // code), v's as an exponent, bytes of 255 as NaN, those of keys that do not
-            // count as 0
+            // a key a lane: k's scale as a number, v's as an exponent, bytes of 255 as
+            // NaN, those of keys that do not count as 0 (2^-127)
             uint32_t top = 0;
 #pragma unroll
             for (int i = lane; i < TT; i += 32) {
                 const uint8_t* b = stp + 2 * TT * ROWB + i;
                 const bool in = i >= lo && i < hi && !((bad >> (i / 16)) & 1);
                 const uint32_t kb = in ? b[0] : 0, vb = in ? b[TT] : 0;
-                // (the exponent field alone is infinity for 255)
-                sc[i] = __uint_as_float(kb << 23 | (kb == 255 ? 1u << 22 : 0u));
+                // the exponent field alone is zero for 0 and infinity for 255
+                sc[i] = __uint_as_float(kb << 23 | (kb == 0 || kb == 255 ? 1u << 22 : 0u));
                 sc[TT + i] = vb == 255 ? __uint_as_float(0x7FC00000u)
                                        : __uint_as_float(0x4B000000u | vb) - 8388735.0f;    // 2^23 + byte, less 2^23 + 127
                 top = max(top, vb);

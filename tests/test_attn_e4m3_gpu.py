@@ -153,3 +153,20 @@ def test_a_scale_byte_of_255_is_nan(hq, hkv, D):
     got, lse = _attend(p, bf16_of(q), [40] * 7, tab, page, window=30)
     assert np.isfinite(got[[2, 5]]).all() and np.isfinite(lse[[2, 5]]).all()
     check_attention(p, q[[5]], [40], tab[[5]], page, got[[5]], lse[[5]], D ** -0.5, window=30)
+
+
+@pytest.mark.parametrize("hq,hkv,D", HEADS)
+def test_scale_byte_zero_is_the_smallest_scale(hq, hkv, D):
+    """2^-127, not zero: seen with queries of 2^120."""
+    rng = np.random.default_rng(D)
+    page, lens = 16, [1, 33, 700]
+    row = -(-max(lens) // page)
+    pages = sum(-(-n // page) for n in lens)
+    p = Pool(pages, hkv, page, D, "e4m3", rng)
+    p.ks[:] = 0
+    p.ks[rng.random(p.ks.shape) < 0.3] = 1
+    tab = table(lens, page, pages, row, rng)
+    q = bf16_of(2.0 ** 120 * rng.standard_normal((len(lens), hq, D)))
+    got, lse = _attend(p, q, lens, tab, page, scale=0.25)
+    check_attention(p, okv.bf16(q), lens, tab, page, got, lse, 0.25)
+    assert np.abs(lse[0]).max() > 2.0 ** -6                          # the scores are there
