@@ -122,6 +122,70 @@ bool clash(const Span& x, int hx, long long ldx, const Span& y, int hy, long lon
 
 constexpr int kMaxTokens = 1 << 24;     // of one moe_rope or moe_kv_append call
 
+// Numbers of about 104 bits, the sum of two doubles, for the rotary table, whose
+// entries are 64-bit fractions: errors below 2^-84 of an entry, exp's doublings
+// included.
+struct Wide {
+    double hi, lo = 0.0;
+};
+
+Wide fast_sum(double a, double b)       // |a| >= |b|, or a = 0
+{
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+
+Wide operator+(Wide x, Wide y)
+{
+    const double s = x.hi + y.hi, b = s - x.hi, e = (x.hi - (s - b)) + (y.hi - b);
+    return fast_sum(s, e + (x.lo + y.lo));
+}
+
+Wide operator-(Wide x) { return {-x.hi, -x.lo}; }
+
+Wide operator*(Wide x, Wide y)
+{
+    const double p = x.hi * y.hi;
+    return fast_sum(p, fma(x.hi, y.lo, fma(x.lo, y.hi, fma(x.hi, y.hi, -p))));
+}
+
+Wide operator/(Wide x, Wide y)
+{
+    Wide q = {x.hi / y.hi};
+    for (int i = 0; i < 2; i++) {
+        const Wide rest = x + -(q * y);
+        q = q + Wide{rest.hi / y.hi};
+    }
+    return q;
+}
+
+// e^x for |x| < 2^11: the series at x / 2^n below 2^-7, squared n times
+Wide wide_exp(Wide x)
+{
+    int n = 0;
+    frexp(x.hi, &n);
+    n = x.hi == 0.0 || n < -7 ? 0 : n + 7;
+    const Wide r = {ldexp(x.hi, -n), ldexp(x.lo, -n)};
+    Wide s = {1.0};
+    for (int i = 16; i > 0; i--) s = Wide{1.0} + r * s / Wide{(double)i};
+    for (; n > 0; n--) s = s * s;
+    return s;
+}
+
+// ln of m in [1/2, 2]: the logarithm of doubles and one step of Newton's
+Wide wide_log_near_one(double m)
+{
+    const Wide y = {log(m)};
+    return y + (Wide{m} * wide_exp(-y) + Wide{-1.0});
+}
+
+Wide wide_log(double x)                 // x >= 1
+{
+    int e;
+    const double m = frexp(x, &e);
+    return wide_log_near_one(m) + wide_log_near_one(2.0) * Wide{(double)e};
+}
+
 }  // namespace
 
 extern "C" {
@@ -202,23 +266,27 @@ int moe_rope_table(int rot_dim, double base, int kind, double factor, int traine
     if (kind != MOE_ROPE_SCALE_NONE && (!(factor >= 1.0) || !isfinite(factor))) return MOE_ERR_INVALID_ARG;
     if (kind == MOE_ROPE_SCALE_NTK && rot_dim < 4) return MOE_ERR_INVALID_ARG;
     if (kind == MOE_ROPE_SCALE_YARN && trained_len <= 0) return MOE_ERR_INVALID_ARG;
-    const double two_pi = 6.283185307179586476925;
+    const Wide two_pi = {6.283185307179586, 2.4492935982947064e-16};
     const double r = rot_dim;
-    const double b = kind == MOE_ROPE_SCALE_NTK ? base * pow(factor, r / (r - 2.0)) : base;
+    Wide ln_base = wide_log(base);
+    if (kind == MOE_ROPE_SCALE_NTK) ln_base = ln_base + wide_log(factor) * Wide{r} / Wide{r - 2.0};
     double lo = 0.0, hi = 0.0;
     if (kind == MOE_ROPE_SCALE_YARN) {
-        auto pair_of = [&](double t) { return r * log(trained_len / (t * two_pi)) / (2.0 * log(base)); };
+        auto pair_of = [&](double t) { return r * log(trained_len / (t * two_pi.hi)) / (2.0 * log(base)); };
         lo = fmax(floor(pair_of(32.0)), 0.0);
         hi = fmin(ceil(pair_of(1.0)), r - 1.0);
     }
     for (int i = 0; i < rot_dim / 2; i++) {
-        double f = pow(b, -2.0 * i / r);
-        if (kind == MOE_ROPE_SCALE_LINEAR) f /= factor;
+        Wide f = wide_exp(ln_base * Wide{-2.0 * i} / Wide{r});
+        if (kind == MOE_ROPE_SCALE_LINEAR) f = f / Wide{factor};
         if (kind == MOE_ROPE_SCALE_YARN) {
-            const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
-            f = f / factor * ramp + f * (1.0 - ramp);
+            const Wide ramp = i <= lo ? Wide{0.0} : i >= hi ? Wide{1.0} : Wide{i - lo} / Wide{hi - lo};
+            f = f * (ramp / Wide{factor} + (Wide{1.0} + -ramp));
         }
-        turns[i] = (uint64_t)(f / two_pi * 18446744073709551616.0 + 0.5);      // f <= 1: below 2^62
+        f = f / two_pi;
+        // f 2^64, below 2^62, to the nearest whole number
+        const double whole = floor(ldexp(f.hi, 64)), rest = ldexp(f.hi, 64) - whole + ldexp(f.lo, 64);
+        turns[i] = (uint64_t)((int64_t)whole + (int64_t)floor(rest + 0.5));
     }
     *scale = kind == MOE_ROPE_SCALE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
     return MOE_OK;

@@ -3,6 +3,7 @@ GPU): the manager against a model with plain lists over random histories, hand
 cases, what it refuses; the table against 64-bit frequencies."""
 import ctypes
 import math
+from decimal import ROUND_CEILING, ROUND_FLOOR, Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -186,3 +187,40 @@ def test_word_call_refusals():
               lambda: moe.moe_attn_decode(None, pool, None, None, None, 1, None),
               lambda: moe.moe_kv_copy_pages(None, [pool], None, 1), lambda: moe.moe_kv_copy_pages(None, [], None, 0)):
         assert _code(f) == e
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def _exact_turns(rot, base, kind, factor, trained):
+    """f_i / (2 pi) 2^64 to 60 digits."""
+    with localcontext() as c:
+        c.prec = 70
+        base, factor, rot = Decimal(base), Decimal(factor), Decimal(rot)
+        ln = base.ln()
+        if kind == moe.MOE_ROPE_SCALE_NTK:
+            ln += factor.ln() * rot / (rot - 2)
+        f = [(-2 * i * ln / rot).exp() for i in range(int(rot) // 2)]
+        if kind == moe.MOE_ROPE_SCALE_LINEAR:
+            f = [x / factor for x in f]
+        if kind == moe.MOE_ROPE_SCALE_YARN:
+            d = lambda t: rot * (trained / (2 * PI * t)).ln() / (2 * ln)     # noqa: E731
+            lo = max(Decimal(0), d(32).to_integral_value(ROUND_FLOOR))
+            hi = min(rot - 1, d(1).to_integral_value(ROUND_CEILING))
+            r = [min(Decimal(1), max(Decimal(0), (i - lo) / max(Decimal("0.001"), hi - lo))) for i in range(len(f))]
+            f = [x / factor * a + x * (1 - a) for x, a in zip(f, r)]
+        return [x / (2 * PI) * 2 ** 64 for x in f]
+
+
+@pytest.mark.parametrize("kind", range(4))
+@pytest.mark.parametrize("rot,base,factor,trained", [
+    (128, 10000.0, 4.0, 8192), (80, 10000.0, 8.0, 4096), (64, 500000.0, 32.0, 4096), (96, 1e6, 1.7, 32768), (16, 10000.0, 1.0, 2048),
+    (1024, 10000.0, 3.0, 100), (6, 1.5, 1e6, 1 << 30), (32, 1.0000001, 2.5, 1), (48, 1e300, 1e10, 5000)])
+def test_rope_table_is_rounded_from_the_frequencies(kind, rot, base, factor, trained):
+    """A position's angle is off by p 2^-65 turns only if the table's entries are
+    the 64-bit fractions next to f_i / (2 pi): half a unit, and 2^-84 of up to 2^62
+    units for the arithmetic."""
+    turns, _ = moe.moe_rope_table(rot, base, kind, factor, trained)
+    want = _exact_turns(rot, base, kind, factor, trained)
+    err = [abs(Decimal(int(t)) - w) for t, w in zip(turns, want)]
+    assert max(err) <= Decimal(0.5 + 2.0 ** -20), (int(np.argmax([float(e) for e in err])), float(max(err)))
