@@ -484,6 +484,7 @@ struct Words {
     {
         double d;
         memcpy(&d, w++, 8);
+        ok = ok && (d == 0.0 || (float)d != 0.0f);      // 0 stands for a default
         return (float)d;
     }
 };

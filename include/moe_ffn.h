@@ -592,7 +592,8 @@ int moe_kv_copy_pages(moe_kv_t h, const moe_kv_pool* pools, int num_pools, const
 /* The four calls above with their arguments as one array of 64-bit words, in
  * their order (pointers and integers as they are, floating arguments as
  * doubles): the same call, for language bindings that pay for every argument.
- * INVALID_ARG: an unknown op, no array, an integer outside its type. */
+ * INVALID_ARG: an unknown op, no array, an integer outside its type, a floating
+ * argument other than 0 that a float holds as 0. */
 enum { MOE_KV_CALL_ROPE = 0, MOE_KV_CALL_APPEND = 1, MOE_KV_CALL_ATTN_DECODE = 2, MOE_KV_CALL_COPY_PAGES = 3 };
 int moe_kv_call(int op, const int64_t* words);
 
