@@ -170,3 +170,21 @@ def test_scale_byte_zero_is_the_smallest_scale(hq, hkv, D):
     got, lse = _attend(p, q, lens, tab, page, scale=0.25)
     check_attention(p, okv.bf16(q), lens, tab, page, got, lse, 0.25)
     assert np.abs(lse[0]).max() > 2.0 ** -6                          # the scores are there
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,D", HEADS + [(12, 1, 32), (24, 1, 128)])
+@pytest.mark.parametrize("softcap,scale,window", [(30.0, 0.0, 0), (2.0, 0.5, 0), (50.0, 0.0, 33), (5.0, -0.4, 100), (0.0, -0.3, 0),
+                                                  (0.0, 1e-3, 17)])
+def test_softcap_and_scale(softcap, scale, window, hq, hkv, D, out):
+    """Every kernel of E4M3 rows with capped and negative scores: the cap comes
+    before the values' scales, the keys' scales before the cap."""
+    rng = np.random.default_rng(D + hq + window)
+    page, lens = 16, [0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257, 3000]
+    row = -(-max(lens) // page)
+    pages = sum(-(-n // page) for n in lens)
+    p = Pool(pages, hkv, page, D, "e4m3", rng, spread=1.5)
+    tab = table(lens, page, pages, row, rng)
+    q = bf16_of(1.5 * rng.standard_normal((len(lens), hq, D)))
+    got, lse = _attend(p, q, lens, tab, page, out, scale=scale, softcap=softcap, window=window)
+    check_attention(p, okv.bf16(q), lens, tab, page, got, lse, scale or D ** -0.5, softcap, window, out == "bf16")
