@@ -53,9 +53,8 @@ constexpr int kThreads = 32 * kWarps;
 // (in powers of two): weights stay below 2^8, and most tiles rescale nothing.
 constexpr float kSlack = 8.0f;
 
-// Keys of a tile: 8 KB of k and v rows, or less (E4M3 rows of 32 elements); tiles of
-// half the keys took 35.7 us where E4M3 rows of 64 now take 33.0 (32 sequences of up
-// to 8000).
+// Keys of a tile: 8 KB of k and v rows; tiles of half the keys took 35.7 us where
+// E4M3 rows of 64 then took 33.0 (32 sequences of up to 8000).
 __host__ __device__ constexpr int tile_keys(int DP, bool F8) { return F8 && DP <= 64 ? 64 : F8 || DP <= 64 ? 32 : 16; }
 __host__ __device__ constexpr int row_bytes(int DP, bool F8) { return DP * (F8 ? 1 : 2); }
 // a tile in the ring: k rows, v rows, then (E4M3) their scale bytes
@@ -63,7 +62,7 @@ __host__ __device__ constexpr int stage_bytes(int DP, bool F8)
 {
     return 2 * tile_keys(DP, F8) * row_bytes(DP, F8) + (F8 ? 2 * tile_keys(DP, F8) : 0);
 }
-__host__ __device__ constexpr int num_stages(int DP, bool F8) { return stage_bytes(DP, F8) < 6000 ? 5 : 3; }
+constexpr int kStages = 3;      // tiles of a warp's ring
 
 // A part of a row: NROW output rows (not divided by the sums), the powers of
 // two that the sums of weights are multiples of, the sums, and (E4M3) the whole
@@ -244,12 +243,13 @@ template <int DP, int CW, bool F8, int NROW, bool FINE>
 struct Kernel {
     static constexpr int TT = tile_keys(DP, F8), ROWB = row_bytes(DP, F8), NT = TT / 8, KS = CW / 16, ND = CW / 8;
     static constexpr int C2 = row_bytes(CW, F8) / 32;        // pairs of chunks computed with
-    static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = num_stages(DP, F8);
+    static constexpr int CPR = ROWB / 16, RPI = 32 / CPR, STAGE = stage_bytes(DP, F8), STAGES = kStages;
     static constexpr int PART = part_floats(DP, F8, NROW), PROW = part_row(DP, F8), PHEAD = NROW * PROW;
     static constexpr int SCALES = F8 ? 8 * TT : 0;           // a tile's scales as numbers
     static constexpr int REGION = STAGES * STAGE + SCALES;   // a warp's ring, and at the end its parts
     static_assert(REGION % 16 == 0 && PART % 4 == 0 && 4 * (2 * PART + 4 * 2 * kWarps * NROW) <= REGION,
                   "a warp's parts, and the merge's tables, fit its ring");
+    static_assert(STAGES * (TT / 16) <= 32, "the ring's tiles have a bit per 16 keys in one word");
     static constexpr int QR = NROW == 8 ? 2 : 4;
 
     // ---- a row's state in one warp: lane 4 g + j holds row g (and g + 8 for

@@ -456,7 +456,6 @@ int moe_kv_copy_pages(moe_kv_t h, const moe_kv_pool* pools, int num_pools, const
     a.kv_bytes = page_kv_bytes(h->cfg);
     a.scale_bytes = page_scale_bytes(h->cfg);
     a.status = h->status;
-    a.sms = h->sms;
     KvGuard guard(h->device);
     cudaError_t e = cudaSuccess;
     for (int l0 = 0; l0 < num_pools && e == cudaSuccess; l0 += kCopyLayers) {

@@ -72,7 +72,6 @@ struct CopyArgs {
     int n, num_pages;
     size_t kv_bytes, scale_bytes;      // of a page's k (and v), of its k scales (and v scales)
     int* status;
-    int sms;
 };
 
 cudaError_t rope_init_device();
