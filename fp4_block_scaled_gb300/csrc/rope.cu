@@ -224,10 +224,12 @@ cudaError_t launch_gl(const RopeArgs& a, cudaStream_t s)
     const int units = a.hq + a.hk + a.hv;
     const long long lanes = (long long)a.T * GL;
     // How many lanes share a token's heads.  Few tokens: enough for 512 lanes an
-    // SM, up to one head each (measured, 48 heads of 128: 8 tokens 2.2 us with 48
-    // sharers and 4.4 with 6; 900 tokens 5.7 us with 12, 9.6 with 48).  Many tokens:
-    // eight heads each, two rounds of loads on one set of angles (16383 tokens:
-    // 64 us with 6 sharers, 70 with 12, 79 with 1).
+    // SM, up to one head each (measured, 48 heads of 128: 8 tokens 2.0 us with 48
+    // sharers and 4.1 with 6; 900 tokens 5.0 us with 10, 6.4 with 6, 8.6 with 48).
+    // Many tokens: eight heads each on one set of angles (16383 tokens: 63.6 us with
+    // 6 sharers, 67 with 10, 79 with 1; 40 heads of them half rotated: 53.9 with 5, 58
+    // with 10, 66 with 1; the E4M3 append of 16000: 63.6 with 6, 67.5 with 10, 67.8
+    // with 1).
     const long long fit = (long long)a.sms * 512 / lanes;
     const int least = (units + 7) / 8;
     const int split = (int)(fit < least ? least : fit > units ? units : fit);
