@@ -269,7 +269,9 @@ cudaError_t moe::lib_zero(void* p, size_t bytes)
 cudaError_t moe::lib_take_status(int* word, cudaStream_t s, int* v)
 {
     *v = 0;
-    cudaError_t e = cudaMemcpyAsync(v, word, sizeof(int), cudaMemcpyDeviceToHost, s);
+    // (first, so that a stream that is being captured takes no copy to v)
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(v, word, sizeof(int), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess || *v == 0) return e;
     e = cudaMemsetAsync(word, 0, sizeof(int), s);
