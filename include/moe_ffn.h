@@ -568,10 +568,13 @@ int moe_kv_append(moe_kv_t h, const moe_kv_pool* pool, const void* k, long long 
  * Scores, softmax and sums are fp32; the weights enter the product with v as
  * 16-bit terms: 16 significant bits for a bf16 output, 24 for an fp32 one
  * (E4M3: the weight times v's scale, to 2^-21 of itself or 2^-31 of the
- * sequence's largest).  A key or value that is not finite
- * makes the outputs it enters not finite, but a score of -inf is a weight of
- * zero (of all keys: as no keys); pool contents outside the keys
- * above are never used, whatever they are.  A page id outside
+ * sequence's largest).  For a bf16 output the sums over the keys may stay in
+ * the tensor core, which cuts them to 24 bits: about 2^-25 of a sum for every
+ * 16 keys, 2^-9 after a million, where the output's rounding is up to 2^-8.
+ * A key or value that is not finite makes the outputs it enters not finite,
+ * but a score of -inf is a weight of zero (of all keys: as no keys); pool
+ * contents outside the keys above are never used, whatever they are.
+ * A page id outside
  * [0, num_pages) sets MOE_ERR_BAD_INDEX and its keys are left out; so does a
  * length below 0 (taken as 0) or above the row's capacity (taken as that).
  * Deterministic.  The split of the work follows the lengths on the device,
