@@ -149,14 +149,17 @@ Wide operator*(Wide x, Wide y)
     return fast_sum(p, fma(x.hi, y.lo, fma(x.lo, y.hi, fma(x.hi, y.hi, -p))));
 }
 
+Wide operator/(Wide x, double d)
+{
+    const double q = x.hi / d;
+    return fast_sum(q, (fma(-q, d, x.hi) + x.lo) / d);
+}
+
 Wide operator/(Wide x, Wide y)
 {
-    Wide q = {x.hi / y.hi};
-    for (int i = 0; i < 2; i++) {
-        const Wide rest = x + -(q * y);
-        q = q + Wide{rest.hi / y.hi};
-    }
-    return q;
+    const double q = x.hi / y.hi;
+    const Wide rest = x + -(y * Wide{q});
+    return fast_sum(q, rest.hi / y.hi);
 }
 
 // e^x for |x| < 2^11: the series at x / 2^n below 2^-7, squared n times
@@ -167,7 +170,7 @@ Wide wide_exp(Wide x)
     n = x.hi == 0.0 || n < -7 ? 0 : n + 7;
     const Wide r = {ldexp(x.hi, -n), ldexp(x.lo, -n)};
     Wide s = {1.0};
-    for (int i = 16; i > 0; i--) s = Wide{1.0} + r * s / Wide{(double)i};
+    for (int i = 13; i > 0; i--) s = Wide{1.0} + r * s / (double)i;
     for (; n > 0; n--) s = s * s;
     return s;
 }
@@ -269,7 +272,7 @@ int moe_rope_table(int rot_dim, double base, int kind, double factor, int traine
     const Wide two_pi = {6.283185307179586, 2.4492935982947064e-16};
     const double r = rot_dim;
     Wide ln_base = wide_log(base);
-    if (kind == MOE_ROPE_SCALE_NTK) ln_base = ln_base + wide_log(factor) * Wide{r} / Wide{r - 2.0};
+    if (kind == MOE_ROPE_SCALE_NTK) ln_base = ln_base + wide_log(factor) * Wide{r} / (r - 2.0);
     double lo = 0.0, hi = 0.0;
     if (kind == MOE_ROPE_SCALE_YARN) {
         auto pair_of = [&](double t) { return r * log(trained_len / (t * two_pi.hi)) / (2.0 * log(base)); };
@@ -277,11 +280,11 @@ int moe_rope_table(int rot_dim, double base, int kind, double factor, int traine
         hi = fmin(ceil(pair_of(1.0)), r - 1.0);
     }
     for (int i = 0; i < rot_dim / 2; i++) {
-        Wide f = wide_exp(ln_base * Wide{-2.0 * i} / Wide{r});
-        if (kind == MOE_ROPE_SCALE_LINEAR) f = f / Wide{factor};
+        Wide f = wide_exp(ln_base * Wide{-2.0 * i} / r);
+        if (kind == MOE_ROPE_SCALE_LINEAR) f = f / factor;
         if (kind == MOE_ROPE_SCALE_YARN) {
-            const Wide ramp = i <= lo ? Wide{0.0} : i >= hi ? Wide{1.0} : Wide{i - lo} / Wide{hi - lo};
-            f = f * (ramp / Wide{factor} + (Wide{1.0} + -ramp));
+            const Wide ramp = i <= lo ? Wide{0.0} : i >= hi ? Wide{1.0} : Wide{i - lo} / (hi - lo);
+            f = f * (ramp / factor + (Wide{1.0} + -ramp));
         }
         f = f / two_pi;
         // f 2^64, below 2^62, to the nearest whole number
