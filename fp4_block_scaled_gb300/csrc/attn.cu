@@ -53,8 +53,8 @@ constexpr int kThreads = 32 * kWarps;
 // (in powers of two): weights stay below 2^8, and most tiles rescale nothing.
 constexpr float kSlack = 8.0f;
 
-// Keys of a tile: 8 KB of k and v rows; tiles of half the keys took 35.7 us where
-// E4M3 rows of 64 then took 33.0 (32 sequences of up to 8000).
+// Keys of a tile: 8 KB of k and v rows; with tiles of half the keys E4M3 rows of 64
+// take 37.9 us instead of 34.9 (32 sequences of up to 8000).
 __host__ __device__ constexpr int tile_keys(int DP, bool F8) { return F8 && DP <= 64 ? 64 : F8 || DP <= 64 ? 32 : 16; }
 __host__ __device__ constexpr int row_bytes(int DP, bool F8) { return DP * (F8 ? 1 : 2); }
 // a tile in the ring: k rows, v rows, then (E4M3) their scale bytes
@@ -203,7 +203,7 @@ __device__ __forceinline__ uint32_t at_chunk(uint32_t base, int r, int c)
 // Rows of up to kWhole keys stay with one warp where every warp has a tile and
 // the rows are short on the average (at most kShort tiles): a part costs more
 // than the few tiles it moves.  256 sequences of up to 30 and 100 keys: 13.4 and
-// 21.3 us when split, 10.4 and 19.2 when not; E4M3 of 100: 18.7 and 16.6.  Where
+// 21.3 us when split, 10.4 and 19.2 when not; E4M3 of 100: 19.3 and 17.4.  Where
 // warps would idle splitting wins: one E4M3 sequence of 100 keys 6.7 us, 9.7 whole.
 constexpr int kWhole = 128;
 constexpr int kShort = 16;
@@ -213,8 +213,8 @@ constexpr int kShort = 16;
 // 16), and twice that where more than half the CTAs have a row anyway (8 key heads
 // of 128, bf16, sequences x keys, without and with it: 1 x 100 7.8 and 5.3 us,
 // 1 x 512 7.8 and 7.7, 8 x 500 9.1 and 8.0, 16 x 600 14.4 and 11.5, 18 x 1000 20.5 and
-// 17.2; beyond it, 1 x 600 would take 8.4 for 7.7 and one E4M3 sequence of 1000 11.6
-// for 8.9; ragged batches gain less, 16 of up to 1000 11.7 and 11.1, or lose, 10 of
+// 17.2; beyond it, 1 x 600 would take 8.4 for 7.7 and one E4M3 sequence of 1000 11.9
+// for 9.4; ragged batches gain less, 16 of up to 1000 11.7 and 11.1, or lose, 10 of
 // up to 1000 10.1 and 10.8).  More rows than CTAs: see snap (20 x 100 8.7 and 7.9, 40 x 48
 // 8.9 and 7.3, 30 x 30, which had no join, 6.0 and 6.2).  The choice costs a line that
 // is full 0.2 us (1 x 3000: 9.0 and 9.2).
@@ -222,8 +222,8 @@ __device__ __forceinline__ uint32_t one_cta_tiles(bool f8, uint32_t rows) { retu
 
 // What a row itself (queries, output, places) costs a warp, in tiles, when the
 // line is shared out: without it the warps with many short rows end last (128
-// E4M3 sequences of up to 8000 keys, some of one key: 189 us, 181 with 1 to 4; 256 of
-// up to 1000: 72 and 54.5; 48 windows of 1000 keys: 43.8 and 36.8).
+// E4M3 sequences of up to 8000 keys, some of one key: 188 us, 177 with it; 256 of
+// up to 1000: 75.7 and 55.7; 48 windows of 1000 keys: 43.8 and 36.8).
 constexpr uint32_t kRowCost = 2;
 
 struct SplitArgs {
@@ -1424,12 +1424,12 @@ cudaError_t dispatch(int D, bool e4m3, int G, bool f32, F f)
         return G <= 8 ? type(C64(), C64(), Bf16(), N8()) : type(C64(), C64(), Bf16(), N16());
     }
     if (!e4m3) return G <= 8 ? type(C128(), C128(), Bf16(), N8()) : type(C128(), C128(), Bf16(), N16());
-    // E4M3 rows of up to 96 are computed 96 wide (32 sequences of up to 8000: 45.8 us, 52.7
+    // E4M3 rows of up to 96 are computed 96 wide (32 sequences of up to 8000: 47.8 us, 52.4
     // with 128); for bf16, which waits for memory, it makes no difference (71.3, 72.5)
     if (D <= 96) return G <= 8 ? type(C128(), C96(), E4m3(), N8()) : type(C128(), C96(), E4m3(), N16());
     // the order of the finer sums is the faster one for E4M3 rows of 128 and up to 8 heads
-    // (128 sequences of up to 8000: 171 us, 180 without), and the slower one for more heads
-    // (32 sequences: 71 and 66 us) and shorter rows (96: 50.4 and 45.8)
+    // (128 sequences of up to 8000: 176 us, 180 without), and the slower one for more heads
+    // (32 sequences: 71.7 and 65.0 us) and shorter rows (96: 48.5 and 47.8)
     return G <= 8 ? f(C128(), C128(), E4m3(), N8(), Fine()) : type(C128(), C128(), E4m3(), N16());
 }
 
