@@ -174,7 +174,7 @@ def _quantize_e2m1(x):
     a = b * _power(254 - s)[..., None]
     m = a.abs()
     code = ((m > 0.25).to(torch.uint8) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0)
-            + 8 * torch.signbit(a)).flatten(-2)
+            + 8 * torch.signbit(a).to(torch.uint8)).flatten(-2)
     return code[..., 0::2] | code[..., 1::2] << 4, s
 
 
