@@ -1,7 +1,7 @@
 """Python binding of libmoe_ffn.so (the GB300 routed FP4 MoE expert-FFN library).
 
 Argument marshalling only: every function forwards to the C entry point of the
-same name in include/moe_ffn.h.  Pointers may be given as ints or as torch
+same name in include/moe_ffn.h and include/moe_lin.h.  Pointers may be given as ints or as torch
 tensors (their data_ptr() is passed); streams as ints, torch streams or None
 (the legacy default stream).  A nonzero return code raises MoeError.  There is
 no fallback: if the CUDA library cannot be built or loaded, importing the
@@ -47,6 +47,10 @@ EXPORTS = [
     "moe_kv_pages_create", "moe_kv_pages_open", "moe_kv_pages_extend", "moe_kv_pages_fork", "moe_kv_pages_free",
     "moe_kv_pages_compact", "moe_kv_pages_row", "moe_kv_pages_length", "moe_kv_pages_free_pages",
     "moe_kv_pages_refs", "moe_kv_pages_destroy",
+]
+LIN_EXPORTS = [                     # of include/moe_lin.h
+    "moe_lin_create", "moe_lin_status", "moe_lin_destroy", "moe_rms_norm", "moe_mx_quant", "moe_mx_values",
+    "moe_linear_packed_bytes", "moe_linear_pack", "moe_linear", "moe_lin_call",
 ]
 
 MOE_KV_BF16 = 0
@@ -102,6 +106,19 @@ class moe_rope_desc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class moe_lin_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("max_tokens", "max_in")]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("n", ctypes.c_int), ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("out_features", ctypes.c_int), ("in_features", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -120,6 +137,7 @@ def lib() -> ctypes.CDLL:
         tblp = ctypes.POINTER(moe_expert_table)
         D, F, LL = ctypes.c_double, ctypes.c_float, ctypes.c_longlong
         kvcp, poolp, ropep = (ctypes.POINTER(t) for t in (moe_kv_config, moe_kv_pool, moe_rope_desc))
+        lincp, normp, linp = (ctypes.POINTER(t) for t in (moe_lin_config, moe_norm_desc, moe_linear_desc))
         sig = {
             "moe_ffn_packed_expert_bytes": (S, [cfgp]),
             "moe_ffn_create": (I, [ctypes.POINTER(P), cfgp, I]),
@@ -174,6 +192,16 @@ def lib() -> ctypes.CDLL:
             "moe_kv_pages_free_pages": (I, [P]),
             "moe_kv_pages_refs": (I, [P, I]),
             "moe_kv_pages_destroy": (None, [P]),
+            "moe_lin_create": (I, [ctypes.POINTER(P), lincp, I]),
+            "moe_lin_status": (I, [P, P]),
+            "moe_lin_destroy": (None, [P]),
+            "moe_rms_norm": (I, [P, normp, P, P, I, P, P, I, P, P, P]),
+            "moe_mx_quant": (I, [P, P, I, I, I, P, P, P]),
+            "moe_mx_values": (I, [P, I, P, P, I, I, I, P, P]),
+            "moe_linear_packed_bytes": (S, [I, I]),
+            "moe_linear_pack": (I, [P, P, P, I, I, P, P]),
+            "moe_linear": (I, [P, linp, I, P, P, I, P, I, P]),
+            "moe_lin_call": (I, [I, ctypes.c_char_p]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -620,3 +648,88 @@ def moe_kv_pages_refs(m, page: int) -> int:
 
 def moe_kv_pages_destroy(m) -> None:
     lib().moe_kv_pages_destroy(m)
+
+
+# ----------------------------------------------- norms and dense projections
+
+def lin_config(max_tokens: int = 0, max_in: int = 0) -> moe_lin_config:
+    return moe_lin_config(max_tokens, max_in)
+
+
+def moe_lin_create(cfg: moe_lin_config, device: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_lin_create(ctypes.byref(h), ctypes.byref(cfg), int(device)), "moe_lin_create")
+    return h.value
+
+
+def moe_lin_status(h, stream=None) -> int:
+    """Returns the (cleared) sticky device status code; does not raise."""
+    return lib().moe_lin_status(h, _s(stream))
+
+
+def moe_lin_destroy(h) -> None:
+    lib().moe_lin_destroy(h)
+
+
+def norm(weight, n: int, eps: float, x_dtype: int = MOE_OUT_BF16, residual_dtype: int = MOE_OUT_BF16) -> moe_norm_desc:
+    """weight: device bf16 [n], or None for ones."""
+    return moe_norm_desc(_p(weight), int(n), float(eps), int(x_dtype), int(residual_dtype))
+
+
+def linear(packed, out_features: int, in_features: int) -> moe_linear_desc:
+    """packed: moe_linear_pack's output in device memory."""
+    return moe_linear_desc(_p(packed), int(out_features), int(in_features))
+
+
+# The calls of a decode step go through moe_lin_call, as those of the cache do.
+_NORM, _QUANT, _VALUES, _LINEAR = struct.Struct("=4QqQQqQQQ"), struct.Struct("=QQqqqQQQ"), struct.Struct("=QqQQqqqQQ"), \
+    struct.Struct("=QQqQQqQqQ")
+
+
+def _lin_call(op: int, words: bytes, where: str) -> None:
+    rc = (_lib or lib()).moe_lin_call(op, words)
+    if rc:
+        raise MoeError(rc, where)
+
+
+def moe_rms_norm(h, norm: moe_norm_desc, x, T: int, residual=None, residual_out=None, out=None, act_mode: int = MOE_ACT_BF16,
+                 codes=None, scales=None, stream=None):
+    d = ctypes.addressof(norm)
+    try:
+        w = _NORM.pack(h, d, x.data_ptr(), 0 if residual is None else residual.data_ptr(), T,
+                       0 if residual_out is None else residual_out.data_ptr(), 0 if out is None else out.data_ptr(), act_mode,
+                       0 if codes is None else codes.data_ptr(), 0 if scales is None else scales.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _NORM.pack(h or 0, d, _p(x) or 0, _p(residual) or 0, T, _p(residual_out) or 0, _p(out) or 0, act_mode,
+                       _p(codes) or 0, _p(scales) or 0, _s(stream) or 0)
+    _lin_call(0, w, "moe_rms_norm")
+
+
+def moe_mx_quant(h, x, rows: int, n: int, act_mode: int, codes, scales, stream=None):
+    _lin_call(1, _QUANT.pack(h or 0, _p(x) or 0, rows, n, act_mode, _p(codes) or 0, _p(scales) or 0, _s(stream) or 0),
+              "moe_mx_quant")
+
+
+def moe_mx_values(h, act_mode: int, codes, scales, rows: int, n: int, out_dtype: int, out, stream=None):
+    _lin_call(2, _VALUES.pack(h or 0, act_mode, _p(codes) or 0, _p(scales) or 0, rows, n, out_dtype, _p(out) or 0, _s(stream) or 0),
+              "moe_mx_values")
+
+
+def moe_linear_packed_bytes(out_features: int, in_features: int) -> int:
+    return lib().moe_linear_packed_bytes(int(out_features), int(in_features))
+
+
+def moe_linear_pack(h, codes, scales, out_features: int, in_features: int, packed, stream=None):
+    _check(lib().moe_linear_pack(h, _p(codes), _p(scales), int(out_features), int(in_features), _p(packed), _s(stream)),
+           "moe_linear_pack")
+
+
+def moe_linear(h, weights: moe_linear_desc, act_mode: int, x, T: int, y, out_dtype: int, x_scales=None, stream=None):
+    """x: codes of act_mode's format with x_scales, or bf16 rows."""
+    d = ctypes.addressof(weights)
+    try:
+        w = _LINEAR.pack(h, d, act_mode, x.data_ptr(), 0 if x_scales is None else x_scales.data_ptr(), T, y.data_ptr(), out_dtype,
+                         stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _LINEAR.pack(h or 0, d, act_mode, _p(x) or 0, _p(x_scales) or 0, T, _p(y) or 0, out_dtype, _s(stream) or 0)
+    _lin_call(3, w, "moe_linear")

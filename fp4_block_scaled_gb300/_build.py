@@ -16,8 +16,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
 SOURCES = ["api.cu", "gemv.cu", "group.cu", "gemm8.cu", "pack.cu", "route.cu", "router.cu", "actquant.cu", "noalloc.cu",
-           "sched.cpp", "cache.cpp", "kv.cu", "rope.cu", "attn.cu", "pages.cu", "pages.cpp"]
-HEADERS = ["common.cuh", "internal.h", "layout.h", "rsel.cuh", "kv.h"]
+           "sched.cpp", "cache.cpp", "kv.cu", "rope.cu", "attn.cu", "pages.cu", "pages.cpp", "lin.cu", "norm.cu",
+           "mxquant.cu", "linear.cu"]
+HEADERS = ["common.cuh", "internal.h", "layout.h", "rsel.cuh", "kv.h", "lin.h", "mx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -34,7 +35,7 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "moe_ffn.h"))
+    files += [os.path.join(ROOT, "include", f) for f in ("moe_ffn.h", "moe_lin.h")]
     files.append(os.path.abspath(__file__))
     return files
 

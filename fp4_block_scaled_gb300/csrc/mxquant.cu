@@ -1,0 +1,128 @@
+// mxquant.cu -- rows to E2M1 codes with one ue8m0 scale per 32 and back, and the
+// packing of a linear layer's weights.
+#include "common.cuh"
+#include "lin.h"
+#include "mx.cuh"
+
+namespace moe {
+
+namespace {
+
+cudaError_t launch(const void* fn, long long blocks, int threads, cudaStream_t s, void** args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Eight elements a thread, four threads to a block of 32.
+__global__ void __launch_bounds__(256) k_mx_quant(MxQuantArgs a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, all = (size_t)a.rows * a.n / 8;
+    float v[8] = {};
+    if (i < all) unpack8(ldg_stream_v4(a.x + 8 * i), v);
+    int s;
+    const uint32_t codes = e2m1_codes8(v, s);
+    if (i >= all) return;
+    reinterpret_cast<uint32_t*>(a.codes)[i] = codes;
+    if (i % 4 == 0) a.scales[i / 4] = (uint8_t)s;
+}
+
+// Sixteen elements a thread; the scale is the row's block's.
+template <int E2M1, int F32>
+__global__ void __launch_bounds__(256) k_mx_values(MxValuesArgs a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = a.n / 16;
+    if (i >= (size_t)a.rows * per) return;
+    const size_t row = i / per;
+    const int c = (int)(i - row * per) * 16;
+    const int s = E2M1 ? a.scales[row * (a.n / 32) + c / 32] : a.scales[row * ((a.n + 127) / 128) + c / 128];
+    const float up = ue8m0_value(s);
+    float v[16];
+    if (E2M1) {
+        const uint2 q = *reinterpret_cast<const uint2*>(a.codes + i * 8);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const float2 f = e2m1x2_to_f32x2((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+            v[2 * j] = f.x * up;
+            v[2 * j + 1] = f.y * up;
+        }
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(a.codes + i * 16);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 16; j++) v[j] = e4m3_value(w[j / 4] >> (8 * (j & 3))) * up;
+    }
+    if (F32) {
+        float4* out = reinterpret_cast<float4*>(a.out) + i * 4;
+#pragma unroll
+        for (int j = 0; j < 4; j++) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+        uint4* out = reinterpret_cast<uint4*>(a.out) + i * 2;
+        out[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        out[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+    }
+}
+
+// One block a unit: thread r copies row r's 128 bytes of codes and its 8 scale bytes.
+__global__ void __launch_bounds__(kLinRows) k_mx_pack(MxPackArgs a, int units)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int u = (int)(blockIdx.x % (unsigned)units), r = threadIdx.x;
+    const long long row = (long long)(blockIdx.x / (unsigned)units) * kLinRows + r;
+    uint8_t* out = a.packed + (size_t)blockIdx.x * kLinUnitBytes;
+    const int k0 = u * kLinUnitK, k1 = min(a.K, k0 + kLinUnitK);
+    const bool in = row < a.N;
+    for (int c = 0; c < 8; c++) {
+        const int k = k0 + 32 * c;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        uint8_t s = 0;
+        if (in && k < k1) {
+            v = *reinterpret_cast<const uint4*>(a.codes + ((size_t)row * a.K + k) / 2);
+            s = a.scales[(size_t)row * (a.K / 32) + k / 32];
+        }
+        *reinterpret_cast<uint4*>(out + r * 128 + c * 16) = v;
+        out[kLinCodeBytes + (c / 4) * kLinAtom + (r % 32) * 16 + (r / 32) * 4 + c % 4] = s;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quant(const MxQuantArgs& a0, cudaStream_t s)
+{
+    MxQuantArgs a = a0;
+    void* args[] = {&a};
+    return launch((const void*)k_mx_quant, ((long long)a.rows * a.n / 8 + 255) / 256, 256, s, args);
+}
+
+cudaError_t launch_mx_values(const MxValuesArgs& a0, cudaStream_t s)
+{
+    MxValuesArgs a = a0;
+    void* args[] = {&a};
+    const void* fn = a.e2m1 ? (a.out_f32 ? (const void*)k_mx_values<1, 1> : (const void*)k_mx_values<1, 0>)
+                            : (a.out_f32 ? (const void*)k_mx_values<0, 1> : (const void*)k_mx_values<0, 0>);
+    return launch(fn, ((long long)a.rows * a.n / 16 + 255) / 256, 256, s, args);
+}
+
+cudaError_t launch_mx_pack(const MxPackArgs& a0, cudaStream_t s)
+{
+    MxPackArgs a = a0;
+    int units = lin_units(a.K);
+    void* args[] = {&a, &units};
+    return launch((const void*)k_mx_pack, (long long)lin_tiles(a.N) * units, kLinRows, s, args);
+}
+
+}  // namespace moe
