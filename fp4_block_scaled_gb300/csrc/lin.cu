@@ -253,7 +253,7 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
     if (!rc) rc = check_rows(N, K);
     if (rc) return rc;
     if (!w->packed || !aligned(w->packed, 128) || !aligned(x, 16) || !aligned(x_scales, 16) || !aligned(y, 16)) return MOE_ERR_INVALID_ARG;
-    if (!x_scales && !linear_takes_bf16(T) && (T > h->cfg.max_tokens || K > h->cfg.max_in)) return MOE_ERR_INVALID_ARG;
+    if (!x_scales && (T > h->cfg.max_tokens || K > h->cfg.max_in)) return MOE_ERR_INVALID_ARG;
     if ((double)T * N > 1e13 || (long long)lin_tiles(N) * lin_units(K) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !y) return MOE_ERR_INVALID_ARG;

@@ -19,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kRing = 16;                  // stages, at most
+constexpr int kMaxNt = 192;                // tokens of a tile, at most
 constexpr int kSplitMax = 8;               // CTAs of a cluster along K, at most (the portable size)
 constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 4;
 constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
@@ -26,7 +27,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct __align__(1024) Control {
-    uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2], drain;
+    uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2], drain, red;
     uint32_t tmem;
     int abort;
 };
@@ -90,6 +91,11 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -103,11 +109,24 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, float v)
+// Bulk copy from this CTA's shared memory to the same place's of another CTA of the
+// cluster, completing on its barrier.
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar, uint32_t rank)
 {
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(saddr),
-                 "r"(rank), "f"(v)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b32 d, b;\n\tmapa.shared::cluster.u32 d, %0, %4;\n\tmapa.shared::cluster.u32 b, %3, %4;\n\t"
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [d], [%1], %2, [b];\n\t}" ::"r"(dst),
+        "r"(src), "r"(bytes), "r"(bar), "r"(rank)
+        : "memory");
+}
+
+// One lane of a converged warp.  (The compiler knows by it that a single thread runs what
+// follows, and keeps the operands of the tensor core's instructions in uniform registers.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void give_up(const LinearArgs& a, Control& ctl)
@@ -125,6 +144,24 @@ __device__ __forceinline__ void store(const LinearArgs& a, long long t, long lon
         ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(v);
 }
 
+// Four features from n, a multiple of 4.
+__device__ __forceinline__ void store4(const LinearArgs& a, long long t, long long n, const float4& v)
+{
+    if (a.N % 4 == 0) {
+        if (n >= a.N) return;
+        const size_t i = (size_t)t * a.N + n;
+        if (a.out_f32)
+            *reinterpret_cast<float4*>((float*)a.y + i) = v;
+        else
+            *reinterpret_cast<uint2*>((uint16_t*)a.y + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        return;
+    }
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (n + j < a.N) store(a, t, n + j, w[j]);
+}
+
 // Four scale bytes of a row from `at`, 0 behind its end.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n)
 {
@@ -136,25 +173,88 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n
     return w;
 }
 
-// The scales of a stage's token rows into their atoms, by one warp.
+// The scales of a stage's token rows, by one warp: lane l holds those of the rows l, l +
+// 32, ..., one word for each 128 elements (E4M3: the row's byte four times).
+constexpr int kLaneRows = kMaxNt / 32;
 template <int E2M1>
-__device__ __forceinline__ void load_scales(const LinearArgs& a, const Plan& p, uint8_t* sfb, int t0, int step, int lane)
+struct Scales {
+    uint32_t w[kLaneRows][E2M1 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const LinearArgs& a, const Plan& p, int t0, int step, int lane)
+    {
+        const int n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
+#pragma unroll
+        for (int i = 0; i < kLaneRows; i++) {
+            const int r = lane + 32 * i;
+            const bool in = r < p.nt && t0 + r < a.T;
+            const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
+            if (E2M1) {
+                w[i][0] = in ? scale_word(row, 8 * step, n) : 0u;
+                w[i][E2M1] = in ? scale_word(row, 8 * step + 4, n) : 0u;
+            } else {
+                w[i][0] = in ? row[step] : 0u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(const Plan& p, uint8_t* sfb, int lane) const
+    {
+        const int atoms = p.nt > 128 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < kLaneRows; i++) {
+            if (32 * i >= p.nt) break;
+            uint8_t* at = sfb + (i / 4) * kLinAtom + lane * 16 + i % 4 * 4;
+            if (E2M1) {
+                *reinterpret_cast<uint32_t*>(at) = w[i][0];
+                *reinterpret_cast<uint32_t*>(at + atoms * kLinAtom) = w[i][E2M1];
+            } else {
+                *reinterpret_cast<uint32_t*>(at) = w[i][0] * 0x01010101u;
+            }
+        }
+    }
+};
+
+// A stage's token rows quantised from bf16 into the swizzled operand and the atoms, by one
+// warp: 256 elements a turn, a row of E2M1 or two rows of E4M3.
+template <int E2M1>
+__device__ __forceinline__ void quantise_stage(const LinearArgs& a, const Plan& p, uint8_t* st, int t0, int step, int lane)
 {
-    const int atoms = p.nt > 128 ? 2 : 1, n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
-    for (int r = lane; r < p.nt; r += 32) {
-        uint8_t* at = sfb + (r / 128) * kLinAtom + (r % 32) * 16 + (r % 128) / 32 * 4;
-        const bool in = t0 + r < a.T;
-        const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
-        if (E2M1) {
-            *reinterpret_cast<uint32_t*>(at) = in ? scale_word(row, 8 * step, n) : 0u;
-            *reinterpret_cast<uint32_t*>(at + atoms * kLinAtom) = in ? scale_word(row, 8 * step + 4, n) : 0u;
-        } else {
-            *reinterpret_cast<uint32_t*>(at) = in ? row[step] * 0x01010101u : 0u;
+    constexpr int kRows = E2M1 ? 1 : 2, kBatch = 4;
+    const int rows = min(p.nt, a.T - t0), l = E2M1 ? lane : lane % 16, k = step * (E2M1 ? 256 : 128) + 8 * l;
+    for (int r0 = 0; r0 < rows; r0 += kRows * kBatch) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            const int r = r0 + i * kRows + (E2M1 ? 0 : lane / 16);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows && k < a.K) u[i] = *reinterpret_cast<const uint4*>(a.x + (size_t)(t0 + r) * a.K + k);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            if (r0 + i * kRows >= rows) break;
+            const int r = r0 + i * kRows + (E2M1 ? 0 : lane / 16);
+            float v[8];
+            unpack8(u[i], v);
+            uint8_t* row = st + p.b + r * 128;
+            uint8_t* atom = st + p.sfb + r % 32 * 16 + r / 32 * 4;
+            int s;
+            if (E2M1) {
+                const uint32_t c = e2m1_codes8(v, s);
+                *reinterpret_cast<uint32_t*>(row + ((l / 4 ^ (r & 7)) << 4) + l % 4 * 4) = c;
+                if (l % 4 == 0) atom[l / 16 * kLinAtom + l / 4 % 4] = (uint8_t)s;
+            } else {
+                const uint2 c = e4m3_codes8(v, s);
+                if (r < rows) {
+                    *reinterpret_cast<uint2*>(row + ((l / 2 ^ (r & 7)) << 4) + l % 2 * 8) = c;
+                    if (l == 0) *reinterpret_cast<uint32_t*>(atom) = (uint32_t)s * 0x01010101u;
+                }
+            }
         }
     }
 }
 
-template <int E2M1>
+// QUANT: x is bf16, a few tokens, quantised here.
+template <int E2M1, int QUANT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, Plan p)
 {
@@ -172,8 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.acc_empty[b], 4);
         }
         mbar_init(&ctl.drain, 1);
+        mbar_init(&ctl.red, 1);
         ctl.abort = 0;
         mbar_fence_init();
+    }
+    if (warp == kWarpProd && elect_one()) {
+        prefetch_map(&wmap);
+        if (!QUANT) prefetch_map(&xmap);
     }
     if (warp == kWarpMma) tmem_alloc(&ctl.tmem, 512);
     tc_fence_before();
@@ -192,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t c = 0, it = 0;
 
     if (warp == kWarpProd) {
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = true;
             for (int i = first; i < tiles && ok; i += stride) {
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
@@ -207,10 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t* bar = &ctl.full[slot];
                     const int z = rt * p.units + (E2M1 ? k : k / 2), half = E2M1 ? 0 : k & 1;
                     const uint32_t sf = E2M1 ? 2 * kLinAtom : kLinAtom;
-                    mbar_arrive_expect_tx(bar, (E2M1 ? kLinCodeBytes : kLinCodeBytes / 2) + sf + p.nt * 128);
+                    // (expanded weights count as the bytes that were read)
+                    mbar_arrive_expect_tx(bar, (E2M1 ? kLinCodeBytes : kLinCodeBytes / 2) + sf + (QUANT ? 0 : p.nt * 128));
                     tma_3d(st, &wmap, half * 128, 0, z, bar);
                     bulk_g2s(st + p.sfa, a.packed + (size_t)z * kLinUnitBytes + kLinCodeBytes + half * kLinAtom, sf, bar);
-                    tma_2d(st + p.b, &xmap, k * 128, t0, bar);
+                    if (!QUANT) tma_2d(st + p.b, &xmap, k * 128, t0, bar);
                 }
             }
             // no copy may be in flight into this CTA's memory at its end
@@ -219,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_bounded(&ctl.full[m % p.ring], m / p.ring & 1, kWaitNs / 64);
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = true;
             for (int i = first; i < tiles && ok; i += stride, it++) {
                 const uint32_t buf = it & 1;
@@ -263,10 +369,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = k0; k < k1; k++, c++) {
                 if (c % p.loaders != (uint32_t)(warp - kWarpLoad)) continue;
                 const uint32_t slot = c % p.ring;
+                Scales<E2M1> sc;
+                if (!QUANT) sc.load(a, p, t0, k, lane);
                 ok = mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kWaitNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                load_scales<E2M1>(a, p, ring + slot * p.stage + p.sfb, t0, k, lane);
+                if (QUANT)
+                    quantise_stage<E2M1>(a, p, ring + slot * p.stage, t0, k, lane);
+                else
+                    sc.store(p, ring + slot * p.stage + p.sfb, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.full[slot]);
@@ -286,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int cols = (int)min((long long)p.nt, a.T - t0);
             const uint32_t from = tmem + buf * p.nt + ((uint32_t)(32 * warp) << 16);
+            float* mine = reinterpret_cast<float*>(ring) + 32 * warp + lane;
             for (int c0 = 0; c0 < cols; c0 += 16) {
                 float v[16];
                 tc_ld16(from + c0, v);
@@ -294,13 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 16; j++)
                         if (c0 + j < cols && n < a.N) store(a, t0 + c0 + j, n, v[j]);
                 } else {
+                    // (the ring is free: every product is done)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        const int col = c0 + j, owner = col / p.width;
-                        if (col < cols)
-                            st_cluster(smem_u32(smem + p.part) + (((rank * p.width + col - owner * p.width) * kLinRows) + 32 * warp + lane) * 4,
-                                       owner, v[j]);
-                    }
+                    for (int j = 0; j < 16; j++) mine[(c0 + j) * kLinRows] = v[j];
                 }
             }
             tc_fence_before();
@@ -310,20 +418,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (p.split > 1) {
-        // (one tile a cluster)
-        cluster_sync();
-        if (warp < 4 && !*(volatile int*)&ctl.abort) {
-            const long long t0 = (long long)(first / p.rtiles) * p.nt, n = (long long)(first % p.rtiles) * kLinRows + 32 * warp + lane;
-            const float* part = reinterpret_cast<const float*>(smem + p.part) + 32 * warp + lane;
-            const int cols = (int)min((long long)p.nt, a.T - t0);
-            for (int j = 0; j < p.width; j++) {
-                const int col = (int)rank * p.width + j;
-                if (col >= cols) break;
-                float v = 0.0f;
-                for (int s = 0; s < p.split; s++) v += part[(s * p.width + j) * kLinRows];
-                if (n < a.N) store(a, t0 + col, n, v);
+        // One tile a cluster.  CTA r adds up the columns r * width ..: every CTA sends it its
+        // own sums of them, and they are added in the CTAs' order.
+        if (warp < 4) {
+            const long long t0 = (long long)(first / p.rtiles) * p.nt, n0 = (long long)(first % p.rtiles) * kLinRows + 4 * lane;
+            const int cols = (int)min((long long)p.nt, a.T - t0), here = min(p.width, cols - (int)rank * p.width);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            named_sync(1, 128);
+            if (warp == 0 && elect_one()) {
+                if (here > 0) mbar_arrive_expect_tx(&ctl.red, p.split * here * kLinRows * 4);
+                for (int o = 0; o < p.split; o++) {
+                    const int m = min(p.width, cols - o * p.width);
+                    if (m > 0)
+                        bulk_to_peer(smem_u32(smem + p.part) + rank * p.width * kLinRows * 4, smem_u32(ring) + o * p.width * kLinRows * 4,
+                                     m * kLinRows * 4, smem_u32(&ctl.red), o);
+                }
+            }
+            if (here > 0) {
+                bool ok = mbar_wait_bounded(&ctl.red, 0, kWaitNs);
+                if (!ok) give_up(a, ctl);
+                const float4* part = reinterpret_cast<const float4*>(smem + p.part) + lane;
+                for (int j = warp; j < here && ok; j += 4) {
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int r = 0; r < kSplitMax; r++)
+                        if (r < p.split) {
+                            const float4 w = part[(r * p.width + j) * (kLinRows / 4)];
+                            v.x += w.x;
+                            v.y += w.y;
+                            v.z += w.z;
+                            v.w += w.w;
+                        }
+                    store4(a, t0 + rank * p.width + j, n0, v);
+                }
             }
         }
+        __syncwarp();
+        cluster_sync();     // nobody's memory is still read
     }
     tc_fence_before();
     __syncthreads();
@@ -335,6 +466,7 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;
+int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
 
 cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
                    const cuuint64_t* strides, const cuuint32_t* box)
@@ -351,7 +483,7 @@ Plan make_plan(const LinearArgs& a)
     Plan best{};
     double least = 0;
     const int rtiles = lin_tiles(a.N), steps = a.e2m1 ? lin_units(a.K) : (a.K + 127) / 128;
-    const int j0 = (a.T + 191) / 192;
+    const int j0 = (a.T + kMaxNt - 1) / kMaxNt;
     for (int j = j0; j < j0 + 4; j++) {
         Plan p{};
         p.nt = ((a.T + j - 1) / j + 15) / 16 * 16;
@@ -360,12 +492,14 @@ Plan make_plan(const LinearArgs& a)
         p.steps = steps;
         p.units = lin_units(a.K);
         const long long tiles = (long long)p.ttiles * rtiles;
-        p.split = (int)std::max(1LL, std::min({(long long)kSplitMax, a.sms / tiles, (long long)steps}));
-        const double waves = (double)((tiles * p.split + a.sms - 1) / a.sms);
-        const double cost = waves * (((steps + p.split - 1) / p.split) * std::max(p.nt, 64) + 512.0) + p.split * 64.0;
-        if (j == j0 || cost < least) {
-            least = cost;
-            best = p;
+        for (p.split = 1; p.split <= std::min(kSplitMax, steps); p.split++) {
+            if (p.split > 1 && tiles > g_clusters[p.split]) continue;
+            const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
+            const double cost = waves * (((steps + p.split - 1) / p.split) * std::max(p.nt, 64) + 512.0) + p.split * 64.0;
+            if (least == 0 || cost < least) {
+                least = cost;
+                best = p;
+            }
         }
     }
     Plan p = best;
@@ -378,7 +512,7 @@ Plan make_plan(const LinearArgs& a)
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0;
     p.sfcols = 4 * h * (1 + sf);
     p.ring = std::min({kRing, (int)((kSmemMax - sizeof(Control) - part) / p.stage), (512 - 2 * p.nt) / p.sfcols,
-                       std::max(2, (int)(p.split > 1 ? (steps + p.split - 1) / p.split : kRing))});
+                       std::max(3, (int)(p.split > 1 ? (steps + p.split - 1) / p.split : kRing))});
     p.loaders = std::min(kLoadWarps, p.ring);
     p.part = sizeof(Control) + p.ring * p.stage;
     // (more than half an SM's, so that no two CTAs of clusters share one and wait for each other's tensor memory)
@@ -388,7 +522,10 @@ Plan make_plan(const LinearArgs& a)
 
 }  // namespace
 
-bool linear_takes_bf16(int) { return false; }
+const void* const kKernels[4] = {(const void*)k_linear<0, 0>, (const void*)k_linear<1, 0>, (const void*)k_linear<0, 1>,
+                                 (const void*)k_linear<1, 1>};
+
+bool linear_takes_bf16(int T) { return T <= 16; }
 
 cudaError_t linear_init_device()
 {
@@ -400,9 +537,25 @@ cudaError_t linear_init_device()
         if (got != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
         g_encode = (EncodeTiled)fn;
     }
-    for (const void* fn : {(const void*)k_linear<0>, (const void*)k_linear<1>}) {
+    for (const void* fn : kKernels) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
         if (e != cudaSuccess) return e;
+    }
+    for (int split = 2; split <= kSplitMax; split++) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)split);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemMax;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&g_clusters[split], kKernels[0], &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            g_clusters[split] = 0;
+        }
     }
     return cudaSuccess;
 }
@@ -411,7 +564,7 @@ cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
 {
     LinearArgs a = a0;
     Plan p = make_plan(a);
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap{};
     const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)p.rtiles * p.units};
     const cuuint64_t ws[2] = {128, kLinUnitBytes};
     const cuuint32_t wb[3] = {128, kLinRows, 1};
@@ -420,7 +573,7 @@ cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
     const cuuint64_t width = a.e2m1 ? a.K / 2 : a.K;
     const cuuint64_t xd[2] = {width, (cuuint64_t)a.T}, xs[1] = {width};
     const cuuint32_t xb[2] = {128, (cuuint32_t)p.nt};
-    e = encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
+    if (a.codes) e = encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)p.ttiles * p.rtiles;
     cudaLaunchConfig_t cfg = {};
@@ -438,7 +591,7 @@ cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
     void* args[] = {&wmap, &xmap, &a, &p};
-    return cudaLaunchKernelExC(&cfg, a.e2m1 ? (const void*)k_linear<1> : (const void*)k_linear<0>, args);
+    return cudaLaunchKernelExC(&cfg, kKernels[(a.codes ? 0 : 2) + a.e2m1], args);
 }
 
 }  // namespace moe
