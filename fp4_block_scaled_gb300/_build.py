@@ -17,8 +17,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
 SOURCES = ["api.cu", "gemv.cu", "group.cu", "gemm8.cu", "pack.cu", "route.cu", "router.cu", "actquant.cu", "noalloc.cu",
            "sched.cpp", "cache.cpp", "kv.cu", "rope.cu", "attn.cu", "pages.cu", "pages.cpp", "lin.cu", "norm.cu",
-           "mxquant.cu", "linear.cu"]
-HEADERS = ["common.cuh", "internal.h", "layout.h", "rsel.cuh", "kv.h", "lin.h", "mx.cuh"]
+           "mxquant.cu", "linear.cu", "linear_pair.cu"]
+HEADERS = ["common.cuh", "internal.h", "layout.h", "rsel.cuh", "kv.h", "lin.h", "mx.cuh", "linear.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -37,8 +37,9 @@ cudaError_t launch_mx_pack(const MxPackArgs& a, cudaStream_t s);
 struct MxQuantArgs {
     const uint16_t* x;          // bf16 [rows][n]
     int rows, n;
-    uint8_t* codes;             // [rows][n / 2]
-    uint8_t* scales;            // [rows][n / 32]
+    int e2m1;                   // else E4M3
+    uint8_t* codes;             // [rows][n / 2], or [rows][n]
+    uint8_t* scales;            // [rows][n / 32], or [rows][ceil(n / 128)]
 };
 cudaError_t launch_mx_quant(const MxQuantArgs& a, cudaStream_t s);
 
@@ -82,6 +83,10 @@ struct LinearArgs {
 // Whether the kernel quantises bf16 rows itself; else they are quantised ahead of it.
 bool linear_takes_bf16(int T);
 cudaError_t linear_init_device();
+// Many tokens on pairs of CTAs (linear_pair.cu), and how many pairs run at once.
+int linear_pairs();
+cudaError_t linear_pair_init_device();
+cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace moe

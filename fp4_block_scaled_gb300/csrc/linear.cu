@@ -6,13 +6,9 @@
 // multiple of 16).  A stage of the ring is 128 bytes of K of both operands, which TMA
 // brings in the 128-byte swizzle that the MMA reads: 256 elements of E2M1, or 128 of
 // E4M3, for which TMA expands the weights to a byte an element on their way.
-#include <cuda.h>
-
 #include <algorithm>
 
-#include "common.cuh"
-#include "lin.h"
-#include "mx.cuh"
+#include "linear.cuh"
 
 namespace moe {
 
@@ -23,8 +19,6 @@ constexpr int kMaxNt = 192;                // tokens of a tile, at most
 constexpr int kSplitMax = 8;               // CTAs of a cluster along K, at most (the portable size)
 constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 4;
 constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct __align__(1024) Control {
     uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2], drain, red;
@@ -49,12 +43,6 @@ struct Plan {
     int sfcols;                 // tensor memory columns of a stage's scales
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-
 template <int E2M1>
 __device__ __forceinline__ uint32_t idesc(uint32_t n, uint32_t sf)
 {
@@ -74,145 +62,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
             "l"(a), "l"(b), "r"(id), "r"(acc), "r"(sfa), "r"(sfb)
             : "memory");
 }
-
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Every thread of every CTA of the cluster.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// Bulk copy from this CTA's shared memory to the same place's of another CTA of the
-// cluster, completing on its barrier.
-__device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar, uint32_t rank)
-{
-    asm volatile(
-        "{\n\t.reg .b32 d, b;\n\tmapa.shared::cluster.u32 d, %0, %4;\n\tmapa.shared::cluster.u32 b, %3, %4;\n\t"
-        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [d], [%1], %2, [b];\n\t}" ::"r"(dst),
-        "r"(src), "r"(bytes), "r"(bar), "r"(rank)
-        : "memory");
-}
-
-// One lane of a converged warp.  (The compiler knows by it that a single thread runs what
-// follows, and keeps the operands of the tensor core's instructions in uniform registers.)
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ void give_up(const LinearArgs& a, Control& ctl)
-{
-    atomicOr(a.status, kStatusTimeout);
-    *(volatile int*)&ctl.abort = 1;
-}
-
-__device__ __forceinline__ void store(const LinearArgs& a, long long t, long long n, float v)
-{
-    const size_t i = (size_t)t * a.N + n;
-    if (a.out_f32)
-        ((float*)a.y)[i] = v;
-    else
-        ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(v);
-}
-
-// Four features from n, a multiple of 4.
-__device__ __forceinline__ void store4(const LinearArgs& a, long long t, long long n, const float4& v)
-{
-    if (a.N % 4 == 0) {
-        if (n >= a.N) return;
-        const size_t i = (size_t)t * a.N + n;
-        if (a.out_f32)
-            *reinterpret_cast<float4*>((float*)a.y + i) = v;
-        else
-            *reinterpret_cast<uint2*>((uint16_t*)a.y + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-        return;
-    }
-    const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (n + j < a.N) store(a, t, n + j, w[j]);
-}
-
-// Four scale bytes of a row from `at`, 0 behind its end.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n)
-{
-    if (n % 4 == 0) return at < n ? *reinterpret_cast<const uint32_t*>(row + at) : 0u;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (at + i < n) w |= (uint32_t)row[at + i] << (8 * i);
-    return w;
-}
-
-// The scales of a stage's token rows, by one warp: lane l holds those of the rows l, l +
-// 32, ..., one word for each 128 elements (E4M3: the row's byte four times).
-constexpr int kLaneRows = kMaxNt / 32;
-template <int E2M1>
-struct Scales {
-    uint32_t w[kLaneRows][E2M1 ? 2 : 1];
-
-    __device__ __forceinline__ void load(const LinearArgs& a, const Plan& p, int t0, int step, int lane)
-    {
-        const int n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
-#pragma unroll
-        for (int i = 0; i < kLaneRows; i++) {
-            const int r = lane + 32 * i;
-            const bool in = r < p.nt && t0 + r < a.T;
-            const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
-            if (E2M1) {
-                w[i][0] = in ? scale_word(row, 8 * step, n) : 0u;
-                w[i][E2M1] = in ? scale_word(row, 8 * step + 4, n) : 0u;
-            } else {
-                w[i][0] = in ? row[step] : 0u;
-            }
-        }
-    }
-
-    __device__ __forceinline__ void store(const Plan& p, uint8_t* sfb, int lane) const
-    {
-        const int atoms = p.nt > 128 ? 2 : 1;
-#pragma unroll
-        for (int i = 0; i < kLaneRows; i++) {
-            if (32 * i >= p.nt) break;
-            uint8_t* at = sfb + (i / 4) * kLinAtom + lane * 16 + i % 4 * 4;
-            if (E2M1) {
-                *reinterpret_cast<uint32_t*>(at) = w[i][0];
-                *reinterpret_cast<uint32_t*>(at + atoms * kLinAtom) = w[i][E2M1];
-            } else {
-                *reinterpret_cast<uint32_t*>(at) = w[i][0] * 0x01010101u;
-            }
-        }
-    }
-};
 
 // A stage's token rows quantised from bf16 into the swizzled operand and the atoms, by one
 // warp: 256 elements a turn, a row of E2M1 or two rows of E4M3.
@@ -303,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
                 for (int k = k0; k < k1; k++, c++) {
                     const uint32_t slot = c % p.ring;
-                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kWaitNs)) {
-                        give_up(a, ctl);
+                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
+                        give_up(a, &ctl.abort);
                         ok = false;
                         break;
                     }
@@ -321,19 +170,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // no copy may be in flight into this CTA's memory at its end
             for (uint32_t m = c > (uint32_t)p.ring ? c - p.ring : 0; m < c; m++)
-                if (!mbar_wait_or_abort(&ctl.full[m % p.ring], m / p.ring & 1, &ctl.abort, kWaitNs))
-                    mbar_wait_bounded(&ctl.full[m % p.ring], m / p.ring & 1, kWaitNs / 64);
+                if (!mbar_wait_or_abort(&ctl.full[m % p.ring], m / p.ring & 1, &ctl.abort, kLinWaitNs))
+                    mbar_wait_bounded(&ctl.full[m % p.ring], m / p.ring & 1, kLinWaitNs / 64);
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
             bool ok = true;
             for (int i = first; i < tiles && ok; i += stride, it++) {
                 const uint32_t buf = it & 1;
-                ok = mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, kWaitNs);
+                ok = mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, kLinWaitNs);
                 const uint32_t acc = tmem + buf * p.nt;
                 for (int k = k0; k < k1 && ok; k++, c++) {
                     const uint32_t slot = c % p.ring;
-                    ok = mbar_wait_or_abort(&ctl.full[slot], c / p.ring & 1, &ctl.abort, kWaitNs);
+                    ok = mbar_wait_or_abort(&ctl.full[slot], c / p.ring & 1, &ctl.abort, kLinWaitNs);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(ring + slot * p.stage);
@@ -357,9 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {
                 // (else the epilogue has waited for the last product)
-                give_up(a, ctl);
+                give_up(a, &ctl.abort);
                 tc_commit(&ctl.drain);
-                mbar_wait_bounded(&ctl.drain, 0, kWaitNs);
+                mbar_wait_bounded(&ctl.drain, 0, kLinWaitNs);
             }
         }
     } else if (warp >= kWarpLoad) {
@@ -369,29 +218,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = k0; k < k1; k++, c++) {
                 if (c % p.loaders != (uint32_t)(warp - kWarpLoad)) continue;
                 const uint32_t slot = c % p.ring;
-                Scales<E2M1> sc;
-                if (!QUANT) sc.load(a, p, t0, k, lane);
-                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kWaitNs);
+                Scales<E2M1, kMaxNt> sc;
+                if (!QUANT) sc.load(a, p.nt, t0, k, lane);
+                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (QUANT)
                     quantise_stage<E2M1>(a, p, ring + slot * p.stage, t0, k, lane);
                 else
-                    sc.store(p, ring + slot * p.stage + p.sfb, lane);
+                    sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.full[slot]);
             }
         }
-        if (!ok && lane == 0) give_up(a, ctl);
+        if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
         for (int i = first; i < tiles; i += stride, it++) {
             const long long t0 = (long long)(i / p.rtiles) * p.nt, n = (long long)(i % p.rtiles) * kLinRows + 32 * warp + lane;
             const uint32_t buf = it & 1;
-            bool ok = mbar_wait_or_abort(&ctl.acc_full[buf], it >> 1 & 1, &ctl.abort, kWaitNs);
+            bool ok = mbar_wait_or_abort(&ctl.acc_full[buf], it >> 1 & 1, &ctl.abort, kLinWaitNs);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
-                if (lane == 0) give_up(a, ctl);
+                if (lane == 0) give_up(a, &ctl.abort);
                 break;
             }
             tc_fence_after();
@@ -435,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (here > 0) {
-                bool ok = mbar_wait_bounded(&ctl.red, 0, kWaitNs);
-                if (!ok) give_up(a, ctl);
+                bool ok = mbar_wait_bounded(&ctl.red, 0, kLinWaitNs);
+                if (!ok) give_up(a, &ctl.abort);
                 const float4* part = reinterpret_cast<const float4*>(smem + p.part) + lane;
                 for (int j = warp; j < here && ok; j += 4) {
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -467,16 +316,6 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;
 int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
-
-cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box)
-{
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return g_encode(map, type, (cuuint32_t)rank, (void*)base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
 
 Plan make_plan(const LinearArgs& a)
 {
@@ -511,16 +350,26 @@ Plan make_plan(const LinearArgs& a)
     p.width = (p.nt + p.split - 1) / p.split;
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0;
     p.sfcols = 4 * h * (1 + sf);
-    p.ring = std::min({kRing, (int)((kSmemMax - sizeof(Control) - part) / p.stage), (512 - 2 * p.nt) / p.sfcols,
+    p.ring = std::min({kRing, (int)((kLinSmemMax - sizeof(Control) - part) / p.stage), (512 - 2 * p.nt) / p.sfcols,
                        std::max(3, (int)(p.split > 1 ? (steps + p.split - 1) / p.split : kRing))});
     p.loaders = std::min(kLoadWarps, p.ring);
     p.part = sizeof(Control) + p.ring * p.stage;
     // (more than half an SM's, so that no two CTAs of clusters share one and wait for each other's tensor memory)
-    p.smem = std::max(p.part + part, kSmemMax / 2 + 2048);
+    p.smem = std::max(p.part + part, kLinSmemMax / 2 + 2048);
     return p;
 }
 
 }  // namespace
+
+cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box)
+{
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return g_encode(map, type, (cuuint32_t)rank, (void*)base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
 
 const void* const kKernels[4] = {(const void*)k_linear<0, 0>, (const void*)k_linear<1, 0>, (const void*)k_linear<0, 1>,
                                  (const void*)k_linear<1, 1>};
@@ -538,14 +387,14 @@ cudaError_t linear_init_device()
         g_encode = (EncodeTiled)fn;
     }
     for (const void* fn : kKernels) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmemMax);
         if (e != cudaSuccess) return e;
     }
     for (int split = 2; split <= kSplitMax; split++) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)split);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemMax;
+        cfg.dynamicSmemBytes = kLinSmemMax;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)split;
@@ -557,23 +406,24 @@ cudaError_t linear_init_device()
             g_clusters[split] = 0;
         }
     }
-    return cudaSuccess;
+    return linear_pair_init_device();
 }
 
 cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
 {
     LinearArgs a = a0;
+    if (a.codes && a.T > 512) return launch_linear_pair(a, s);
     Plan p = make_plan(a);
     CUtensorMap wmap, xmap{};
     const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)p.rtiles * p.units};
     const cuuint64_t ws[2] = {128, kLinUnitBytes};
     const cuuint32_t wb[3] = {128, kLinRows, 1};
-    cudaError_t e = encode(&wmap, a.e2m1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, a.packed, wd, ws, wb);
+    cudaError_t e = linear_map(&wmap, a.e2m1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, a.packed, wd, ws, wb);
     if (e != cudaSuccess) return e;
     const cuuint64_t width = a.e2m1 ? a.K / 2 : a.K;
     const cuuint64_t xd[2] = {width, (cuuint64_t)a.T}, xs[1] = {width};
     const cuuint32_t xb[2] = {128, (cuuint32_t)p.nt};
-    if (a.codes) e = encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
+    if (a.codes) e = linear_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)p.ttiles * p.rtiles;
     cudaLaunchConfig_t cfg = {};

@@ -1,0 +1,185 @@
+// linear.cuh -- what the two kernels of the dense product share: operand descriptors,
+// TMA and cluster helpers, the scales of token rows.
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+#include "lin.h"
+#include "mx.cuh"
+
+namespace moe {
+
+constexpr uint64_t kLinWaitNs = 2000000000ull;
+constexpr uint32_t kLinSmemMax = 227 * 1024;
+
+// K-major operand of 128-byte rows in TMA's 128-byte swizzle, groups of 8 rows of 1 KB.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Bulk copy from this CTA's shared memory to the same place's of another CTA of the
+// cluster, completing on its barrier.
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{\n\t.reg .b32 d, b;\n\tmapa.shared::cluster.u32 d, %0, %4;\n\tmapa.shared::cluster.u32 b, %3, %4;\n\t"
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [d], [%1], %2, [b];\n\t}" ::"r"(dst),
+        "r"(src), "r"(bytes), "r"(bar), "r"(rank)
+        : "memory");
+}
+
+// One lane of a converged warp.  (The compiler knows by it that a single thread runs what
+// follows, and keeps the operands of the tensor core's instructions in uniform registers.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void give_up(const LinearArgs& a, int* abort)
+{
+    atomicOr(a.status, kStatusTimeout);
+    *(volatile int*)abort = 1;
+}
+
+__device__ __forceinline__ void store(const LinearArgs& a, long long t, long long n, float v)
+{
+    const size_t i = (size_t)t * a.N + n;
+    if (a.out_f32)
+        ((float*)a.y)[i] = v;
+    else
+        ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(v);
+}
+
+// Four features from n, a multiple of 4.
+__device__ __forceinline__ void store4(const LinearArgs& a, long long t, long long n, const float4& v)
+{
+    if (a.N % 4 == 0) {
+        if (n >= a.N) return;
+        const size_t i = (size_t)t * a.N + n;
+        if (a.out_f32)
+            *reinterpret_cast<float4*>((float*)a.y + i) = v;
+        else
+            *reinterpret_cast<uint2*>((uint16_t*)a.y + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        return;
+    }
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (n + j < a.N) store(a, t, n + j, w[j]);
+}
+
+// Warp-collective, without waiting: 32 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// A whole sector of 32 bytes by one thread.
+__device__ __forceinline__ void st_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
+// Four scale bytes of a row from `at`, 0 behind its end.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n)
+{
+    if (n % 4 == 0) return at < n ? *reinterpret_cast<const uint32_t*>(row + at) : 0u;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        if (at + i < n) w |= (uint32_t)row[at + i] << (8 * i);
+    return w;
+}
+
+// The scales of a stage's token rows, by one warp: lane l holds those of the rows l, l +
+// 32, ..., one word for each 128 elements (E4M3: the row's byte four times).
+template <int E2M1, int ROWS>
+struct Scales {
+    uint32_t w[ROWS / 32][E2M1 ? 2 : 1];
+
+    // rows of the tile from t0, `rows` of them
+    __device__ __forceinline__ void load(const LinearArgs& a, int rows, int t0, int step, int lane)
+    {
+        const int n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; i++) {
+            const int r = lane + 32 * i;
+            const bool in = r < rows && t0 + r < a.T;
+            const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
+            if (E2M1) {
+                w[i][0] = in ? scale_word(row, 8 * step, n) : 0u;
+                w[i][E2M1] = in ? scale_word(row, 8 * step + 4, n) : 0u;
+            } else {
+                w[i][0] = in ? row[step] : 0u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(int rows, uint8_t* atoms, int lane) const
+    {
+        const int per = rows > 128 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; i++) {
+            if (32 * i >= rows) break;
+            uint8_t* at = atoms + (i / 4) * kLinAtom + lane * 16 + i % 4 * 4;
+            if (E2M1) {
+                *reinterpret_cast<uint32_t*>(at) = w[i][0];
+                *reinterpret_cast<uint32_t*>(at + per * kLinAtom) = w[i][E2M1];
+            } else {
+                *reinterpret_cast<uint32_t*>(at) = w[i][0] * 0x01010101u;
+            }
+        }
+    }
+};
+
+// A tensor map for TMA loads of 128-byte rows in the 128-byte swizzle.
+cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box);
+
+}  // namespace moe

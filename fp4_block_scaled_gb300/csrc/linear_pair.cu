@@ -1,0 +1,368 @@
+// linear_pair.cu -- the dense product for many tokens: pairs of CTAs
+// (tcgen05 cta_group::2), one tile of 256 tokens by 256 features a pair.
+//
+// The tokens are the MMA's rows here, 128 of each CTA, so that a thread of the epilogue
+// holds consecutive features of one token; each CTA brings its own tokens and half of
+// the features, a packed tile of 128, and the tensor cores read the other half from the
+// other CTA's shared memory.
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRing = 6;
+constexpr int kTokens = 256, kFeatures = 256;
+constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 4;
+constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
+// Tensor memory: the accumulators of two tiles in turn, which share kShared columns, and
+// behind them the scales of two stages (E4M3: four).  The epilogue empties the shared columns
+// first, and then the next tile's products may begin.
+constexpr int kShared = 48, kScaleCols = 2 * kFeatures - kShared;
+
+struct __align__(1024) Control {
+    uint64_t full[kRing], peer[kRing], empty[kRing], acc_full, acc_empty, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+template <int E2M1>
+struct Stage {
+    static constexpr int kAtoms = E2M1 ? 2 : 1;                 // of 128 elements
+    static constexpr uint32_t b = 128 * 128, sfa = 2 * b, sfb = sfa + kAtoms * kLinAtom;
+    static constexpr uint32_t bytes = (sfb + 2 * kAtoms * kLinAtom + 1023) / 1024 * 1024;
+    static constexpr int cols = 12 * kAtoms, slots = kShared / cols;
+    static_assert(sizeof(Control) + kRing * bytes <= kLinSmemMax && kLoadWarps <= kRing && slots >= 2, "sizes");
+};
+
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank)
+{
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tmbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(
+                     smem_u32(bar)),
+                 "r"(rank)
+                 : "memory");
+}
+
+__device__ __forceinline__ void commit_both(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <int E2M1>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sfa, uint32_t sfb, uint32_t acc)
+{
+    if (E2M1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(acc), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(acc), "r"(sfa), "r"(sfb)
+            : "memory");
+}
+
+// A: the rows (E2M1 1, or E4M3 0); B: the weights (E2M1, 1 of kind::mxf4 and 5 of
+// kind::mxf8f6f4); ue8m0 scales, whose bytes `sf` selects.
+template <int E2M1>
+__device__ __forceinline__ constexpr uint32_t idesc(uint32_t sf)
+{
+    return (E2M1 ? (1u << 7) | (1u << 10) : (5u << 10)) | ((uint32_t)(kFeatures >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(kTokens >> 4) << 24) | (sf << 29) | (sf << 4);
+}
+
+// 32 features of one token from n.
+template <int F32>
+__device__ __forceinline__ void store32(const LinearArgs& a, long long t, int n, const uint32_t (&r)[32], bool wide)
+{
+    const size_t i = (size_t)t * a.N + n;
+    if (wide && n + 32 <= a.N) {
+        if (F32) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) st_v8((float*)a.y + i + j, r[j], r[j + 1], r[j + 2], r[j + 3], r[j + 4], r[j + 5], r[j + 6], r[j + 7]);
+        } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; j++) w[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) st_v8((uint16_t*)a.y + i + 2 * j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j++)
+        if (n + j < a.N) {
+            if (F32)
+                ((float*)a.y)[i + j] = __uint_as_float(r[j]);
+            else
+                ((__nv_bfloat16*)a.y)[i + j] = __float2bfloat16_rn(__uint_as_float(r[j]));
+        }
+}
+
+template <int E2M1, int F32>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int ftiles, int units)
+{
+    using S = Stage<E2M1>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Control& ctl = *reinterpret_cast<Control*>(smem);
+    uint8_t* ring = smem + sizeof(Control);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; s++) {
+            mbar_init(&ctl.full[s], 2);
+            mbar_init(&ctl.peer[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        mbar_init(&ctl.acc_full, 1);
+        mbar_init(&ctl.acc_empty, 8);
+        mbar_init(&ctl.drain, 1);
+        ctl.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kWarpProd && elect_one()) {
+        prefetch_map(&wmap);
+        prefetch_map(&xmap);
+    }
+    if (warp == kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    pdl_trigger();
+    pdl_wait();
+
+    const int steps = E2M1 ? units : (a.K + 127) / 128;
+    const int tiles = (int)((a.T + kTokens - 1LL) / kTokens) * ftiles, first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const int rtiles = (a.N + kLinRows - 1) / kLinRows;
+    uint32_t c = 0, it = 0;
+
+    if (warp == kWarpProd) {
+        if (elect_one()) {
+            bool ok = true;
+            for (int i = first; i < tiles && ok; i += stride) {
+                const int f = i % ftiles, t0 = i / ftiles * kTokens + (int)rank * 128;
+                // (a pair's second tile of weights may be behind the last: its features are not stored)
+                const int w0 = min(2 * f, rtiles - 1) * units, w1 = min(2 * f + 1, rtiles - 1) * units;
+                for (int k = 0; k < steps; k++, c++) {
+                    const uint32_t slot = c % kRing;
+                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
+                        give_up(a, &ctl.abort);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = ring + slot * S::bytes;
+                    uint64_t* bar = &ctl.full[slot];
+                    const int u = E2M1 ? k : k / 2, half = E2M1 ? 0 : k & 1;
+                    const uint32_t sf = S::kAtoms * kLinAtom;
+                    // (expanded weights count as the bytes that were read)
+                    mbar_arrive_expect_tx(bar, 128 * 128 + (E2M1 ? 128 * 128 : 128 * 64) + 2 * sf);
+                    tma_2d(st, &xmap, k * 128, t0, bar);
+                    tma_3d(st + S::b, &wmap, half * 128, 0, (rank ? w1 : w0) + u, bar);
+                    const uint8_t* scales = a.packed + kLinCodeBytes + half * kLinAtom;
+#pragma unroll
+                    for (int h = 0; h < S::kAtoms; h++) {
+                        // atom h of both tiles of weights, side by side
+                        bulk_g2s(st + S::sfb + 2 * h * kLinAtom, scales + (size_t)(w0 + u) * kLinUnitBytes + h * kLinAtom, kLinAtom, bar);
+                        bulk_g2s(st + S::sfb + (2 * h + 1) * kLinAtom, scales + (size_t)(w1 + u) * kLinUnitBytes + h * kLinAtom, kLinAtom, bar);
+                    }
+                }
+            }
+            for (uint32_t m = c > (uint32_t)kRing ? c - kRing : 0; m < c; m++)
+                if (!mbar_wait_or_abort(&ctl.full[m % kRing], m / kRing & 1, &ctl.abort, kLinWaitNs))
+                    mbar_wait_bounded(&ctl.full[m % kRing], m / kRing & 1, kLinWaitNs / 64);
+        }
+    } else if (warp == kWarpMma) {
+        if (elect_one()) {
+            bool ok = true;
+            for (int i = first; i < tiles && ok; i += stride, it++) {
+                const uint32_t acc = tmem + (it & 1) * (kFeatures - kShared);
+                // the tile before has left the shared columns (and with them the one before it everything)
+                if (rank == 0 && it > 0) ok = mbar_wait_or_abort(&ctl.acc_empty, (it - 1) & 1, &ctl.abort, kLinWaitNs);
+                for (int k = 0; k < steps && ok; k++, c++) {
+                    const uint32_t slot = c % kRing, parity = c / kRing & 1;
+                    ok = mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs);
+                    if (!ok) break;
+                    if (rank != 0) {                            // tell the CTA that issues for both
+                        arrive_at(&ctl.peer[slot], 0);
+                        continue;
+                    }
+                    ok = mbar_wait_or_abort(&ctl.peer[slot], parity, &ctl.abort, kLinWaitNs);
+                    // the scales' columns are free once the products that read them are done
+                    const uint32_t before = c - S::slots;
+                    if (ok && c >= (uint32_t)S::slots)
+                        ok = mbar_wait_or_abort(&ctl.empty[before % kRing], before / kRing & 1, &ctl.abort, kLinWaitNs);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(ring + slot * S::bytes);
+                    const uint32_t sfa = tmem + kScaleCols + c % S::slots * S::cols, sfb = sfa + 4 * S::kAtoms;
+                    const uint64_t sd = umma_desc(st + S::sfa, 16, 128), ad = desc_sw128(st);
+#pragma unroll
+                    for (int h = 0; h < S::kAtoms; h++) cp_scales(sfa + 4 * h, sd + h * (kLinAtom / 16));
+#pragma unroll
+                    for (int h = 0; h < 2 * S::kAtoms; h++) cp_scales(sfb + 4 * h, sd + (S::kAtoms + h) * (kLinAtom / 16));
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int h = E2M1 ? j / 2 : 0;
+                        mma<E2M1>(acc, ad + 2 * j, ad + S::b / 16 + 2 * j, idesc<E2M1>(E2M1 ? 2 * (j & 1) : j), sfa + 4 * h, sfb + 8 * h,
+                                  k > 0 || j > 0);
+                    }
+                    commit_both(&ctl.empty[slot]);
+                }
+                if (ok && rank == 0) commit_both(&ctl.acc_full);
+            }
+            if (!ok) {
+                give_up(a, &ctl.abort);
+                if (rank == 0) {
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl.drain)) : "memory");
+                    mbar_wait_bounded(&ctl.drain, 0, kLinWaitNs);
+                }
+            }
+        }
+    } else if (warp >= kWarpLoad) {
+        bool ok = true;
+        for (int i = first; i < tiles && ok; i += stride) {
+            const int t0 = i / ftiles * kTokens + (int)rank * 128;
+            for (int k = 0; k < steps; k++, c++) {
+                if (c % kLoadWarps != (uint32_t)(warp - kWarpLoad)) continue;
+                const uint32_t slot = c % kRing;
+                Scales<E2M1, 128> sc;
+                sc.load(a, 128, t0, k, lane);
+                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, kLinWaitNs);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                sc.store(128, ring + slot * S::bytes + S::sfa, lane);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.full[slot]);
+            }
+        }
+        if (!ok && lane == 0) give_up(a, &ctl.abort);
+    } else {
+        const bool wide = (uintptr_t)a.y % 32 == 0 && (size_t)a.N * (F32 ? 4 : 2) % 32 == 0;
+        for (int i = first; i < tiles; i += stride, it++) {
+            const int n0 = i % ftiles * kFeatures;
+            const long long t = (long long)(i / ftiles) * kTokens + rank * 128 + 32 * warp + lane;
+            bool ok = mbar_wait_or_abort(&ctl.acc_full, it & 1, &ctl.abort, kLinWaitNs);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) {
+                if (lane == 0) give_up(a, &ctl.abort);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t from = tmem + (it & 1) * (kFeatures - kShared) + ((uint32_t)(32 * warp) << 16);
+            // The shared columns lie in the first two or the last two of eight groups of 32.
+            const int g0 = it & 1 ? 0 : 6;
+            uint32_t r[2][32];
+            tc_ld32_nowait(from + 32 * g0, r[0]);
+            tc_ld32_nowait(from + 32 * g0 + 32, r[1]);
+            tc_wait_ld();
+            tc_ld_fence_regs<32>(r[0]);
+            tc_ld_fence_regs<32>(r[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(&ctl.acc_empty, 0);
+            const bool in = t < a.T;
+            for (int g = 0; g < 8; g += 2) {
+                const int h = (g + g0) % 8;
+                if (g > 0) {
+                    tc_ld32_nowait(from + 32 * h, r[0]);
+                    tc_ld32_nowait(from + 32 * h + 32, r[1]);
+                    tc_wait_ld();
+                    tc_ld_fence_regs<32>(r[0]);
+                    tc_ld_fence_regs<32>(r[1]);
+                }
+                if (in && n0 + 32 * h < a.N) store32<F32>(a, t, n0 + 32 * h, r[0], wide);
+                if (in && n0 + 32 * h + 32 < a.N) store32<F32>(a, t, n0 + 32 * h + 32, r[1], wide);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();     // no product still reads the other's memory, and no arrival is on its way
+    tc_fence_after();
+    if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+const void* kernel(bool e2m1, bool f32)
+{
+    return e2m1 ? (f32 ? (const void*)k_linear_pair<1, 1> : (const void*)k_linear_pair<1, 0>)
+                : (f32 ? (const void*)k_linear_pair<0, 1> : (const void*)k_linear_pair<0, 0>);
+}
+
+size_t smem_bytes(bool e2m1) { return sizeof(Control) + kRing * (e2m1 ? Stage<1>::bytes : Stage<0>::bytes); }
+
+int g_pairs;        // that run at once
+
+}  // namespace
+
+int linear_pairs() { return g_pairs; }
+
+cudaError_t linear_pair_init_device()
+{
+    for (int i = 0; i < 4; i++) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(i & 1));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(true);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&g_pairs, kernel(true, false), &cfg);
+}
+
+cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
+{
+    LinearArgs a = a0;
+    int units = lin_units(a.K), ftiles = (a.N + kFeatures - 1) / kFeatures;
+    CUtensorMap wmap, xmap;
+    const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)lin_tiles(a.N) * units};
+    const cuuint64_t ws[2] = {128, kLinUnitBytes};
+    const cuuint32_t wb[3] = {128, kLinRows, 1};
+    cudaError_t e = linear_map(&wmap, a.e2m1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, a.packed, wd, ws, wb);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t width = a.e2m1 ? a.K / 2 : a.K;
+    const cuuint64_t xd[2] = {width, (cuuint64_t)a.T}, xs[1] = {width};
+    const cuuint32_t xb[2] = {128, 128};
+    e = linear_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (a.T + kTokens - 1LL) / kTokens * ftiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, (long long)g_pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(a.e2m1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&wmap, &xmap, &a, &ftiles, &units};
+    return cudaLaunchKernelExC(&cfg, kernel(a.e2m1, a.out_f32), args);
+}
+
+}  // namespace moe
