@@ -6,6 +6,8 @@
 // multiple of 16).  A stage of the ring is 128 bytes of K of both operands, which TMA
 // brings in the 128-byte swizzle that the MMA reads: 256 elements of E2M1, or 128 of
 // E4M3, for which TMA expands the weights to a byte an element on their way.
+#include <math.h>
+
 #include <algorithm>
 
 #include "linear.cuh"
@@ -17,7 +19,7 @@ namespace {
 constexpr int kRing = 16;                  // stages, at most
 constexpr int kMaxNt = 192;                // tokens of a tile, at most
 constexpr int kSplitMax = 8;               // CTAs of a cluster along K, at most (the portable size)
-constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 4;
+constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 8;
 constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
 
 struct __align__(1024) Control {
@@ -41,6 +43,9 @@ struct Plan {
     uint32_t part;                      // byte offset of the partial sums
     uint32_t smem;
     int sfcols;                 // tensor memory columns of a stage's scales
+    int tmem;                   // columns in all
+    int acc;                    // column of the second accumulator (0: there is one)
+    int ahead;                  // fetch weights into L2 before the kernel ahead is done
 };
 
 template <int E2M1>
@@ -102,9 +107,48 @@ __device__ __forceinline__ void quantise_stage(const LinearArgs& a, const Plan& 
     }
 }
 
+// The MMA's thread: per stage the scales to tensor memory and four products.  Its
+// instructions follow one another by few cycles only if little is computed between them:
+// descriptors differ in their low words, by constants.  ATOMS: of 128 tokens' scales.
+template <int E2M1, int ATOMS>
+__device__ __forceinline__ bool multiply(const Plan& p, Control& ctl, uint8_t* ring, uint32_t tmem, int k0, int k1, int first, int tiles, int stride)
+{
+    constexpr int kHalves = E2M1 ? 2 : 1, kUnit = kLinAtom / 16;
+    const uint64_t ad0 = desc_sw128(smem_u32(ring)), bd0 = ad0 + p.b / 16, sd0 = umma_desc(smem_u32(ring) + p.sfa, 16, 128);
+    const uint32_t id = idesc<E2M1>(p.nt, 0), sf0 = tmem + p.nt + p.acc, stage = p.stage / 16, cols = p.sfcols;
+    const int n = k1 - k0, depth = p.ring;
+    uint32_t slot = 0, parity = 0, it = 0;
+    for (int i = first; i < tiles; i += stride, it++) {
+        const uint32_t buf = it & 1, acc = tmem + buf * p.acc;
+        if (!mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, kLinWaitNs)) return false;
+        for (int k = 0; k < n; k++) {
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
+            tc_fence_after();
+            const uint64_t ad = ad0 + slot * stage, bd = bd0 + slot * stage, sd = sd0 + slot * stage;
+            const uint32_t sfa = sf0 + slot * cols, sfb = sfa + 4 * kHalves;
+#pragma unroll
+            for (int h = 0; h < kHalves; h++) tc_cp_sf(sfa + 4 * h, sd + h * kUnit);
+#pragma unroll
+            for (int h = 0; h < kHalves * ATOMS; h++) tc_cp_sf(sfb + 4 * h, sd + (kHalves + h) * kUnit);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t sf = E2M1 ? 2 * (j & 1) : j, h = E2M1 ? j / 2 : 0;
+                mma<E2M1>(acc, ad + 2 * j, bd + 2 * j, id | (sf << 29) | (sf << 4), sfa + 4 * h, sfb + 4 * ATOMS * h, k > 0 || j > 0);
+            }
+            tc_commit(&ctl.empty[slot]);
+            if (++slot == (uint32_t)depth) {
+                slot = 0;
+                parity ^= 1;
+            }
+        }
+        tc_commit(&ctl.acc_full[buf]);
+    }
+    return true;
+}
+
 // QUANT: x is bf16, a few tokens, quantised here.
 template <int E2M1, int QUANT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     k_linear(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, Plan p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -129,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(&wmap);
         if (!QUANT) prefetch_map(&xmap);
     }
-    if (warp == kWarpMma) tmem_alloc(&ctl.tmem, 512);
+    if (warp == kWarpMma) tmem_alloc(&ctl.tmem, p.tmem);
     tc_fence_before();
     if (p.split > 1)
         cluster_sync();
@@ -137,21 +181,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    pdl_trigger();
-    pdl_wait();
-
     const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
     const int k0 = (int)((long long)p.steps * rank / p.split), k1 = (int)((long long)p.steps * (rank + 1) / p.split);
     const int tiles = p.ttiles * p.rtiles, first = (int)blockIdx.x / p.split, stride = (int)gridDim.x / p.split;
     uint32_t c = 0, it = 0;
-
+    pdl_trigger();
     if (warp == kWarpProd) {
         if (elect_one()) {
-            bool ok = true;
+            bool ok = true, waited = false;
             for (int i = first; i < tiles && ok; i += stride) {
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
+                // The weights of as many stages as there are come while the kernel before this
+                // one still runs, its tokens after it.
+                const int early = waited ? 0 : min(k1 - k0, p.ring);
+                if (!waited)
+                    for (int k = k0 + early; k < k1; k += E2M1 ? 1 : 2)
+                        prefetch_l2(a.packed + ((size_t)rt * p.units + (E2M1 ? k : k / 2)) * kLinUnitBytes, kLinUnitBytes);
                 for (int k = k0; k < k1; k++, c++) {
                     const uint32_t slot = c % p.ring;
+                    if (k == k0 + early && !waited) {
+                        pdl_wait();
+                        waited = true;
+                        if (!QUANT)
+                            for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
+                    }
                     if (!mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
                         give_up(a, &ctl.abort);
                         ok = false;
@@ -165,7 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(bar, (E2M1 ? kLinCodeBytes : kLinCodeBytes / 2) + sf + (QUANT ? 0 : p.nt * 128));
                     tma_3d(st, &wmap, half * 128, 0, z, bar);
                     bulk_g2s(st + p.sfa, a.packed + (size_t)z * kLinUnitBytes + kLinCodeBytes + half * kLinAtom, sf, bar);
-                    if (!QUANT) tma_2d(st + p.b, &xmap, k * 128, t0, bar);
+                    if (!QUANT && waited) tma_2d(st + p.b, &xmap, k * 128, t0, bar);
+                }
+                if (!waited) {
+                    pdl_wait();
+                    waited = true;
+                    if (!QUANT)
+                        for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
                 }
             }
             // no copy may be in flight into this CTA's memory at its end
@@ -175,35 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
-            bool ok = true;
-            for (int i = first; i < tiles && ok; i += stride, it++) {
-                const uint32_t buf = it & 1;
-                ok = mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, kLinWaitNs);
-                const uint32_t acc = tmem + buf * p.nt;
-                for (int k = k0; k < k1 && ok; k++, c++) {
-                    const uint32_t slot = c % p.ring;
-                    ok = mbar_wait_or_abort(&ctl.full[slot], c / p.ring & 1, &ctl.abort, kLinWaitNs);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(ring + slot * p.stage);
-                    const uint32_t sfa = tmem + 2 * p.nt + slot * p.sfcols, sfb = sfa + (E2M1 ? 8 : 4);
-                    const int atoms = p.nt > 128 ? 2 : 1;
-                    for (int h = 0; h < (E2M1 ? 2 : 1); h++) {
-                        tc_cp_sf(sfa + 4 * h, umma_desc(st + p.sfa + h * kLinAtom, 16, 128));
-                        for (int m = 0; m < atoms; m++)
-                            tc_cp_sf(sfb + 4 * (atoms * h + m), umma_desc(st + p.sfb + (atoms * h + m) * kLinAtom, 16, 128));
-                    }
-                    const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + p.b);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int h = E2M1 ? j / 2 : 0;
-                        mma<E2M1>(acc, ad + 2 * j, bd + 2 * j, idesc<E2M1>(p.nt, E2M1 ? 2 * (j & 1) : j), sfa + 4 * h,
-                                  sfb + 4 * atoms * h, k > k0 || j > 0);
-                    }
-                    tc_commit(&ctl.empty[slot]);
-                }
-                if (ok) tc_commit(&ctl.acc_full[buf]);
-            }
+            const bool ok = p.nt > 128 ? multiply<E2M1, 2>(p, ctl, ring, tmem, k0, k1, first, tiles, stride)
+                                       : multiply<E2M1, 1>(p, ctl, ring, tmem, k0, k1, first, tiles, stride);
             if (!ok) {
                 // (else the epilogue has waited for the last product)
                 give_up(a, &ctl.abort);
@@ -212,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp >= kWarpLoad) {
+        pdl_wait();
         bool ok = true;
         for (int i = first; i < tiles && ok; i += stride) {
             const int t0 = i / p.rtiles * p.nt;
@@ -234,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
+        pdl_wait();
         for (int i = first; i < tiles; i += stride, it++) {
             const long long t0 = (long long)(i / p.rtiles) * p.nt, n = (long long)(i % p.rtiles) * kLinRows + 32 * warp + lane;
             const uint32_t buf = it & 1;
@@ -245,19 +279,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const int cols = (int)min((long long)p.nt, a.T - t0);
-            const uint32_t from = tmem + buf * p.nt + ((uint32_t)(32 * warp) << 16);
+            const uint32_t from = tmem + buf * p.acc + ((uint32_t)(32 * warp) << 16);
             float* mine = reinterpret_cast<float*>(ring) + 32 * warp + lane;
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-                float v[16];
-                tc_ld16(from + c0, v);
-                if (p.split == 1) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        if (c0 + j < cols && n < a.N) store(a, t0 + c0 + j, n, v[j]);
-                } else {
+            size_t at = (size_t)t0 * a.N + n;
+            for (int c0 = 0; c0 < cols; c0 += 32) {
+                uint32_t r[2][16];
+                const int have = cols - c0;
+                tc_ld16_nowait(from + c0, r[0]);
+                if (have > 16) tc_ld16_nowait(from + c0 + 16, r[1]);
+                tc_wait_ld();
+                tc_ld_fence_regs<16>(r[0]);
+                tc_ld_fence_regs<16>(r[1]);
+                if (p.split > 1) {
                     // (the ring is free: every product is done)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) mine[(c0 + j) * kLinRows] = v[j];
+                    for (int j = 0; j < 32; j++)
+                        if (j < have) mine[(c0 + j) * kLinRows] = __uint_as_float(r[j / 16][j % 16]);
+                } else if (n < a.N) {
+                    if (a.out_f32) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++, at += a.N)
+                            if (j < have) ((float*)a.y)[at] = __uint_as_float(r[j / 16][j % 16]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j++, at += a.N)
+                            if (j < have) ((__nv_bfloat16*)a.y)[at] = __float2bfloat16_rn(__uint_as_float(r[j / 16][j % 16]));
+                    }
                 }
             }
             tc_fence_before();
@@ -269,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.split > 1) {
         // One tile a cluster.  CTA r adds up the columns r * width ..: every CTA sends it its
         // own sums of them, and they are added in the CTAs' order.
+        const long long t0 = (long long)(first / p.rtiles) * p.nt, n0 = (long long)(first % p.rtiles) * kLinRows + 4 * lane;
+        const int cols = (int)min((long long)p.nt, a.T - t0), here = min(p.width, cols - (int)rank * p.width);
         if (warp < 4) {
-            const long long t0 = (long long)(first / p.rtiles) * p.nt, n0 = (long long)(first % p.rtiles) * kLinRows + 4 * lane;
-            const int cols = (int)min((long long)p.nt, a.T - t0), here = min(p.width, cols - (int)rank * p.width);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             named_sync(1, 128);
             if (warp == 0 && elect_one()) {
@@ -283,32 +330,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      m * kLinRows * 4, smem_u32(&ctl.red), o);
                 }
             }
-            if (here > 0) {
-                bool ok = mbar_wait_bounded(&ctl.red, 0, kLinWaitNs);
-                if (!ok) give_up(a, &ctl.abort);
-                const float4* part = reinterpret_cast<const float4*>(smem + p.part) + lane;
-                for (int j = warp; j < here && ok; j += 4) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        // (the producer's and the MMA's warps have no part in it)
+        const int adder = warp < 4 ? warp : warp - 2, adders = 4 + kLoadWarps;
+        if (here > adder && (warp < 4 || warp >= kWarpLoad)) {
+            const bool ok = mbar_wait_bounded(&ctl.red, 0, kLinWaitNs);
+            if (!ok) give_up(a, &ctl.abort);
+            const float4* part = reinterpret_cast<const float4*>(smem + p.part) + lane;
+            for (int j = adder; j < here && ok; j += adders) {
+                float4 w[kSplitMax], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                    for (int r = 0; r < kSplitMax; r++)
-                        if (r < p.split) {
-                            const float4 w = part[(r * p.width + j) * (kLinRows / 4)];
-                            v.x += w.x;
-                            v.y += w.y;
-                            v.z += w.z;
-                            v.w += w.w;
-                        }
-                    store4(a, t0 + rank * p.width + j, n0, v);
-                }
+                for (int r = 0; r < kSplitMax; r++)
+                    if (r < p.split) w[r] = part[(r * p.width + j) * (kLinRows / 4)];
+#pragma unroll
+                for (int r = 0; r < kSplitMax; r++)
+                    if (r < p.split) {
+                        v.x += w[r].x;
+                        v.y += w[r].y;
+                        v.z += w[r].z;
+                        v.w += w[r].w;
+                    }
+                store4(a, t0 + rank * p.width + j, n0, v);
             }
         }
         __syncwarp();
-        cluster_sync();     // nobody's memory is still read
+        cluster_meet();     // nobody's memory is still read
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    if (warp == kWarpMma) tmem_dealloc(tmem, p.tmem);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -317,31 +368,61 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
 EncodeTiled g_encode = nullptr;
 int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
 
+long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
+
+// Time of a product in microseconds, as measured in CUDA graphs of products one after the
+// other (K = 512 .. 8192, N = 512 .. 8192, T = 1 .. 1024, within 15 %): a start and end of
+// 4.2, the longer of a CTA's stages (a row of a TMA box takes about 2.6 cycles) and of what
+// all of them fetch through L2, and the epilogue; a split product's sums meet in 0.9 and 0.024
+// a token.
+double tile_cost(const LinearArgs& a, const Plan& p)
+{
+    const long long tiles = tiles_of(p);
+    const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
+    const double serial = waves * ((p.steps + p.split - 1) / p.split) * std::max(0.24, (kLinRows + p.nt) * 0.00137);
+    const double feed = (double)tiles * p.steps * ((a.e2m1 ? 17408 : 8704) + p.nt * 132) * 1e-7;
+    return 4.2 + std::max(serial, feed) + (p.split > 1 ? 0.9 + 0.024 * p.nt : 0.2 + 0.004 * p.nt * waves);
+}
+
+// And of one on pairs of CTAs: 0.37 (E4M3 0.31) a stage, 3 more a tile where y is not
+// stored by TMA.
+double pair_cost(const LinearArgs& a, int steps)
+{
+    const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, linear_pairs()));
+    return 4.5 + waves * (steps * (a.e2m1 ? 0.37 : 0.31) + (a.N % (a.out_f32 ? 4 : 8) ? 3.0 : 0.0));
+}
+
+// The cheapest tile and split; no tile (nt = 0) where pairs of CTAs are cheaper.
 Plan make_plan(const LinearArgs& a)
 {
-    Plan best{};
-    double least = 0;
-    const int rtiles = lin_tiles(a.N), steps = a.e2m1 ? lin_units(a.K) : (a.K + 127) / 128;
-    const int j0 = (a.T + kMaxNt - 1) / kMaxNt;
-    for (int j = j0; j < j0 + 4; j++) {
-        Plan p{};
-        p.nt = ((a.T + j - 1) / j + 15) / 16 * 16;
-        p.ttiles = (a.T + p.nt - 1) / p.nt;
-        p.rtiles = rtiles;
-        p.steps = steps;
-        p.units = lin_units(a.K);
-        const long long tiles = (long long)p.ttiles * rtiles;
-        for (p.split = 1; p.split <= std::min(kSplitMax, steps); p.split++) {
-            if (p.split > 1 && tiles > g_clusters[p.split]) continue;
-            const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
-            const double cost = waves * (((steps + p.split - 1) / p.split) * std::max(p.nt, 64) + 512.0) + p.split * 64.0;
-            if (least == 0 || cost < least) {
+    Plan p{};
+    p.rtiles = lin_tiles(a.N);
+    p.steps = a.e2m1 ? lin_units(a.K) : (a.K + 127) / 128;
+    p.units = lin_units(a.K);
+    Plan best = p;
+    double least = a.codes && a.T > 64 ? pair_cost(a, p.steps) : HUGE_VAL;
+    // (beyond that no tile of one CTA was cheaper)
+    const int widest = a.codes && a.T > 4096 ? 0 : std::min(kMaxNt, (a.T + 15) / 16 * 16);
+    for (p.nt = widest; p.nt > 0; p.nt -= 16) {
+        const int ttiles = (a.T + p.nt - 1) / p.nt;
+        if (ttiles == p.ttiles) continue;       // no fewer tokens a tile than that needs: below
+        p.ttiles = ttiles;
+        Plan q = p;
+        q.nt = ((a.T + ttiles - 1) / ttiles + 15) / 16 * 16;
+        const long long tiles = tiles_of(q);
+        for (q.split = 1; q.split <= std::min(kSplitMax, q.steps); q.split++) {
+            // clusters that run at once: two CTAs an SM where they are small
+            if (q.split > 1 && (tiles * q.split > a.sms || tiles > g_clusters[q.split] * (q.nt <= 32 ? 2 : 1))) break;
+            const double cost = tile_cost(a, q);
+            if (cost < least) {
                 least = cost;
-                best = p;
+                best = q;
             }
         }
+        if (tiles > 8 * a.sms) break;
     }
-    Plan p = best;
+    p = best;
+    if (p.nt == 0) return p;
     const uint32_t sf = p.nt > 128 ? 2 : 1, h = a.e2m1 ? 2 : 1;
     p.b = kLinCodeBytes;
     p.sfa = p.b + p.nt * 128;
@@ -351,11 +432,22 @@ Plan make_plan(const LinearArgs& a)
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0;
     p.sfcols = 4 * h * (1 + sf);
     p.ring = std::min({kRing, (int)((kLinSmemMax - sizeof(Control) - part) / p.stage), (512 - 2 * p.nt) / p.sfcols,
-                       std::max(3, (int)(p.split > 1 ? (steps + p.split - 1) / p.split : kRing))});
+                       std::max(3, (int)(p.split > 1 ? (p.steps + p.split - 1) / p.split : kRing))});
+    // Where four stages of weights fit half an SM, two CTAs share one, so that a kernel can begin
+    // beside the one before it, each with at most half of the tensor memory.  Else a CTA takes
+    // more than half of the shared memory, so that no two CTAs of clusters share an SM and wait
+    // for each other's tensor memory.
+    const bool one = p.split > 1 || tiles_of(p) <= a.sms;
+    const int two = (int)((kLinSmemTwo - sizeof(Control) - part) / p.stage);
+    p.ahead = one && part < kLinSmemTwo / 2 && two >= 4;
+    if (p.ahead) p.ring = std::min(p.ring, two);
     p.loaders = std::min(kLoadWarps, p.ring);
     p.part = sizeof(Control) + p.ring * p.stage;
-    // (more than half an SM's, so that no two CTAs of clusters share one and wait for each other's tensor memory)
-    p.smem = std::max(p.part + part, kLinSmemMax / 2 + 2048);
+    p.smem = p.part + part;
+    if (!p.ahead) p.smem = std::max(p.smem, kLinSmemMax / 2 + 4096);
+    p.acc = one ? 0 : p.nt;
+    p.tmem = 32;
+    while (p.tmem < p.nt + p.acc + p.ring * p.sfcols) p.tmem *= 2;
     return p;
 }
 
@@ -374,7 +466,7 @@ cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, con
 const void* const kKernels[4] = {(const void*)k_linear<0, 0>, (const void*)k_linear<1, 0>, (const void*)k_linear<0, 1>,
                                  (const void*)k_linear<1, 1>};
 
-bool linear_takes_bf16(int T) { return T <= 16; }
+bool linear_takes_bf16(int T) { return T <= 4; }
 
 cudaError_t linear_init_device()
 {
@@ -401,10 +493,8 @@ cudaError_t linear_init_device()
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&g_clusters[split], kKernels[0], &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            g_clusters[split] = 0;
-        }
+        if (cudaOccupancyMaxActiveClusters(&g_clusters[split], kKernels[0], &cfg) != cudaSuccess) g_clusters[split] = 0;
+        cudaGetLastError();
     }
     return linear_pair_init_device();
 }
@@ -412,8 +502,8 @@ cudaError_t linear_init_device()
 cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
 {
     LinearArgs a = a0;
-    if (a.codes && a.T > 512) return launch_linear_pair(a, s);
     Plan p = make_plan(a);
+    if (p.nt == 0) return launch_linear_pair(a, s);
     CUtensorMap wmap, xmap{};
     const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)p.rtiles * p.units};
     const cuuint64_t ws[2] = {128, kLinUnitBytes};

@@ -10,7 +10,7 @@
 namespace moe {
 
 constexpr uint64_t kLinWaitNs = 2000000000ull;
-constexpr uint32_t kLinSmemMax = 227 * 1024;
+constexpr uint32_t kLinSmemMax = 227 * 1024, kLinSmemTwo = 113 * 1024;     // of a CTA, and of each of two on an SM
 
 // K-major operand of 128-byte rows in TMA's 128-byte swizzle, groups of 8 rows of 1 KB.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
@@ -40,6 +40,12 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// size: a multiple of 16
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t size)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(size) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -51,6 +57,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The same without making memory visible: it does not wait for the stores before it.
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // Bulk copy from this CTA's shared memory to the same place's of another CTA of the

@@ -17,6 +17,7 @@ constexpr int kRing = 6;
 constexpr int kTokens = 256, kFeatures = 256;
 constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 4;
 constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
+constexpr uint32_t kOutBytes = 32 * 128;        // of an epilogue warp's box
 // Tensor memory: the accumulators of two tiles in turn, which share kShared columns, and
 // behind them the scales of two stages (E4M3: four).  The epilogue empties the shared columns
 // first, and then the next tile's products may begin.
@@ -34,7 +35,7 @@ struct Stage {
     static constexpr uint32_t b = 128 * 128, sfa = 2 * b, sfb = sfa + kAtoms * kLinAtom;
     static constexpr uint32_t bytes = (sfb + 2 * kAtoms * kLinAtom + 1023) / 1024 * 1024;
     static constexpr int cols = 12 * kAtoms, slots = kShared / cols;
-    static_assert(sizeof(Control) + kRing * bytes <= kLinSmemMax && kLoadWarps <= kRing && slots >= 2, "sizes");
+    static_assert(sizeof(Control) + kRing * bytes + 4 * kOutBytes <= kLinSmemMax && kLoadWarps <= kRing && slots >= 2, "sizes");
 };
 
 __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank)
@@ -83,37 +84,51 @@ __device__ __forceinline__ constexpr uint32_t idesc(uint32_t sf)
            ((uint32_t)(kTokens >> 4) << 24) | (sf << 29) | (sf << 4);
 }
 
-// 32 features of one token from n.
-template <int F32>
-__device__ __forceinline__ void store32(const LinearArgs& a, long long t, int n, const uint32_t (&r)[32], bool wide)
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src)
 {
-    const size_t i = (size_t)t * a.N + n;
-    if (wide && n + 32 <= a.N) {
-        if (F32) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\tcp.async.bulk.commit_group;" ::"l"(map),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+
+// 32 tokens (a lane each) by 128 bytes of features from n, by one warp: through its 4 KB of
+// shared memory, in TMA's swizzle, to whole lines of y.  Where y's rows do not begin on 16
+// bytes, which TMA needs, a row after the other by plain stores.
+template <int F32>
+__device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap* ymap, bool tma, uint8_t* out, int t, int n, int lane,
+                                          const uint32_t (&w)[32])
+{
+    // (the box before has left)
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) st_v8((float*)a.y + i + j, r[j], r[j + 1], r[j + 2], r[j + 3], r[j + 4], r[j + 5], r[j + 6], r[j + 7]);
-        } else {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; j++) w[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-#pragma unroll
-            for (int j = 0; j < 16; j += 8) st_v8((uint16_t*)a.y + i + 2 * j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
-        }
+    for (int j = 0; j < 8; j++)
+        *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    if (tma) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tma_store(ymap, n, t, out);
         return;
     }
-#pragma unroll
-    for (int j = 0; j < 32; j++)
-        if (n + j < a.N) {
-            if (F32)
-                ((float*)a.y)[i + j] = __uint_as_float(r[j]);
-            else
-                ((__nv_bfloat16*)a.y)[i + j] = __float2bfloat16_rn(__uint_as_float(r[j]));
+    __syncwarp();
+    constexpr int kEach = F32 ? 1 : 2;
+    const int c = n + kEach * lane;
+    for (int r = 0; r < 32 && t + r < a.T; r++) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(out + r * 128 + ((lane / 4 ^ (r & 7)) << 4) + lane % 4 * 4);
+        const size_t i = (size_t)(t + r) * a.N + c;
+        if (F32) {
+            if (c < a.N) ((uint32_t*)a.y)[i] = v;
+        } else {
+            if (c < a.N) ((uint16_t*)a.y)[i] = (uint16_t)v;
+            if (c + 1 < a.N) ((uint16_t*)a.y)[i + 1] = (uint16_t)(v >> 16);
         }
+    }
 }
 
 template <int E2M1, int F32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    k_linear_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LinearArgs a, int ftiles, int units)
+    k_linear_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                  const __grid_constant__ CUtensorMap ymap, LinearArgs a, int ftiles, int units, int tma)
 {
     using S = Stage<E2M1>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -256,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
-        const bool wide = (uintptr_t)a.y % 32 == 0 && (size_t)a.N * (F32 ? 4 : 2) % 32 == 0;
+        uint8_t* out = ring + kRing * S::bytes + warp * kOutBytes;
         for (int i = first; i < tiles; i += stride, it++) {
             const int n0 = i % ftiles * kFeatures;
-            const long long t = (long long)(i / ftiles) * kTokens + rank * 128 + 32 * warp + lane;
+            const int t = i / ftiles * kTokens + (int)rank * 128 + 32 * warp;
             bool ok = mbar_wait_or_abort(&ctl.acc_full, it & 1, &ctl.abort, kLinWaitNs);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
@@ -268,36 +283,40 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             tc_fence_after();
             const uint32_t from = tmem + (it & 1) * (kFeatures - kShared) + ((uint32_t)(32 * warp) << 16);
-            // The shared columns lie in the first two or the last two of eight groups of 32.
-            const int g0 = it & 1 ? 0 : 6;
-            uint32_t r[2][32];
-            tc_ld32_nowait(from + 32 * g0, r[0]);
-            tc_ld32_nowait(from + 32 * g0 + 32, r[1]);
-            tc_wait_ld();
-            tc_ld_fence_regs<32>(r[0]);
-            tc_ld_fence_regs<32>(r[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(&ctl.acc_empty, 0);
-            const bool in = t < a.T;
-            for (int g = 0; g < 8; g += 2) {
-                const int h = (g + g0) % 8;
-                if (g > 0) {
-                    tc_ld32_nowait(from + 32 * h, r[0]);
-                    tc_ld32_nowait(from + 32 * h + 32, r[1]);
-                    tc_wait_ld();
-                    tc_ld_fence_regs<32>(r[0]);
-                    tc_ld_fence_regs<32>(r[1]);
+            // The shared columns lie in the first or the last of four groups of 64.
+            const int g0 = it & 1 ? 0 : 3;
+            for (int g = 0; g < 4; g++) {
+                const int n = 64 * ((g + g0) & 3);
+                uint32_t r[2][32];
+                tc_ld32_nowait(from + n, r[0]);
+                tc_ld32_nowait(from + n + 32, r[1]);
+                tc_wait_ld();
+                tc_ld_fence_regs<32>(r[0]);
+                tc_ld_fence_regs<32>(r[1]);
+                if (g == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(&ctl.acc_empty, 0);
                 }
-                if (in && n0 + 32 * h < a.N) store32<F32>(a, t, n0 + 32 * h, r[0], wide);
-                if (in && n0 + 32 * h + 32 < a.N) store32<F32>(a, t, n0 + 32 * h + 32, r[1], wide);
+                if (t >= a.T || n0 + n >= a.N) continue;
+                if (F32) {
+                    store_box<1>(a, &ymap, tma, out, t, n0 + n, lane, r[0]);
+                    if (n0 + n + 32 < a.N) store_box<1>(a, &ymap, tma, out, t, n0 + n + 32, lane, r[1]);
+                } else {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        w[j] = pack_bf16(__uint_as_float(r[j / 16][2 * j % 32]), __uint_as_float(r[j / 16][2 * j % 32 + 1]));
+                    store_box<0>(a, &ymap, tma, out, t, n0 + n, lane, w);
+                }
             }
             tc_fence_before();
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();     // no product still reads the other's memory, and no arrival is on its way
+    cluster_meet();     // no product still reads the other's memory, and no arrival is on its way
     tc_fence_after();
     if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
@@ -308,7 +327,7 @@ const void* kernel(bool e2m1, bool f32)
                 : (f32 ? (const void*)k_linear_pair<0, 1> : (const void*)k_linear_pair<0, 0>);
 }
 
-size_t smem_bytes(bool e2m1) { return sizeof(Control) + kRing * (e2m1 ? Stage<1>::bytes : Stage<0>::bytes); }
+size_t smem_bytes(bool e2m1) { return sizeof(Control) + kRing * (e2m1 ? Stage<1>::bytes : Stage<0>::bytes) + 4 * kOutBytes; }
 
 int g_pairs;        // that run at once
 
@@ -339,7 +358,7 @@ cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
 {
     LinearArgs a = a0;
     int units = lin_units(a.K), ftiles = (a.N + kFeatures - 1) / kFeatures;
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap, ymap{};
     const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)lin_tiles(a.N) * units};
     const cuuint64_t ws[2] = {128, kLinUnitBytes};
     const cuuint32_t wb[3] = {128, kLinRows, 1};
@@ -350,6 +369,14 @@ cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
     const cuuint32_t xb[2] = {128, 128};
     e = linear_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, xd, xs, xb);
     if (e != cudaSuccess) return e;
+    const cuuint64_t size = a.out_f32 ? 4 : 2;
+    int tma = a.N * size % 16 == 0;
+    if (tma) {
+        const cuuint64_t yd[2] = {(cuuint64_t)a.N, (cuuint64_t)a.T}, ys[1] = {a.N * size};
+        const cuuint32_t yb[2] = {(cuuint32_t)(128 / size), 32};
+        e = linear_map(&ymap, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y, yd, ys, yb);
+        if (e != cudaSuccess) return e;
+    }
     const long long tiles = (a.T + kTokens - 1LL) / kTokens * ftiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, (long long)g_pairs)));
@@ -361,7 +388,7 @@ cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[] = {&wmap, &xmap, &a, &ftiles, &units};
+    void* args[] = {&wmap, &xmap, &ymap, &a, &ftiles, &units, &tma};
     return cudaLaunchKernelExC(&cfg, kernel(a.e2m1, a.out_f32), args);
 }
 

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256) k_mx_values(MxValuesArgs a)
 // One block a unit: thread r copies row r's 128 bytes of codes and its 8 scale bytes.
 __global__ void __launch_bounds__(kLinRows) k_mx_pack(MxPackArgs a, int units)
 {
-    pdl_trigger();
+    // (dependents start after the end: the product reads weights before it waits)
     pdl_wait();
     const int u = (int)(blockIdx.x % (unsigned)units), r = threadIdx.x;
     const long long row = (long long)(blockIdx.x / (unsigned)units) * kLinRows + r;

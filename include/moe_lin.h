@@ -100,7 +100,11 @@ int moe_linear_pack(moe_lin_t h, const uint8_t* codes, const uint8_t* scales, in
  *             moe_mx_quant does (T and in_features within the handle's config)
  *   y         device [T][out_features] of out_dtype, apart from the inputs
  * Deterministic.  Scales whose product with a code leaves fp32's range make
- * infinities and NaN as they would there. */
+ * infinities and NaN as they would there.  The kernel reads `packed` before it
+ * waits for the stream's previous kernel (programmatic dependent launch), as
+ * moe_ffn_forward does its routing: packed must be written by an ordinary kernel
+ * or copy, or by moe_linear_pack, not by a kernel that lets its dependents
+ * launch early. */
 typedef struct {
     const void* packed;     /* DEVICE, made by moe_linear_pack */
     int out_features;
