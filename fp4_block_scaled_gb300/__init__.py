@@ -706,13 +706,19 @@ def moe_rms_norm(h, norm: moe_norm_desc, x, T: int, residual=None, residual_out=
 
 
 def moe_mx_quant(h, x, rows: int, n: int, act_mode: int, codes, scales, stream=None):
-    _lin_call(1, _QUANT.pack(h or 0, _p(x) or 0, rows, n, act_mode, _p(codes) or 0, _p(scales) or 0, _s(stream) or 0),
-              "moe_mx_quant")
+    try:
+        w = _QUANT.pack(h, x.data_ptr(), rows, n, act_mode, codes.data_ptr(), scales.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _QUANT.pack(h or 0, _p(x) or 0, rows, n, act_mode, _p(codes) or 0, _p(scales) or 0, _s(stream) or 0)
+    _lin_call(1, w, "moe_mx_quant")
 
 
 def moe_mx_values(h, act_mode: int, codes, scales, rows: int, n: int, out_dtype: int, out, stream=None):
-    _lin_call(2, _VALUES.pack(h or 0, act_mode, _p(codes) or 0, _p(scales) or 0, rows, n, out_dtype, _p(out) or 0, _s(stream) or 0),
-              "moe_mx_values")
+    try:
+        w = _VALUES.pack(h, act_mode, codes.data_ptr(), scales.data_ptr(), rows, n, out_dtype, out.data_ptr(), stream.cuda_stream)
+    except (AttributeError, struct.error):
+        w = _VALUES.pack(h or 0, act_mode, _p(codes) or 0, _p(scales) or 0, rows, n, out_dtype, _p(out) or 0, _s(stream) or 0)
+    _lin_call(2, w, "moe_mx_values")
 
 
 def moe_linear_packed_bytes(out_features: int, in_features: int) -> int:

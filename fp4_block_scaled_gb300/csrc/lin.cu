@@ -188,6 +188,7 @@ int moe_rms_norm(moe_lin_t h, const moe_norm_desc* d, const void* x, const void*
     a.res_f32 = d->residual_dtype == MOE_OUT_F32;
     a.e2m1 = act_mode == MOE_ACT_E2M1_UE8M0_32;
     a.eps = d->eps;
+    a.sms = h->sms;
     LinGuard guard(h->device);
     return cuda_rc(launch_norm(a, (cudaStream_t)stream));
 }

@@ -64,6 +64,7 @@ struct NormArgs {
     int x_f32, res_f32;
     int e2m1;                   // the codes' format
     float eps;
+    int sms;
 };
 constexpr int kNormMaxN = 32768;
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
