@@ -87,17 +87,15 @@ __device__ __forceinline__ void quantise_stage(const LinearArgs& a, const Plan& 
         for (int i = 0; i < kBatch; i++) {
             if (r0 + i * kRows >= rows) break;
             const int r = r0 + i * kRows + (E2M1 ? 0 : lane / 16);
-            float v[8];
-            unpack8(u[i], v);
             uint8_t* row = st + p.b + r * 128;
             uint8_t* atom = st + p.sfb + r % 32 * 16 + r / 32 * 4;
             int s;
             if (E2M1) {
-                const uint32_t c = e2m1_codes8(v, s);
+                const uint32_t c = e2m1_quantise(u[i], s);
                 *reinterpret_cast<uint32_t*>(row + ((l / 4 ^ (r & 7)) << 4) + l % 4 * 4) = c;
                 if (l % 4 == 0) atom[l / 16 * kLinAtom + l / 4 % 4] = (uint8_t)s;
             } else {
-                const uint2 c = e4m3_codes8(v, s);
+                const uint2 c = e4m3_quantise(u[i], s);
                 if (r < rows) {
                     *reinterpret_cast<uint2*>(row + ((l / 2 ^ (r & 7)) << 4) + l % 2 * 8) = c;
                     if (l == 0) *reinterpret_cast<uint32_t*>(atom) = (uint32_t)s * 0x01010101u;

@@ -52,17 +52,15 @@ __global__ void __launch_bounds__(256) k_mx_quant(MxQuantArgs a)
     }
 #pragma unroll
     for (int j = 0; j < LOADS; j++) {
-        float v[8];
-        unpack8(u[j], v);
         const size_t i = i0 + 256 * j;
         int s;
         if (E2M1) {
-            const uint32_t c = e2m1_codes8(v, s);
+            const uint32_t c = e2m1_quantise(u[j], s);
             if (!in[j]) continue;
             reinterpret_cast<uint32_t*>(a.codes)[i] = c;
             if (i % 4 == 0) a.scales[i / 4] = (uint8_t)s;
         } else {
-            const uint2 c = e4m3_codes8(v, s);
+            const uint2 c = e4m3_quantise(u[j], s);
             if (!in[j]) continue;
             reinterpret_cast<uint2*>(a.codes)[at[j]] = c;
             if (i % 16 == 0) a.scales[i / 16] = (uint8_t)s;
@@ -70,42 +68,57 @@ __global__ void __launch_bounds__(256) k_mx_quant(MxQuantArgs a)
     }
 }
 
-// Sixteen elements a thread; the scale is the row's block's.
+// Eight elements a thread and turn, in rows of `groups` of them.
+constexpr int kValuesTurns = 4;
 template <int E2M1, int F32>
 __global__ void __launch_bounds__(256) k_mx_values(MxValuesArgs a)
 {
     pdl_trigger();
     pdl_wait();
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    const int per = a.n / 16;
-    if (i >= (size_t)a.rows * per) return;
-    const size_t row = i / per;
-    const int c = (int)(i - row * per) * 16;
-    const int s = E2M1 ? a.scales[row * (a.n / 32) + c / 32] : a.scales[row * ((a.n + 127) / 128) + c / 128];
-    const float up = ue8m0_value(s);
-    float v[16];
-    if (E2M1) {
-        const uint2 q = *reinterpret_cast<const uint2*>(a.codes + i * 8);
+    const int groups = a.n / 8, per = E2M1 ? 4 : 16;     // of a row, and of a scale
+    const size_t all = (size_t)a.rows * groups, i0 = (size_t)blockIdx.x * (256 * kValuesTurns) + threadIdx.x;
+    uint2 q[kValuesTurns];
+    int s[kValuesTurns];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float2 f = e2m1x2_to_f32x2((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-            v[2 * j] = f.x * up;
-            v[2 * j + 1] = f.y * up;
+    for (int j = 0; j < kValuesTurns; j++) {
+        const size_t i = i0 + 256 * j;
+        if (i >= all) continue;
+        if (E2M1)
+            q[j].x = reinterpret_cast<const uint32_t*>(a.codes)[i];
+        else
+            q[j] = reinterpret_cast<const uint2*>(a.codes)[i];
+        if (groups % per == 0) {
+            s[j] = a.scales[i / per];
+        } else {
+            const uint32_t row = (uint32_t)(i / groups);
+            s[j] = a.scales[(size_t)row * ((groups + per - 1) / per) + (int)(i - (size_t)row * groups) / per];
         }
-    } else {
-        const uint4 q = *reinterpret_cast<const uint4*>(a.codes + i * 16);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 16; j++) v[j] = e4m3_value(w[j / 4] >> (8 * (j & 3))) * up;
     }
-    if (F32) {
-        float4* out = reinterpret_cast<float4*>(a.out) + i * 4;
 #pragma unroll
-        for (int j = 0; j < 4; j++) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-        uint4* out = reinterpret_cast<uint4*>(a.out) + i * 2;
-        out[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-        out[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+    for (int j = 0; j < kValuesTurns; j++) {
+        const size_t i = i0 + 256 * j;
+        if (i >= all) continue;
+        const float up = ue8m0_value(s[j]);
+        float v[8];
+        if (E2M1) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float2 f = e2m1x2_to_f32x2(q[j].x >> (8 * e));
+                v[2 * e] = f.x * up;
+                v[2 * e + 1] = f.y * up;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = e4m3_value((e < 4 ? q[j].x : q[j].y) >> (8 * (e & 3))) * up;
+        }
+        if (F32) {
+            float4* out = reinterpret_cast<float4*>(a.out) + i * 2;
+            out[0] = make_float4(v[0], v[1], v[2], v[3]);
+            out[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            reinterpret_cast<uint4*>(a.out)[i] =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        }
     }
 }
 
@@ -138,13 +151,13 @@ cudaError_t launch_mx_quant(const MxQuantArgs& a0, cudaStream_t s)
 {
     MxQuantArgs a = a0;
     void* args[] = {&a};
-    // four loads a thread where that leaves every SM a few blocks (16384 x 4096 to E2M1 29 us,
-    // with one 37), else one (77 x 2880 3.5 -> 2.9 us, quantisation and values)
+    // two loads a thread where that leaves every SM many blocks (16384 x 4096 to E4M3 32.2 us, with
+    // one 44, with four 34.4), else one (77 x 2880, quantisation and values, 2.9 us, with four 3.5)
     const long long groups = (long long)a.rows * (a.e2m1 ? a.n / 8 : (a.n + 127) / 128 * 16);
     const bool many = groups > 4 * 1024 * 152;
-    const void* fn = a.e2m1 ? (many ? (const void*)k_mx_quant<1, 4> : (const void*)k_mx_quant<1, 1>)
-                            : (many ? (const void*)k_mx_quant<0, 4> : (const void*)k_mx_quant<0, 1>);
-    const int per = many ? 1024 : 256;
+    const void* fn = a.e2m1 ? (many ? (const void*)k_mx_quant<1, 2> : (const void*)k_mx_quant<1, 1>)
+                            : (many ? (const void*)k_mx_quant<0, 2> : (const void*)k_mx_quant<0, 1>);
+    const int per = many ? 512 : 256;
     return launch(fn, (groups + per - 1) / per, 256, s, args);
 }
 
@@ -154,7 +167,8 @@ cudaError_t launch_mx_values(const MxValuesArgs& a0, cudaStream_t s)
     void* args[] = {&a};
     const void* fn = a.e2m1 ? (a.out_f32 ? (const void*)k_mx_values<1, 1> : (const void*)k_mx_values<1, 0>)
                             : (a.out_f32 ? (const void*)k_mx_values<0, 1> : (const void*)k_mx_values<0, 0>);
-    return launch(fn, ((long long)a.rows * a.n / 16 + 255) / 256, 256, s, args);
+    const long long per = 256 * kValuesTurns;
+    return launch(fn, ((long long)a.rows * a.n / 8 + per - 1) / per, 256, s, args);
 }
 
 cudaError_t launch_mx_pack(const MxPackArgs& a0, cudaStream_t s)

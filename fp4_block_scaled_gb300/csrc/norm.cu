@@ -145,23 +145,18 @@ __global__ void __launch_bounds__(ROW ? 32 * kNormWarps : 1024) k_norm(NormArgs 
                 for (int i = 0; i < 8; i++) v[j][i] *= inv;
             }
             // the codes are those of the bf16 output
-            const uint4 u = bf16x8(v[j]);
+            uint4 u = bf16x8(v[j]);
             if (a.out && in) *reinterpret_cast<uint4*>(a.out + base + 8 * g) = u;
             if (CODES == 0) continue;
-            if (in) {
-                unpack8(u, v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
-            }
+            if (!in) u = make_uint4(0, 0, 0, 0);
             int s;
             if (CODES == 1) {
-                const uint2 c = e4m3_codes8(v[j], s);
+                const uint2 c = e4m3_quantise(u, s);
                 if (!in) continue;
                 *reinterpret_cast<uint2*>(a.codes + base + 8 * g) = c;
                 if (g % 16 == 0) a.scales[(size_t)t * ((a.n + 127) / 128) + g / 16] = (uint8_t)s;
             } else {
-                const uint32_t c = e2m1_codes8(v[j], s);
+                const uint32_t c = e2m1_quantise(u, s);
                 if (!in) continue;
                 *reinterpret_cast<uint32_t*>(a.codes + (base + 8 * g) / 2) = c;
                 if (g % 4 == 0) a.scales[(size_t)t * (a.n / 32) + g / 4] = (uint8_t)s;
