@@ -24,7 +24,7 @@ constexpr uint32_t kOutBytes = 32 * 128;        // of an epilogue warp's box
 constexpr int kShared = 48, kScaleCols = 2 * kFeatures - kShared;
 
 struct __align__(1024) Control {
-    uint64_t full[kRing], peer[kRing], empty[kRing], acc_full, acc_empty, drain;
+    uint64_t full[kRing], empty[kRing], acc_full, acc_empty, drain;
     uint32_t tmem;
     int abort;
 };
@@ -125,6 +125,71 @@ __device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap
     }
 }
 
+// The thread of the pair that issues for both CTAs.  (Little is computed between its
+// instructions, as in linear.cu.)
+template <int E2M1>
+__device__ __forceinline__ bool multiply(Control& ctl, uint8_t* ring, uint32_t tmem, int steps, int first, int tiles, int stride)
+{
+    using S = Stage<E2M1>;
+    constexpr uint32_t kUnit = kLinAtom / 16;
+    const uint64_t ad0 = desc_sw128(smem_u32(ring)), sd0 = umma_desc(smem_u32(ring) + S::sfa, 16, 128);
+    const uint32_t sf0 = tmem + kScaleCols;
+    uint32_t slot = 0, parity = 0, cols = 0, it = 0;
+    // the stage whose products are the last to read the scales' columns that come next
+    uint32_t before = (uint32_t)kRing - S::slots, before_parity = 1;
+    for (int i = first; i < tiles; i += stride, it++) {
+        const uint32_t acc = tmem + (it & 1) * (kFeatures - kShared);
+        for (int k = 0; k < steps; k++) {
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
+            if (!mbar_wait_or_abort(&ctl.empty[before], before_parity, &ctl.abort, kLinWaitNs)) return false;
+            tc_fence_after();
+            const uint64_t ad = ad0 + slot * (S::bytes / 16), sd = sd0 + slot * (S::bytes / 16);
+            const uint32_t sfa = sf0 + cols, sfb = sfa + 4 * S::kAtoms;
+#pragma unroll
+            for (int h = 0; h < S::kAtoms; h++) cp_scales(sfa + 4 * h, sd + h * kUnit);
+#pragma unroll
+            for (int h = 0; h < 2 * S::kAtoms; h++) cp_scales(sfb + 4 * h, sd + (S::kAtoms + h) * kUnit);
+            // the tile before has left the shared columns (and with them the one before it everything)
+            if (k == 0 && it > 0 && !mbar_wait_or_abort(&ctl.acc_empty, (it - 1) & 1, &ctl.abort, kLinWaitNs)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int h = E2M1 ? j / 2 : 0;
+                mma<E2M1>(acc, ad + 2 * j, ad + S::b / 16 + 2 * j, idesc<E2M1>(E2M1 ? 2 * (j & 1) : j), sfa + 4 * h, sfb + 8 * h, k > 0 || j > 0);
+            }
+            commit_both(&ctl.empty[slot]);
+            if (++slot == (uint32_t)kRing) {
+                slot = 0;
+                parity ^= 1;
+            }
+            if (++before == (uint32_t)kRing) {
+                before = 0;
+                before_parity ^= 1;
+            }
+            cols = cols + S::cols == (uint32_t)(S::slots * S::cols) ? 0 : cols + S::cols;
+        }
+        commit_both(&ctl.acc_full);
+    }
+    return true;
+}
+
+// The other CTA's: tells the first that its half of a stage is there.
+template <int E2M1>
+__device__ __forceinline__ bool relay(Control& ctl, int steps, int first, int tiles, int stride)
+{
+    uint32_t slot = 0, parity = 0;
+    for (int i = first; i < tiles; i += stride)
+        for (int k = 0; k < steps; k++) {
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
+            arrive_at(&ctl.full[slot], 0);
+            if (++slot == (uint32_t)kRing) {
+                slot = 0;
+                parity ^= 1;
+            }
+        }
+    return true;
+}
+
 template <int E2M1, int F32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -138,8 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRing; s++) {
-            mbar_init(&ctl.full[s], 2);
-            mbar_init(&ctl.peer[s], 1);
+            mbar_init(&ctl.full[s], rank == 0 ? 3 : 2);     // copies, scales; the other CTA's full
             mbar_init(&ctl.empty[s], 1);
         }
         mbar_init(&ctl.acc_full, 1);
@@ -206,43 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
-            bool ok = true;
-            for (int i = first; i < tiles && ok; i += stride, it++) {
-                const uint32_t acc = tmem + (it & 1) * (kFeatures - kShared);
-                // the tile before has left the shared columns (and with them the one before it everything)
-                if (rank == 0 && it > 0) ok = mbar_wait_or_abort(&ctl.acc_empty, (it - 1) & 1, &ctl.abort, kLinWaitNs);
-                for (int k = 0; k < steps && ok; k++, c++) {
-                    const uint32_t slot = c % kRing, parity = c / kRing & 1;
-                    ok = mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs);
-                    if (!ok) break;
-                    if (rank != 0) {                            // tell the CTA that issues for both
-                        arrive_at(&ctl.peer[slot], 0);
-                        continue;
-                    }
-                    ok = mbar_wait_or_abort(&ctl.peer[slot], parity, &ctl.abort, kLinWaitNs);
-                    // the scales' columns are free once the products that read them are done
-                    const uint32_t before = c - S::slots;
-                    if (ok && c >= (uint32_t)S::slots)
-                        ok = mbar_wait_or_abort(&ctl.empty[before % kRing], before / kRing & 1, &ctl.abort, kLinWaitNs);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(ring + slot * S::bytes);
-                    const uint32_t sfa = tmem + kScaleCols + c % S::slots * S::cols, sfb = sfa + 4 * S::kAtoms;
-                    const uint64_t sd = umma_desc(st + S::sfa, 16, 128), ad = desc_sw128(st);
-#pragma unroll
-                    for (int h = 0; h < S::kAtoms; h++) cp_scales(sfa + 4 * h, sd + h * (kLinAtom / 16));
-#pragma unroll
-                    for (int h = 0; h < 2 * S::kAtoms; h++) cp_scales(sfb + 4 * h, sd + (S::kAtoms + h) * (kLinAtom / 16));
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int h = E2M1 ? j / 2 : 0;
-                        mma<E2M1>(acc, ad + 2 * j, ad + S::b / 16 + 2 * j, idesc<E2M1>(E2M1 ? 2 * (j & 1) : j), sfa + 4 * h, sfb + 8 * h,
-                                  k > 0 || j > 0);
-                    }
-                    commit_both(&ctl.empty[slot]);
-                }
-                if (ok && rank == 0) commit_both(&ctl.acc_full);
-            }
+            const bool ok = rank == 0 ? multiply<E2M1>(ctl, ring, tmem, steps, first, tiles, stride)
+                                      : relay<E2M1>(ctl, steps, first, tiles, stride);
             if (!ok) {
                 give_up(a, &ctl.abort);
                 if (rank == 0) {
