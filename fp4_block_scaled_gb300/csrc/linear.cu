@@ -5,7 +5,26 @@
 // A tile is 128 output features (the MMA's rows) by nt tokens (its columns, a
 // multiple of 16).  A stage of the ring is 128 bytes of K of both operands, which TMA
 // brings in the 128-byte swizzle that the MMA reads: 256 elements of E2M1, or 128 of
-// E4M3, for which TMA expands the weights to a byte an element on their way.
+// E4M3, for which TMA expands the weights to a byte an element on their way (HBM and L2
+// hold them packed).  Scales lie beside them as the atoms that tcgen05.cp moves; the
+// weights' were packed so, the tokens' are gathered from their rows by warps of their own,
+// or made there from a few tokens of bf16.
+//
+// Few tiles are cut along K between the CTAs of a cluster, which send one another their sums
+// by bulk copies between their shared memories and add them in a fixed order: a join
+// through global memory would cost a ticket's round trip more.
+//
+// Roles: warps 0-3 epilogue, 4 TMA, 5 MMA, 6-13 the tokens' scales.  The weights of a CTA's
+// first stages are fetched before the kernel ahead has finished, its tokens after it.
+//
+// Bounds (GB300, in CUDA graphs of such products with other weights each): a single token by
+// 4096 x 6144 in E2M1 takes 5.1 us where its 13.4 MB are 2.0 at the copy rate, 64 tokens by
+// 4096 x 4096 in E4M3 8.8: the latencies of a start (dependency wait, tokens, first product:
+// 1.1 us), of the stages (0.24 us each, or 2.6 cycles a row of a TMA box), of the sums' way
+// to their CTA (1 us) and of the end.  What counted: operands of tcgen05 instructions in uniform
+// registers (elect.sync; with a lane chosen by its number each took 120 cycles, not 40), scales
+// loaded ahead of the wait for their slot, weights before the dependency wait.  From about
+// 200 tokens on pairs of CTAs (linear_pair.cu) are faster.
 #include <math.h>
 
 #include <algorithm>
@@ -45,7 +64,6 @@ struct Plan {
     int sfcols;                 // tensor memory columns of a stage's scales
     int tmem;                   // columns in all
     int acc;                    // column of the second accumulator (0: there is one)
-    int ahead;                  // fetch weights into L2 before the kernel ahead is done
 };
 
 template <int E2M1>
@@ -187,6 +205,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kWarpProd) {
         if (elect_one()) {
             bool ok = true, waited = false;
+            // then the tokens of the stages whose weights are on their way
+            const auto wait = [&](int early, int t0) {
+                if (waited) return;
+                pdl_wait();
+                waited = true;
+                if (!QUANT)
+                    for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
+            };
             for (int i = first; i < tiles && ok; i += stride) {
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
                 // The weights of as many stages as there are come while the kernel before this
@@ -197,12 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         prefetch_l2(a.packed + ((size_t)rt * p.units + (E2M1 ? k : k / 2)) * kLinUnitBytes, kLinUnitBytes);
                 for (int k = k0; k < k1; k++, c++) {
                     const uint32_t slot = c % p.ring;
-                    if (k == k0 + early && !waited) {
-                        pdl_wait();
-                        waited = true;
-                        if (!QUANT)
-                            for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
-                    }
+                    if (k == k0 + early) wait(early, t0);
                     if (!mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
                         give_up(a, &ctl.abort);
                         ok = false;
@@ -218,12 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     bulk_g2s(st + p.sfa, a.packed + (size_t)z * kLinUnitBytes + kLinCodeBytes + half * kLinAtom, sf, bar);
                     if (!QUANT && waited) tma_2d(st + p.b, &xmap, k * 128, t0, bar);
                 }
-                if (!waited) {
-                    pdl_wait();
-                    waited = true;
-                    if (!QUANT)
-                        for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
-                }
+                wait(early, t0);
             }
             // no copy may be in flight into this CTA's memory at its end
             for (uint32_t m = c > (uint32_t)p.ring ? c - p.ring : 0; m < c; m++)
@@ -390,6 +406,37 @@ double pair_cost(const LinearArgs& a, int steps)
     return 4.5 + waves * (steps * (a.e2m1 ? 0.37 : 0.31) + (a.N % (a.out_f32 ? 4 : 8) ? 3.0 : 0.0));
 }
 
+// Shared and tensor memory of a plan whose tile and split are set; false if it has no room.
+bool lay_out(const LinearArgs& a, Plan& p)
+{
+    const int sf = p.nt > 128 ? 2 : 1, h = a.e2m1 ? 2 : 1, slice = (p.steps + p.split - 1) / p.split;
+    p.b = kLinCodeBytes;
+    p.sfa = p.b + p.nt * 128;
+    p.sfb = p.sfa + h * kLinAtom;
+    p.stage = (p.sfb + h * sf * kLinAtom + 1023) / 1024 * 1024;
+    p.width = (p.nt + p.split - 1) / p.split;
+    p.sfcols = 4 * h * (1 + sf);
+    const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0, fixed = sizeof(Control) + part;
+    const bool one = p.split > 1 || tiles_of(p) <= a.sms;       // a CTA has one tile
+    p.acc = one ? 0 : p.nt;
+    p.ring = std::min({kRing, (int)((kLinSmemMax - fixed) / p.stage), (512 - p.nt - p.acc) / p.sfcols, one ? std::max(slice, 3) : kRing});
+    // Where four stages fit half an SM, two CTAs share one, so that a kernel can begin beside the
+    // one before it, each with at most half of the tensor memory (one token by 4096 x 6144 6.5 us,
+    // before 6.8; their registers allow no third).  Else a CTA takes more than half of the
+    // shared memory: no two CTAs of clusters may share an SM and wait for each other's tensor
+    // memory.
+    const int two = fixed < kLinSmemTwo ? (int)((kLinSmemTwo - fixed) / p.stage) : 0;
+    const bool share = one && two >= 4 && p.nt + std::min(p.ring, two) * p.sfcols <= 256;
+    if (share) p.ring = std::min(p.ring, two);
+    p.loaders = std::min(kLoadWarps, p.ring);
+    p.part = sizeof(Control) + p.ring * p.stage;
+    p.smem = share ? p.part + part : std::max(p.part + part, kLinSmemMax / 2 + 4096);
+    p.tmem = 32;
+    while (p.tmem < p.nt + p.acc + p.ring * p.sfcols) p.tmem *= 2;
+    // a split tile's sums are laid down in the ring
+    return p.ring >= 3 && (p.split == 1 || p.ring * p.stage >= (uint32_t)p.nt * kLinRows * 4);
+}
+
 // The cheapest tile and split; no tile (nt = 0) where pairs of CTAs are cheaper.
 Plan make_plan(const LinearArgs& a)
 {
@@ -399,54 +446,27 @@ Plan make_plan(const LinearArgs& a)
     p.units = lin_units(a.K);
     Plan best = p;
     double least = a.codes && a.T > 64 ? pair_cost(a, p.steps) : HUGE_VAL;
-    // (beyond that no tile of one CTA was cheaper)
+    // (beyond 4096 tokens no tile of one CTA was cheaper)
     const int widest = a.codes && a.T > 4096 ? 0 : std::min(kMaxNt, (a.T + 15) / 16 * 16);
     for (p.nt = widest; p.nt > 0; p.nt -= 16) {
         const int ttiles = (a.T + p.nt - 1) / p.nt;
-        if (ttiles == p.ttiles) continue;       // no fewer tokens a tile than that needs: below
+        if (ttiles == p.ttiles) continue;
         p.ttiles = ttiles;
         Plan q = p;
-        q.nt = ((a.T + ttiles - 1) / ttiles + 15) / 16 * 16;
+        q.nt = ((a.T + ttiles - 1) / ttiles + 15) / 16 * 16;    // no more than so many tiles need
         const long long tiles = tiles_of(q);
         for (q.split = 1; q.split <= std::min(kSplitMax, q.steps); q.split++) {
             // clusters that run at once: two CTAs an SM where they are small
             if (q.split > 1 && (tiles * q.split > a.sms || tiles > g_clusters[q.split] * (q.nt <= 32 ? 2 : 1))) break;
             const double cost = tile_cost(a, q);
-            if (cost < least) {
+            if (cost < least && lay_out(a, q)) {
                 least = cost;
                 best = q;
             }
         }
         if (tiles > 8 * a.sms) break;
     }
-    p = best;
-    if (p.nt == 0) return p;
-    const uint32_t sf = p.nt > 128 ? 2 : 1, h = a.e2m1 ? 2 : 1;
-    p.b = kLinCodeBytes;
-    p.sfa = p.b + p.nt * 128;
-    p.sfb = p.sfa + h * kLinAtom;
-    p.stage = (p.sfb + h * sf * kLinAtom + 1023) / 1024 * 1024;
-    p.width = (p.nt + p.split - 1) / p.split;
-    const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0;
-    p.sfcols = 4 * h * (1 + sf);
-    p.ring = std::min({kRing, (int)((kLinSmemMax - sizeof(Control) - part) / p.stage), (512 - 2 * p.nt) / p.sfcols,
-                       std::max(3, (int)(p.split > 1 ? (p.steps + p.split - 1) / p.split : kRing))});
-    // Where four stages of weights fit half an SM, two CTAs share one, so that a kernel can begin
-    // beside the one before it, each with at most half of the tensor memory.  Else a CTA takes
-    // more than half of the shared memory, so that no two CTAs of clusters share an SM and wait
-    // for each other's tensor memory.
-    const bool one = p.split > 1 || tiles_of(p) <= a.sms;
-    const int two = (int)((kLinSmemTwo - sizeof(Control) - part) / p.stage);
-    p.ahead = one && part < kLinSmemTwo / 2 && two >= 4;
-    if (p.ahead) p.ring = std::min(p.ring, two);
-    p.loaders = std::min(kLoadWarps, p.ring);
-    p.part = sizeof(Control) + p.ring * p.stage;
-    p.smem = p.part + part;
-    if (!p.ahead) p.smem = std::max(p.smem, kLinSmemMax / 2 + 4096);
-    p.acc = one ? 0 : p.nt;
-    p.tmem = 32;
-    while (p.tmem < p.nt + p.acc + p.ring * p.sfcols) p.tmem *= 2;
-    return p;
+    return best;
 }
 
 }  // namespace

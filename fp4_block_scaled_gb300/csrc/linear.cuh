@@ -131,13 +131,6 @@ __device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]
         : "r"(taddr));
 }
 
-// A whole sector of 32 bytes by one thread.
-__device__ __forceinline__ void st_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
-
 // Four scale bytes of a row from `at`, 0 behind its end.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n)
 {

@@ -2,6 +2,13 @@
 // and the block formats behind it, in one pass: a row stays in the registers of the
 // threads that hold it, so that it is read once and everything made of it is
 // written once.
+//
+// u = r / sqrt(mean(r^2) + eps) * w with r = x + residual: the sum of squares is the only thing
+// that the threads of a row exchange (shuffles, and one barrier where a CTA holds the row).
+// Bound by HBM: 16384 rows of 4096, bf16 with a bf16 residual, to bf16 and E4M3, 91 us (98 % of
+// the copy rate); 16384 of 4096 without a residual 43 us (92 %); 4099 of 2880 14.6 us (84 %: 1.7
+// rounds of rows); a million of 128 93 us (81 %).  One row of 4096 takes 1.7 us, 128 rows 3.3:
+// a launch, a trip to memory, two exchanges.
 #include <algorithm>
 
 #include "common.cuh"

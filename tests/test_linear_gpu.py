@@ -51,7 +51,7 @@ def check(y, q, s, w, fmt, out="f32", some=None):
 @pytest.mark.parametrize("T,K,N", [
     (1, 32, 1), (1, 64, 64), (2, 96, 127), (1, 256, 128), (3, 288, 129), (1, 4096, 640), (7, 2880, 384), (16, 4096, 1000), (17, 1024, 256),
     (33, 512, 257), (64, 2080, 4096), (100, 160, 130), (130, 2880, 384), (200, 4096, 512), (257, 4096, 128), (333, 2880, 4099), (800, 544, 96),
-    (2000, 256, 1000)])
+    (2000, 256, 1000), (4200, 64, 1), (4500, 96, 24), (4097, 1056, 258)])
 def test_sizes(fmt, T, K, N):
     rng = np.random.default_rng([T, K, N])
     with handle(T, K) as h:
