@@ -294,22 +294,41 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_after();
             const int cols = (int)min((long long)p.nt, a.T - t0);
             const uint32_t from = tmem + buf * p.acc + ((uint32_t)(32 * warp) << 16);
-            float* mine = reinterpret_cast<float*>(ring) + 32 * warp + lane;
-            size_t at = (size_t)t0 * a.N + n;
-            for (int c0 = 0; c0 < cols; c0 += 32) {
-                uint32_t r[2][16];
-                const int have = cols - c0;
-                tc_ld16_nowait(from + c0, r[0]);
-                if (have > 16) tc_ld16_nowait(from + c0 + 16, r[1]);
-                tc_wait_ld();
-                tc_ld_fence_regs<16>(r[0]);
-                tc_ld_fence_regs<16>(r[1]);
-                if (p.split > 1) {
-                    // (the ring is free: every product is done)
+            if (p.split > 1) {
+                // CTA o adds up the columns o * width ..: every CTA sends it its own sums of them, by
+                // way of its ring, which is free (every product is done), 16 columns or an owner's
+                // at a time and its neighbour's first, so that copies and reads overlap.
+                const int own = min(p.width, cols - (int)rank * p.width), group = max(1, 16 / p.width), groups = (p.split + group - 1) / group;
+                if (warp == 0 && own > 0 && elect_one()) mbar_arrive_expect_tx(&ctl.red, p.split * own * kLinRows * 4);
+                float* mine = reinterpret_cast<float*>(ring) + 32 * warp + lane;
+                for (int d = 1; d <= groups; d++) {
+                    const int o0 = ((int)rank / group + d) % groups * group, c1 = min(min(o0 + group, p.split) * p.width, cols);
+                    if (o0 * p.width >= c1) continue;
+                    for (int c0 = o0 * p.width; c0 < c1; c0 += 16) {
+                        float v[16];
+                        tc_ld16(from + c0, v);
 #pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        if (j < have) mine[(c0 + j) * kLinRows] = __uint_as_float(r[j / 16][j % 16]);
-                } else if (n < a.N) {
+                        for (int j = 0; j < 16; j++)
+                            if (c0 + j < c1) mine[(c0 + j) * kLinRows] = v[j];
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    named_sync(1, 128);
+                    if (warp == 0 && elect_one())
+                        for (int o = o0; o * p.width < c1; o++)
+                            bulk_to_peer(smem_u32(smem + p.part) + rank * p.width * kLinRows * 4, smem_u32(ring) + o * p.width * kLinRows * 4,
+                                         min(p.width, c1 - o * p.width) * kLinRows * 4, smem_u32(&ctl.red), o);
+                }
+            } else {
+                size_t at = (size_t)t0 * a.N + n;
+                for (int c0 = 0; c0 < cols; c0 += 32) {
+                    uint32_t r[2][16];
+                    const int have = cols - c0;
+                    tc_ld16_nowait(from + c0, r[0]);
+                    if (have > 16) tc_ld16_nowait(from + c0 + 16, r[1]);
+                    tc_wait_ld();
+                    tc_ld_fence_regs<16>(r[0]);
+                    tc_ld_fence_regs<16>(r[1]);
+                    if (n >= a.N) continue;
                     if (a.out_f32) {
 #pragma unroll
                         for (int j = 0; j < 32; j++, at += a.N)
@@ -328,23 +347,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     if (p.split > 1) {
-        // One tile a cluster.  CTA r adds up the columns r * width ..: every CTA sends it its
-        // own sums of them, and they are added in the CTAs' order.
+        // One tile a cluster: its CTAs' sums are added in their order.
         const long long t0 = (long long)(first / p.rtiles) * p.nt, n0 = (long long)(first % p.rtiles) * kLinRows + 4 * lane;
         const int cols = (int)min((long long)p.nt, a.T - t0), here = min(p.width, cols - (int)rank * p.width);
-        if (warp < 4) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            named_sync(1, 128);
-            if (warp == 0 && elect_one()) {
-                if (here > 0) mbar_arrive_expect_tx(&ctl.red, p.split * here * kLinRows * 4);
-                for (int o = 0; o < p.split; o++) {
-                    const int m = min(p.width, cols - o * p.width);
-                    if (m > 0)
-                        bulk_to_peer(smem_u32(smem + p.part) + rank * p.width * kLinRows * 4, smem_u32(ring) + o * p.width * kLinRows * 4,
-                                     m * kLinRows * 4, smem_u32(&ctl.red), o);
-                }
-            }
-        }
         // (the producer's and the MMA's warps have no part in it)
         const int adder = warp < 4 ? warp : warp - 2, adders = 4 + kLoadWarps;
         if (here > adder && (warp < 4 || warp >= kWarpLoad)) {
