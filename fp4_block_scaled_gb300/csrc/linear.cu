@@ -53,6 +53,7 @@ struct Plan {
     int units;                  // of the packed weights along K
     int split;                  // CTAs along K
     int width;                  // columns that each of them sums
+    int group, groups;          // CTAs whose columns leave together, and how many times
     int ring;
     // Warps that load scales, a stage each in turn: no more than the ring has stages, or a
     // warp could wait for a slot that is two rounds behind it, whose barrier has the parity
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const long long t0 = (long long)(i / p.rtiles) * p.nt, n = (long long)(i % p.rtiles) * kLinRows + 32 * warp + lane;
             const uint32_t buf = it & 1;
             bool ok = mbar_wait_or_abort(&ctl.acc_full[buf], it >> 1 & 1, &ctl.abort, kLinWaitNs);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            // (the warps of a split tile meet below: all of them go on, or none)
+            ok = p.split > 1 ? all_of(1, 128, ok) : __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
                 if (lane == 0) give_up(a, &ctl.abort);
                 break;
@@ -298,11 +300,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // CTA o adds up the columns o * width ..: every CTA sends it its own sums of them, by
                 // way of its ring, which is free (every product is done), 16 columns or an owner's
                 // at a time and its neighbour's first, so that copies and reads overlap.
-                const int own = min(p.width, cols - (int)rank * p.width), group = max(1, 16 / p.width), groups = (p.split + group - 1) / group;
+                const int own = min(p.width, cols - (int)rank * p.width);
                 if (warp == 0 && own > 0 && elect_one()) mbar_arrive_expect_tx(&ctl.red, p.split * own * kLinRows * 4);
                 float* mine = reinterpret_cast<float*>(ring) + 32 * warp + lane;
-                for (int d = 1; d <= groups; d++) {
-                    const int o0 = ((int)rank / group + d) % groups * group, c1 = min(min(o0 + group, p.split) * p.width, cols);
+                int turn = p.groups == 1 ? 0 : (int)rank / p.group;
+                for (int d = 0; d < p.groups; d++) {
+                    if (++turn >= p.groups) turn = 0;
+                    const int o0 = turn * p.group, c1 = min(min(o0 + p.group, p.split) * p.width, cols);
                     if (o0 * p.width >= c1) continue;
                     for (int c0 = o0 * p.width; c0 < c1; c0 += 16) {
                         float v[16];
@@ -420,6 +424,8 @@ bool lay_out(const LinearArgs& a, Plan& p)
     p.sfb = p.sfa + h * kLinAtom;
     p.stage = (p.sfb + h * sf * kLinAtom + 1023) / 1024 * 1024;
     p.width = (p.nt + p.split - 1) / p.split;
+    p.group = std::max(1, 16 / p.width);
+    p.groups = (p.split + p.group - 1) / p.group;
     p.sfcols = 4 * h * (1 + sf);
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0, fixed = sizeof(Control) + part;
     const bool one = p.split > 1 || tiles_of(p) <= a.sms;       // a CTA has one tile

@@ -85,6 +85,17 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Whether v holds in each of the `threads` threads that meet at named barrier `id`.
+__device__ __forceinline__ bool all_of(int id, int threads, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(threads), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ void give_up(const LinearArgs& a, int* abort)
 {
     atomicOr(a.status, kStatusTimeout);

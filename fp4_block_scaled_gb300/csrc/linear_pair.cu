@@ -13,7 +13,7 @@
 //
 // Bounds (GB300): 16384 tokens by 4096 x 6144 in E2M1 take 119 us from codes, 6.9 PFLOP/s, 92 %
 // of four times the measured bf16 rate (the K = 64 steps' nominal ratio); 8191 by 4096 x 5760 in
-// E4M3 109 us, 3.5 PFLOP/s, 94 % of twice that rate.  The tensor pipe is active 72 % and 84 % of
+// E4M3 109 us, 3.5 PFLOP/s, 94 % of twice that rate.  The tensor pipe is active 77 % and 89 % of
 // the time (ncu), the rest is the first stage of a tile behind the last of the one before, and
 // the last round of tiles.  What counted: arrivals at the other CTA's barriers that do not wait
 // for memory (with a release at cluster scope each took 1600 cycles, a stage 1750 in all),
