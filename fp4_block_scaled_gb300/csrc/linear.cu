@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
-    const int k0 = (int)((long long)p.steps * rank / p.split), k1 = (int)((long long)p.steps * (rank + 1) / p.split);
+    const int k0 = p.steps * (int)rank / p.split, k1 = p.steps * ((int)rank + 1) / p.split;     // (at most 8192 stages)
     const int tiles = p.ttiles * p.rtiles, first = (int)blockIdx.x / p.split, stride = (int)gridDim.x / p.split;
     uint32_t c = 0, it = 0;
     pdl_trigger();
@@ -260,15 +260,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp >= kWarpLoad) {
         pdl_wait();
-        bool ok = true;
-        for (int i = first; i < tiles && ok; i += stride) {
+        // every loaders-th stage
+        bool ok = warp - kWarpLoad < p.loaders;
+        uint32_t slot = warp - kWarpLoad, parity = 1;
+        int k = k0 + warp - kWarpLoad;
+        for (int i = first; i < tiles && ok; i += stride, k -= k1 - k0) {
             const int t0 = i / p.rtiles * p.nt;
-            for (int k = k0; k < k1; k++, c++) {
-                if (c % p.loaders != (uint32_t)(warp - kWarpLoad)) continue;
-                const uint32_t slot = c % p.ring;
+            for (; k < k1; k += p.loaders) {
                 Scales<E2M1, kMaxNt> sc;
                 if (!QUANT) sc.load(a, p.nt, t0, k, lane);
-                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs);
+                ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, kLinWaitNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (QUANT)
@@ -278,8 +279,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.full[slot]);
+                slot += p.loaders;
+                if (slot >= (uint32_t)p.ring) {
+                    slot -= p.ring;
+                    parity ^= 1;
+                }
             }
         }
+        ok = ok || warp - kWarpLoad >= p.loaders;
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
         pdl_wait();
