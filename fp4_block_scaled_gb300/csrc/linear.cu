@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     Control& ctl = *reinterpret_cast<Control*>(smem);
     uint8_t* ring = smem + sizeof(Control);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kRing; s++) {
-            mbar_init(&ctl.full[s], 2);
-            mbar_init(&ctl.empty[s], 1);
-        }
+    if (threadIdx.x < kRing) {
+        mbar_init(&ctl.full[threadIdx.x], 2);
+        mbar_init(&ctl.empty[threadIdx.x], 1);
+        mbar_fence_init();
+    } else if (threadIdx.x == 32) {
         for (int b = 0; b < 2; b++) {
             mbar_init(&ctl.acc_full[b], 1);
             mbar_init(&ctl.acc_empty[b], 4);
@@ -214,31 +214,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!QUANT)
                     for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
             };
+            uint32_t slot = 0, parity = 1;
             for (int i = first; i < tiles && ok; i += stride) {
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
+                const uint8_t* scales = a.packed + (size_t)rt * p.units * kLinUnitBytes + kLinCodeBytes;
                 // The weights of as many stages as there are come while the kernel before this
                 // one still runs, its tokens after it.
                 const int early = waited ? 0 : min(k1 - k0, p.ring);
                 if (!waited)
                     for (int k = k0 + early; k < k1; k += E2M1 ? 1 : 2)
-                        prefetch_l2(a.packed + ((size_t)rt * p.units + (E2M1 ? k : k / 2)) * kLinUnitBytes, kLinUnitBytes);
+                        prefetch_l2(scales - kLinCodeBytes + (size_t)(E2M1 ? k : k / 2) * kLinUnitBytes, kLinUnitBytes);
                 for (int k = k0; k < k1; k++, c++) {
-                    const uint32_t slot = c % p.ring;
                     if (k == k0 + early) wait(early, t0);
-                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / p.ring & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
+                    if (!mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, kLinWaitNs)) {
                         give_up(a, &ctl.abort);
                         ok = false;
                         break;
                     }
                     uint8_t* st = ring + slot * p.stage;
                     uint64_t* bar = &ctl.full[slot];
-                    const int z = rt * p.units + (E2M1 ? k : k / 2), half = E2M1 ? 0 : k & 1;
+                    const int u = E2M1 ? k : k / 2, half = E2M1 ? 0 : k & 1;
                     const uint32_t sf = E2M1 ? 2 * kLinAtom : kLinAtom;
                     // (expanded weights count as the bytes that were read)
                     mbar_arrive_expect_tx(bar, (E2M1 ? kLinCodeBytes : kLinCodeBytes / 2) + sf + (QUANT ? 0 : p.nt * 128));
-                    tma_3d(st, &wmap, half * 128, 0, z, bar);
-                    bulk_g2s(st + p.sfa, a.packed + (size_t)z * kLinUnitBytes + kLinCodeBytes + half * kLinAtom, sf, bar);
+                    tma_3d(st, &wmap, half * 128, 0, rt * p.units + u, bar);
+                    bulk_g2s(st + p.sfa, scales + (size_t)u * kLinUnitBytes + half * kLinAtom, sf, bar);
                     if (!QUANT && waited) tma_2d(st + p.b, &xmap, k * 128, t0, bar);
+                    if (++slot == (uint32_t)p.ring) {
+                        slot = 0;
+                        parity ^= 1;
+                    }
                 }
                 wait(early, t0);
             }

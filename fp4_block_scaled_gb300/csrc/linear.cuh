@@ -165,6 +165,7 @@ struct Scales {
         const int n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
 #pragma unroll
         for (int i = 0; i < ROWS / 32; i++) {
+            if (32 * i >= rows) break;
             const int r = lane + 32 * i;
             const bool in = r < rows && t0 + r < a.T;
             const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
