@@ -201,31 +201,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
     const int k0 = p.steps * (int)rank / p.split, k1 = p.steps * ((int)rank + 1) / p.split;     // (at most 8192 stages)
     const int tiles = p.ttiles * p.rtiles, first = (int)blockIdx.x / p.split, stride = (int)gridDim.x / p.split;
+    const int early = min(k1 - k0, p.ring);     // stages whose weights come first
     uint32_t c = 0, it = 0;
     pdl_trigger();
     if (warp == kWarpProd) {
         if (elect_one()) {
             bool ok = true, waited = false;
-            // then the tokens of the stages whose weights are on their way
-            const auto wait = [&](int early, int t0) {
-                if (waited) return;
-                pdl_wait();
-                waited = true;
-                if (!QUANT)
-                    for (int e = 0; e < early; e++) tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, t0, &ctl.full[e]);
-            };
             uint32_t slot = 0, parity = 1;
             for (int i = first; i < tiles && ok; i += stride) {
                 const int rt = i % p.rtiles, t0 = i / p.rtiles * p.nt;
                 const uint8_t* scales = a.packed + (size_t)rt * p.units * kLinUnitBytes + kLinCodeBytes;
                 // The weights of as many stages as there are come while the kernel before this
-                // one still runs, its tokens after it.
-                const int early = waited ? 0 : min(k1 - k0, p.ring);
+                // one still runs; their tokens the MMA's thread fetches after it.
                 if (!waited)
                     for (int k = k0 + early; k < k1; k += E2M1 ? 1 : 2)
                         prefetch_l2(scales - kLinCodeBytes + (size_t)(E2M1 ? k : k / 2) * kLinUnitBytes, kLinUnitBytes);
                 for (int k = k0; k < k1; k++, c++) {
-                    if (k == k0 + early) wait(early, t0);
+                    if (k == k0 + early && !waited) {
+                        pdl_wait();
+                        waited = true;
+                    }
                     if (!mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, kLinWaitNs)) {
                         give_up(a, &ctl.abort);
                         ok = false;
@@ -245,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         parity ^= 1;
                     }
                 }
-                wait(early, t0);
+                if (!waited) pdl_wait();
+                waited = true;
             }
             // no copy may be in flight into this CTA's memory at its end
             for (uint32_t m = c > (uint32_t)p.ring ? c - p.ring : 0; m < c; m++)
@@ -254,6 +250,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
+            if (!QUANT) {
+                // (their bytes may be there before the weights' thread expects them: it is its
+                // arrival that the barrier's phase waits for)
+                pdl_wait();
+                for (int e = 0; e < early && first < tiles; e++)
+                    tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, first / p.rtiles * p.nt, &ctl.full[e]);
+            }
             const bool ok = p.nt > 128 ? multiply<E2M1, 2>(p, ctl, ring, tmem, k0, k1, first, tiles, stride)
                                        : multiply<E2M1, 1>(p, ctl, ring, tmem, k0, k1, first, tiles, stride);
             if (!ok) {
@@ -320,12 +323,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (++turn >= p.groups) turn = 0;
                     const int o0 = turn * p.group, c1 = min(min(o0 + p.group, p.split) * p.width, cols);
                     if (o0 * p.width >= c1) continue;
-                    for (int c0 = o0 * p.width; c0 < c1; c0 += 16) {
-                        float v[16];
-                        tc_ld16(from + c0, v);
+                    for (int c0 = o0 * p.width; c0 < c1; c0 += 32) {
+                        uint32_t r[2][16];
+                        const int have = c1 - c0;
+                        tc_ld16_nowait(from + c0, r[0]);
+                        if (have > 16) tc_ld16_nowait(from + c0 + 16, r[1]);
+                        tc_wait_ld();
+                        tc_ld_fence_regs<16>(r[0]);
+                        tc_ld_fence_regs<16>(r[1]);
 #pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (c0 + j < c1) mine[(c0 + j) * kLinRows] = v[j];
+                        for (int j = 0; j < 32; j++)
+                            if (j < have) mine[(c0 + j) * kLinRows] = __uint_as_float(r[j / 16][j % 16]);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     named_sync(1, 128);
