@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t from = tmem + buf * p.acc + ((uint32_t)(32 * warp) << 16);
             if (p.split > 1) {
                 // CTA o adds up the columns o * width ..: every CTA sends it its own sums of them, by
-                // way of its ring, which is free (every product is done), 16 columns or an owner's
+                // way of its ring, which is free (every product is done), 32 columns or an owner's
                 // at a time and its neighbour's first, so that copies and reads overlap.
                 const int own = min(p.width, cols - (int)rank * p.width);
                 if (warp == 0 && own > 0 && elect_one()) mbar_arrive_expect_tx(&ctl.red, p.split * own * kLinRows * 4);
@@ -444,7 +444,7 @@ bool lay_out(const LinearArgs& a, Plan& p)
     p.sfb = p.sfa + h * kLinAtom;
     p.stage = (p.sfb + h * sf * kLinAtom + 1023) / 1024 * 1024;
     p.width = (p.nt + p.split - 1) / p.split;
-    p.group = std::max(1, 16 / p.width);
+    p.group = std::max(1, 32 / p.width);
     p.groups = (p.split + p.group - 1) / p.group;
     p.sfcols = 4 * h * (1 + sf);
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0, fixed = sizeof(Control) + part;

@@ -240,22 +240,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     pdl_trigger();
-    pdl_wait();
 
     const int steps = E2M1 ? units : (a.K + 127) / 128;
     const int tiles = (int)((a.T + kTokens - 1LL) / kTokens) * ftiles, first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int rtiles = (a.N + kLinRows - 1) / kLinRows;
+    const int early = min(steps, kRing);        // stages whose weights come before the kernel ahead is done
     uint32_t c = 0, it = 0;
 
     if (warp == kWarpProd) {
         if (elect_one()) {
-            bool ok = true;
+            bool ok = true, waited = false;
             for (int i = first; i < tiles && ok; i += stride) {
                 const int f = i % ftiles, t0 = i / ftiles * kTokens + (int)rank * 128;
                 // (a pair's second tile of weights may be behind the last: its features are not stored)
                 const int w0 = min(2 * f, rtiles - 1) * units, w1 = min(2 * f + 1, rtiles - 1) * units;
                 for (int k = 0; k < steps; k++, c++) {
                     const uint32_t slot = c % kRing;
+                    if (k == early && !waited) {
+                        pdl_wait();
+                        waited = true;
+                    }
                     if (!mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
                         give_up(a, &ctl.abort);
                         ok = false;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const uint32_t sf = S::kAtoms * kLinAtom;
                     // (expanded weights count as the bytes that were read)
                     mbar_arrive_expect_tx(bar, 128 * 128 + (E2M1 ? 128 * 128 : 128 * 64) + 2 * sf);
-                    tma_2d(st, &xmap, k * 128, t0, bar);
+                    if (waited) tma_2d(st, &xmap, k * 128, t0, bar);        // (else the MMA's thread does)
                     tma_3d(st + S::b, &wmap, half * 128, 0, (rank ? w1 : w0) + u, bar);
                     const uint8_t* scales = a.packed + kLinCodeBytes + half * kLinAtom;
 #pragma unroll
@@ -277,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         bulk_g2s(st + S::sfb + (2 * h + 1) * kLinAtom, scales + (size_t)(w1 + u) * kLinUnitBytes + h * kLinAtom, kLinAtom, bar);
                     }
                 }
+                if (!waited) pdl_wait();
+                waited = true;
             }
             for (uint32_t m = c > (uint32_t)kRing ? c - kRing : 0; m < c; m++)
                 if (!mbar_wait_or_abort(&ctl.full[m % kRing], m / kRing & 1, &ctl.abort, kLinWaitNs))
@@ -284,6 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
+            // (their bytes may be there before the weights' thread expects them: it is its arrival
+            // that the barrier's phase waits for)
+            pdl_wait();
+            for (int e = 0; e < early && first < tiles; e++)
+                tma_2d(ring + e * S::bytes, &xmap, e * 128, first / ftiles * kTokens + (int)rank * 128, &ctl.full[e]);
             const bool ok = rank == 0 ? multiply<E2M1>(ctl, ring, tmem, steps, first, tiles, stride)
                                       : relay<E2M1>(ctl, steps, first, tiles, stride);
             if (!ok) {
@@ -295,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
     } else if (warp >= kWarpLoad) {
+        pdl_wait();
         bool ok = true;
         for (int i = first; i < tiles && ok; i += stride) {
             const int t0 = i / ftiles * kTokens + (int)rank * 128;
@@ -314,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
+        pdl_wait();
         uint8_t* out = ring + kRing * S::bytes + warp * kOutBytes;
         for (int i = first; i < tiles; i += stride, it++) {
             const int n0 = i % ftiles * kFeatures;
