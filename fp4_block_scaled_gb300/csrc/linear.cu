@@ -18,13 +18,14 @@
 // first stages are fetched before the kernel ahead has finished, its tokens after it.
 //
 // Bounds (GB300, in CUDA graphs of such products with other weights each): a single token by
-// 4096 x 6144 in E2M1 takes 5.1 us where its 13.4 MB are 2.0 at the copy rate, 64 tokens by
-// 4096 x 4096 in E4M3 8.8: the latencies of a start (dependency wait, tokens, first product:
-// 1.1 us), of the stages (0.24 us each, or 2.6 cycles a row of a TMA box), of the sums' way
-// to their CTA (1 us) and of the end.  What counted: operands of tcgen05 instructions in uniform
-// registers (elect.sync; with a lane chosen by its number each took 120 cycles, not 40), scales
-// loaded ahead of the wait for their slot, weights before the dependency wait.  From about
-// 200 tokens on pairs of CTAs (linear_pair.cu) are faster.
+// 4096 x 6144 in E2M1 takes 4.5 us where its 13.4 MB are 2.0 at the copy rate, 64 tokens by
+// 4096 x 4096 in E4M3 6.8 from codes: the latencies of a start (dependency wait, tokens, first
+// product: 0.9 us), of the stages (0.2 us each, or 2.2 to 2.8 cycles a row of a TMA box), of
+// the sums' way to their CTA (0.7 us and more) and of the end.  What counted: operands of tcgen05
+// instructions in uniform registers (elect.sync; with a lane chosen by its number each took 120
+// cycles, not 40), scales loaded ahead of the wait for their slot, weights before the dependency
+// wait and the first tokens by another thread beside them, no divisions in the roles' loops.  For
+// many tokens pairs of CTAs (linear_pair.cu) are faster.
 #include <math.h>
 
 #include <algorithm>
@@ -414,25 +415,26 @@ int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
 long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 
 // Time of a product in microseconds, as measured in CUDA graphs of products one after the
-// other (K = 512 .. 8192, N = 512 .. 8192, T = 1 .. 1024, within 15 %): a start and end of
-// 4.2, the longer of a CTA's stages (a row of a TMA box takes about 2.6 cycles) and of what
-// all of them fetch through L2, and the epilogue; a split product's sums meet in 0.9 and 0.024
-// a token.
+// other (K = 512 .. 8192, N = 300 .. 8192, T = 1 .. 3000; what the rule takes is within 15 % of the
+// best tile and split): a start and end of 3.2, the longer of a CTA's stages (a row of a TMA
+// box takes 2.2 to 2.8 cycles) and of what all of them fetch through L2, and the
+// epilogue; a split product's sums meet in 0.2 and 0.02 a token.
 double tile_cost(const LinearArgs& a, const Plan& p)
 {
     const long long tiles = tiles_of(p);
     const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
-    const double serial = waves * ((p.steps + p.split - 1) / p.split) * std::max(0.24, (kLinRows + p.nt) * 0.00137);
-    const double feed = (double)tiles * p.steps * ((a.e2m1 ? 17408 : 8704) + p.nt * 132) * 1e-7;
-    return 4.2 + std::max(serial, feed) + (p.split > 1 ? 0.9 + 0.024 * p.nt : 0.2 + 0.004 * p.nt * waves);
+    const double stage = std::max(0.215, (kLinRows + p.nt) * (a.e2m1 ? 0.00145 : 0.00113));
+    const double serial = waves * ((p.steps + p.split - 1) / p.split) * stage;
+    const double feed = (double)tiles * p.steps * ((a.e2m1 ? 17408 : 8704) + p.nt * 132) * 0.77e-7;
+    return 3.2 + std::max(serial, feed) + (p.split > 1 ? 0.2 + 0.02 * p.nt : 0.2 + 0.004 * p.nt * waves);
 }
 
-// And of one on pairs of CTAs: 0.37 (E4M3 0.31) a stage, 3 more a tile where y is not
+// And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage, 3 more a tile where y is not
 // stored by TMA.
 double pair_cost(const LinearArgs& a, int steps)
 {
     const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, linear_pairs()));
-    return 4.5 + waves * (steps * (a.e2m1 ? 0.37 : 0.31) + (a.N % (a.out_f32 ? 4 : 8) ? 3.0 : 0.0));
+    return 4.2 + waves * (steps * (a.e2m1 ? 0.365 : 0.3) + (a.N % (a.out_f32 ? 4 : 8) ? 3.0 : 0.0));
 }
 
 // Shared and tensor memory of a plan whose tile and split are set; false if it has no room.
@@ -451,13 +453,13 @@ bool lay_out(const LinearArgs& a, Plan& p)
     const bool one = p.split > 1 || tiles_of(p) <= a.sms;       // a CTA has one tile
     p.acc = one ? 0 : p.nt;
     p.ring = std::min({kRing, (int)((kLinSmemMax - fixed) / p.stage), (512 - p.nt - p.acc) / p.sfcols, one ? std::max(slice, 3) : kRing});
-    // Where four stages fit half an SM, two CTAs share one, so that a kernel can begin beside the
-    // one before it, each with at most half of the tensor memory (one token by 4096 x 6144 6.5 us,
+    // Where four stages fit half an SM and a CTA has no more than twice its stages, two CTAs share
+    // one, so that a kernel can begin beside the one before it, each with at most half of the tensor memory (one token by 4096 x 6144 6.5 us,
     // before 6.8; their registers allow no third).  Else a CTA takes more than half of the
     // shared memory: no two CTAs of clusters may share an SM and wait for each other's tensor
     // memory.
     const int two = fixed < kLinSmemTwo ? (int)((kLinSmemTwo - fixed) / p.stage) : 0;
-    const bool share = one && two >= 4 && p.nt + std::min(p.ring, two) * p.sfcols <= 256;
+    const bool share = one && two >= 4 && slice <= 2 * two && p.nt + std::min(p.ring, two) * p.sfcols <= 256;
     if (share) p.ring = std::min(p.ring, two);
     p.loaders = std::min(kLoadWarps, p.ring);
     p.part = sizeof(Control) + p.ring * p.stage;
