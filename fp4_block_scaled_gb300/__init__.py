@@ -50,7 +50,7 @@ EXPORTS = [
 ]
 LIN_EXPORTS = [                     # of include/moe_lin.h
     "moe_lin_create", "moe_lin_status", "moe_lin_destroy", "moe_rms_norm", "moe_mx_quant", "moe_mx_values",
-    "moe_linear_packed_bytes", "moe_linear_pack", "moe_linear", "moe_lin_call",
+    "moe_linear_packed_bytes", "moe_linear_pack", "moe_linear", "moe_lin_call", "moe_lin_test_set_wait",
 ]
 
 MOE_KV_BF16 = 0
@@ -202,6 +202,7 @@ def lib() -> ctypes.CDLL:
             "moe_linear_pack": (I, [P, P, P, I, I, P, P]),
             "moe_linear": (I, [P, linp, I, P, P, I, P, I, P]),
             "moe_lin_call": (I, [I, ctypes.c_char_p]),
+            "moe_lin_test_set_wait": (I, [P, ctypes.c_ulonglong, I]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -739,3 +740,9 @@ def moe_linear(h, weights: moe_linear_desc, act_mode: int, x, T: int, y, out_dty
     except (AttributeError, struct.error):
         w = _LINEAR.pack(h or 0, d, act_mode, _p(x) or 0, _p(x_scales) or 0, T, _p(y) or 0, out_dtype, _s(stream) or 0)
     _lin_call(3, w, "moe_linear")
+
+
+def moe_lin_test_set_wait(h, wait_ns: int, withhold: bool) -> None:
+    """Test hook: bounded-wait limit of the products and the withheld report
+    that makes their waits run out (see include/moe_lin.h)."""
+    _check(lib().moe_lin_test_set_wait(h, int(wait_ns), 1 if withhold else 0), "moe_lin_test_set_wait")

@@ -16,6 +16,8 @@ struct moe_lin_s {
     int device;
     int sms;
     int* status;
+    uint32_t wait_ns;
+    int withhold;
     uint8_t* codes;             // bf16 rows quantised ahead of a product, in the same allocation
     uint8_t* scales;
 };
@@ -102,6 +104,7 @@ int moe_lin_create(moe_lin_t* out, const moe_lin_config* cfg, int device)
     if (!h) return MOE_ERR_OOM;
     h->cfg = *cfg;
     h->device = device;
+    h->wait_ns = kLinWaitNs;
     if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         linear_init_device() != cudaSuccess) {
         delete h;
@@ -273,6 +276,8 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
     a.out_f32 = out_dtype == MOE_OUT_F32;
     a.sms = h->sms;
     a.status = h->status;
+    a.wait_ns = h->wait_ns;
+    a.withhold = h->withhold;
     LinGuard guard(h->device);
     if (!x_scales) {
         if (linear_takes_bf16(T)) {
@@ -284,6 +289,14 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
         }
     }
     return cuda_rc(launch_linear(a, (cudaStream_t)stream));
+}
+
+int moe_lin_test_set_wait(moe_lin_t h, unsigned long long wait_ns, int withhold)
+{
+    if (!h || wait_ns > kLinWaitNs) return MOE_ERR_INVALID_ARG;
+    h->wait_ns = wait_ns ? (uint32_t)wait_ns : kLinWaitNs;
+    h->withhold = withhold != 0;
+    return MOE_OK;
 }
 
 int moe_lin_call(int op, const int64_t* words)

@@ -80,7 +80,10 @@ struct LinearArgs {
     int out_f32;
     int sms;
     int* status;
+    uint32_t wait_ns;           // limit of every bounded wait in the kernels
+    int withhold;               // test hook: the first CTA never reports its first stage's scales
 };
+constexpr uint32_t kLinWaitNs = 2000000000u;
 // Whether the kernel quantises bf16 rows itself; else they are quantised ahead of it.
 bool linear_takes_bf16(int T);
 cudaError_t linear_init_device();

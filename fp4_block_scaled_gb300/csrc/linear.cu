@@ -129,7 +129,8 @@ __device__ __forceinline__ void quantise_stage(const LinearArgs& a, const Plan& 
 // instructions follow one another by few cycles only if little is computed between them:
 // descriptors differ in their low words, by constants.  ATOMS: of 128 tokens' scales.
 template <int E2M1, int ATOMS>
-__device__ __forceinline__ bool multiply(const Plan& p, Control& ctl, uint8_t* ring, uint32_t tmem, int k0, int k1, int first, int tiles, int stride)
+__device__ __forceinline__ bool multiply(const LinearArgs& a, const Plan& p, Control& ctl, uint8_t* ring, uint32_t tmem, int k0, int k1, int first,
+                                         int tiles, int stride)
 {
     constexpr int kHalves = E2M1 ? 2 : 1, kUnit = kLinAtom / 16;
     const uint64_t ad0 = desc_sw128(smem_u32(ring)), bd0 = ad0 + p.b / 16, sd0 = umma_desc(smem_u32(ring) + p.sfa, 16, 128);
@@ -138,9 +139,9 @@ __device__ __forceinline__ bool multiply(const Plan& p, Control& ctl, uint8_t* r
     uint32_t slot = 0, parity = 0, it = 0;
     for (int i = first; i < tiles; i += stride, it++) {
         const uint32_t buf = it & 1, acc = tmem + buf * p.acc;
-        if (!mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, kLinWaitNs)) return false;
+        if (!mbar_wait_or_abort(&ctl.acc_empty[buf], (it >> 1 & 1) ^ 1, &ctl.abort, a.wait_ns)) return false;
         for (int k = 0; k < n; k++) {
-            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, a.wait_ns)) return false;
             tc_fence_after();
             const uint64_t ad = ad0 + slot * stage, bd = bd0 + slot * stage, sd = sd0 + slot * stage;
             const uint32_t sfa = sf0 + slot * cols, sfb = sfa + 4 * kHalves;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         pdl_wait();
                         waited = true;
                     }
-                    if (!mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, kLinWaitNs)) {
+                    if (!mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns)) {
                         give_up(a, &ctl.abort);
                         ok = false;
                         break;
@@ -246,25 +247,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // no copy may be in flight into this CTA's memory at its end
             for (uint32_t m = c > (uint32_t)p.ring ? c - p.ring : 0; m < c; m++)
-                if (!mbar_wait_or_abort(&ctl.full[m % p.ring], m / p.ring & 1, &ctl.abort, kLinWaitNs))
-                    mbar_wait_bounded(&ctl.full[m % p.ring], m / p.ring & 1, kLinWaitNs / 64);
+                if (!mbar_wait_or_abort(&ctl.full[m % p.ring], m / p.ring & 1, &ctl.abort, a.wait_ns))
+                    mbar_wait_bounded(&ctl.full[m % p.ring], m / p.ring & 1, a.wait_ns / 64);
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
+            pdl_wait();     // (no limit runs while the kernel ahead does)
             if (!QUANT) {
                 // (their bytes may be there before the weights' thread expects them: it is its
                 // arrival that the barrier's phase waits for)
-                pdl_wait();
                 for (int e = 0; e < early && first < tiles; e++)
                     tma_2d(ring + e * p.stage + p.b, &xmap, (k0 + e) * 128, first / p.rtiles * p.nt, &ctl.full[e]);
             }
-            const bool ok = p.nt > 128 ? multiply<E2M1, 2>(p, ctl, ring, tmem, k0, k1, first, tiles, stride)
-                                       : multiply<E2M1, 1>(p, ctl, ring, tmem, k0, k1, first, tiles, stride);
+            const bool ok = p.nt > 128 ? multiply<E2M1, 2>(a, p, ctl, ring, tmem, k0, k1, first, tiles, stride)
+                                       : multiply<E2M1, 1>(a, p, ctl, ring, tmem, k0, k1, first, tiles, stride);
             if (!ok) {
                 // (else the epilogue has waited for the last product)
                 give_up(a, &ctl.abort);
                 tc_commit(&ctl.drain);
-                mbar_wait_bounded(&ctl.drain, 0, kLinWaitNs);
+                mbar_wait_bounded(&ctl.drain, 0, a.wait_ns);
             }
         }
     } else if (warp >= kWarpLoad) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (; k < k1; k += p.loaders) {
                 Scales<E2M1, kMaxNt> sc;
                 if (!QUANT) sc.load(a, p.nt, t0, k, lane);
-                ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, kLinWaitNs);
+                ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (QUANT)
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.full[slot]);
+                if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);
                 slot += p.loaders;
                 if (slot >= (uint32_t)p.ring) {
                     slot -= p.ring;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = first; i < tiles; i += stride, it++) {
             const long long t0 = (long long)(i / p.rtiles) * p.nt, n = (long long)(i % p.rtiles) * kLinRows + 32 * warp + lane;
             const uint32_t buf = it & 1;
-            bool ok = mbar_wait_or_abort(&ctl.acc_full[buf], it >> 1 & 1, &ctl.abort, kLinWaitNs);
+            bool ok = mbar_wait_or_abort(&ctl.acc_full[buf], it >> 1 & 1, &ctl.abort, a.wait_ns);
             // (the warps of a split tile meet below: all of them go on, or none)
             ok = p.split > 1 ? all_of(1, 128, ok) : __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // (the producer's and the MMA's warps have no part in it)
         const int adder = warp < 4 ? warp : warp - 2, adders = 4 + kLoadWarps;
         if (here > adder && (warp < 4 || warp >= kWarpLoad)) {
-            const bool ok = mbar_wait_bounded(&ctl.red, 0, kLinWaitNs);
+            const bool ok = mbar_wait_bounded(&ctl.red, 0, a.wait_ns);
             if (!ok) give_up(a, &ctl.abort);
             const float4* part = reinterpret_cast<const float4*>(smem + p.part) + lane;
             for (int j = adder; j < here && ok; j += adders) {

@@ -9,7 +9,6 @@
 
 namespace moe {
 
-constexpr uint64_t kLinWaitNs = 2000000000ull;
 constexpr uint32_t kLinSmemMax = 227 * 1024, kLinSmemTwo = 113 * 1024;     // of a CTA, and of each of two on an SM
 
 // K-major operand of 128-byte rows in TMA's 128-byte swizzle, groups of 8 rows of 1 KB.

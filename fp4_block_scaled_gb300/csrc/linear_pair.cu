@@ -142,7 +142,7 @@ __device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap
 // The thread of the pair that issues for both CTAs.  (Little is computed between its
 // instructions, as in linear.cu.)
 template <int E2M1>
-__device__ __forceinline__ bool multiply(Control& ctl, uint8_t* ring, uint32_t tmem, int steps, int first, int tiles, int stride)
+__device__ __forceinline__ bool multiply(const LinearArgs& a, Control& ctl, uint8_t* ring, uint32_t tmem, int steps, int first, int tiles, int stride)
 {
     using S = Stage<E2M1>;
     constexpr uint32_t kUnit = kLinAtom / 16;
@@ -154,8 +154,8 @@ __device__ __forceinline__ bool multiply(Control& ctl, uint8_t* ring, uint32_t t
     for (int i = first; i < tiles; i += stride, it++) {
         const uint32_t acc = tmem + (it & 1) * (kFeatures - kShared);
         for (int k = 0; k < steps; k++) {
-            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
-            if (!mbar_wait_or_abort(&ctl.empty[before], before_parity, &ctl.abort, kLinWaitNs)) return false;
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, a.wait_ns)) return false;
+            if (!mbar_wait_or_abort(&ctl.empty[before], before_parity, &ctl.abort, a.wait_ns)) return false;
             tc_fence_after();
             const uint64_t ad = ad0 + slot * (S::bytes / 16), sd = sd0 + slot * (S::bytes / 16);
             const uint32_t sfa = sf0 + cols, sfb = sfa + 4 * S::kAtoms;
@@ -164,7 +164,7 @@ __device__ __forceinline__ bool multiply(Control& ctl, uint8_t* ring, uint32_t t
 #pragma unroll
             for (int h = 0; h < 2 * S::kAtoms; h++) cp_scales(sfb + 4 * h, sd + (S::kAtoms + h) * kUnit);
             // the tile before has left the shared columns (and with them the one before it everything)
-            if (k == 0 && it > 0 && !mbar_wait_or_abort(&ctl.acc_empty, (it - 1) & 1, &ctl.abort, kLinWaitNs)) return false;
+            if (k == 0 && it > 0 && !mbar_wait_or_abort(&ctl.acc_empty, (it - 1) & 1, &ctl.abort, a.wait_ns)) return false;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -189,12 +189,12 @@ __device__ __forceinline__ bool multiply(Control& ctl, uint8_t* ring, uint32_t t
 
 // The other CTA's: tells the first that its half of a stage is there.
 template <int E2M1>
-__device__ __forceinline__ bool relay(Control& ctl, int steps, int first, int tiles, int stride)
+__device__ __forceinline__ bool relay(const LinearArgs& a, Control& ctl, int steps, int first, int tiles, int stride)
 {
     uint32_t slot = 0, parity = 0;
     for (int i = first; i < tiles; i += stride)
         for (int k = 0; k < steps; k++) {
-            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, kLinWaitNs)) return false;
+            if (!mbar_wait_or_abort(&ctl.full[slot], parity, &ctl.abort, a.wait_ns)) return false;
             arrive_at(&ctl.full[slot], 0);
             if (++slot == (uint32_t)kRing) {
                 slot = 0;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         pdl_wait();
                         waited = true;
                     }
-                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, kLinWaitNs)) {
+                    if (!mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, a.wait_ns)) {
                         give_up(a, &ctl.abort);
                         ok = false;
                         break;
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 waited = true;
             }
             for (uint32_t m = c > (uint32_t)kRing ? c - kRing : 0; m < c; m++)
-                if (!mbar_wait_or_abort(&ctl.full[m % kRing], m / kRing & 1, &ctl.abort, kLinWaitNs))
-                    mbar_wait_bounded(&ctl.full[m % kRing], m / kRing & 1, kLinWaitNs / 64);
+                if (!mbar_wait_or_abort(&ctl.full[m % kRing], m / kRing & 1, &ctl.abort, a.wait_ns))
+                    mbar_wait_bounded(&ctl.full[m % kRing], m / kRing & 1, a.wait_ns / 64);
         }
     } else if (warp == kWarpMma) {
         if (elect_one()) {
@@ -295,13 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             pdl_wait();
             for (int e = 0; e < early && first < tiles; e++)
                 tma_2d(ring + e * S::bytes, &xmap, e * 128, first / ftiles * kTokens + (int)rank * 128, &ctl.full[e]);
-            const bool ok = rank == 0 ? multiply<E2M1>(ctl, ring, tmem, steps, first, tiles, stride)
-                                      : relay<E2M1>(ctl, steps, first, tiles, stride);
+            const bool ok = rank == 0 ? multiply<E2M1>(a, ctl, ring, tmem, steps, first, tiles, stride)
+                                      : relay<E2M1>(a, ctl, steps, first, tiles, stride);
             if (!ok) {
                 give_up(a, &ctl.abort);
                 if (rank == 0) {
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl.drain)) : "memory");
-                    mbar_wait_bounded(&ctl.drain, 0, kLinWaitNs);
+                    mbar_wait_bounded(&ctl.drain, 0, a.wait_ns);
                 }
             }
         }
@@ -315,13 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t slot = c % kRing;
                 Scales<E2M1, 128> sc;
                 sc.load(a, 128, t0, k, lane);
-                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, kLinWaitNs);
+                ok = mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 sc.store(128, ring + slot * S::bytes + S::sfa, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.full[slot]);
+                if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);
             }
         }
         if (!ok && lane == 0) give_up(a, &ctl.abort);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = first; i < tiles; i += stride, it++) {
             const int n0 = i % ftiles * kFeatures;
             const int t = i / ftiles * kTokens + (int)rank * 128 + 32 * warp;
-            bool ok = mbar_wait_or_abort(&ctl.acc_full, it & 1, &ctl.abort, kLinWaitNs);
+            bool ok = mbar_wait_or_abort(&ctl.acc_full, it & 1, &ctl.abort, a.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
                 if (lane == 0) give_up(a, &ctl.abort);

@@ -113,6 +113,14 @@ typedef struct {
 int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* x, const uint8_t* x_scales, int T,
                void* y, int out_dtype, void* stream);
 
+/* Test hook, as moe_ffn_test_set_wait: later products on h give up every
+ * bounded device-side wait after wait_ns nanoseconds (at 2 GHz SM clock; at
+ * most the default, 2 s, which 0 restores), and with withhold != 0 the first CTA
+ * never reports the first scales it has loaded, so that its waits run out: the
+ * call completes, y is incomplete, and moe_lin_status returns
+ * MOE_ERR_DEVICE_TIMEOUT.  Errors: INVALID_ARG. */
+int moe_lin_test_set_wait(moe_lin_t h, unsigned long long wait_ns, int withhold);
+
 /* Calls above with their arguments as one array of 64-bit words, in their
  * order: the same call, for language bindings that pay for every argument.
  * INVALID_ARG: an unknown op, no array, an integer outside its type. */

@@ -1,6 +1,8 @@
 """The norms' and projections' calls on streams and in graphs: first calls
 captured, a packed layer's first product, handles at work at once, a handle made
 beside a busy default stream, weights that change between calls."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -178,3 +180,33 @@ def test_a_new_handle_works_at_once_on_a_stream_beside_a_busy_default_one():
                 assert moe.moe_lin_status(h, st) == moe.MOE_OK
             moe.moe_lin_destroy(h)
             a.check()
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 6144), (16, 2048, 256), (100, 512, 30000), (150, 4096, 1024), (5000, 1056, 520)])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_waits_that_run_out_end_the_call(fmt, T, K, N):
+    """A report that never comes: every wait that follows from it gives up, the call ends at once, says so, and the next
+    one is right.  (One tile cut along K, two, tiles taken in turn, and pairs of CTAs.)"""
+    rng = np.random.default_rng(6)
+    with handle(T, K) as h:
+        w = Weights(h, N, K, rng)
+        x = rand(rng, (T, K)).to(torch.bfloat16)
+        q, s = code_buffers(T, K, fmt)
+        moe.moe_mx_quant(h, x, T, K, MODE[fmt], q, s)
+        y, want = (torch.zeros((T, N), dtype=torch.float32, device="cuda") for _ in range(2))
+        call = lambda out, **kw: moe.moe_linear(h, w.desc, MODE[fmt], kw.get("x", q), T, out, TYPE["f32"], x_scales=kw.get("s", s))  # noqa: E731
+        call(want)
+        assert moe.moe_lin_status(h) == moe.MOE_OK
+        for kw in ({}, dict(x=x, s=None)):
+            moe.moe_lin_test_set_wait(h, 1000000, True)
+            t = time.perf_counter()
+            call(y, **kw)
+            assert moe.moe_lin_status(h) == moe.MOE_ERR_DEVICE_TIMEOUT
+            assert time.perf_counter() - t < 1.0
+            moe.moe_lin_test_set_wait(h, 0, False)
+            for _ in range(2):
+                y.fill_(float("nan"))
+                call(y, **kw)
+                assert moe.moe_lin_status(h) == moe.MOE_OK and torch.equal(y, want)
+        with pytest.raises(moe.MoeError):
+            moe.moe_lin_test_set_wait(h, 2000000001, False)
