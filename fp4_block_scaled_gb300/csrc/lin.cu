@@ -280,7 +280,7 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
     a.withhold = h->withhold;
     LinGuard guard(h->device);
     if (!x_scales) {
-        if (linear_takes_bf16(T)) {
+        if (linear_takes_bf16(a)) {
             a.codes = a.scales = nullptr;
             a.x = (const uint16_t*)x;
         } else {

@@ -85,7 +85,7 @@ struct LinearArgs {
 };
 constexpr uint32_t kLinWaitNs = 2000000000u;
 // Whether the kernel quantises bf16 rows itself; else they are quantised ahead of it.
-bool linear_takes_bf16(int T);
+bool linear_takes_bf16(const LinearArgs& a);
 cudaError_t linear_init_device();
 // Many tokens on pairs of CTAs (linear_pair.cu), and how many pairs run at once.
 int linear_pairs();

@@ -88,41 +88,82 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
             : "memory");
 }
 
-// A stage's token rows quantised from bf16 into the swizzled operand and the atoms, by one
-// warp: 256 elements a turn, a row of E2M1 or two rows of E4M3.
+// Up to 16 token rows quantised from bf16 into the swizzled operand and the atoms, by eight
+// warps: a turn is 256 elements of a stage, a row of E2M1 or two rows of E4M3, and a warp has
+// one or two turns of every stage, or with few rows, of every second or fourth.
+constexpr int kQuantRows = 16;
+struct QuantShare {
+    int rows, turns, stages;    // warps that share a stage's rows, turns of each, stages from one of its own to the next
+    __host__ __device__ QuantShare(bool e2m1, int T, int ring)
+    {
+        const int all = e2m1 ? T : (T + 1) / 2;
+        rows = all < kLoadWarps ? all : kLoadWarps;
+        turns = (all + kLoadWarps - 1) / kLoadWarps;
+        // (no more than the ring has, as for the scales' warps)
+        stages = rows <= 2 && ring >= 4 ? 4 : rows <= 4 ? 2 : 1;
+    }
+};
+
 template <int E2M1>
-__device__ __forceinline__ void quantise_stage(const LinearArgs& a, const Plan& p, uint8_t* st, int t0, int step, int lane)
+__device__ __forceinline__ bool quantise_rows(const LinearArgs& a, const Plan& p, Control& ctl, uint8_t* ring, int k0, int k1, int first, int tiles,
+                                              int stride, int warp, int lane)
 {
-    constexpr int kRows = E2M1 ? 1 : 2, kBatch = 4;
-    const int rows = min(p.nt, a.T - t0), l = E2M1 ? lane : lane % 16, k = step * (E2M1 ? 256 : 128) + 8 * l;
-    for (int r0 = 0; r0 < rows; r0 += kRows * kBatch) {
-        uint4 u[kBatch];
+    constexpr int kBatch = 4;           // turns whose rows are loaded ahead
+    const QuantShare share(E2M1, a.T, p.ring);
+    const int w = warp % share.rows, turns = share.turns, l = E2M1 ? lane : lane % 16;
+    if (warp >= share.rows * share.stages) return true;
+    uint32_t slot = warp / share.rows, parity = 1;
+    int from = k0 + (int)slot;
+    for (int i = first; i < tiles; i += stride) {
+        const int n = (k1 - from + share.stages - 1) / share.stages * turns;     // (0 or less: none)
+        for (int u0 = 0; u0 < n; u0 += kBatch) {
+            uint4 x[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            const int r = r0 + i * kRows + (E2M1 ? 0 : lane / 16);
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows && k < a.K) u[i] = *reinterpret_cast<const uint4*>(a.x + (size_t)(t0 + r) * a.K + k);
-        }
+            for (int b = 0; b < kBatch; b++) {
+                const int u = u0 + b, r = E2M1 ? w + (turns == 2 ? u & 1 : 0) * kLoadWarps : 2 * w + lane / 16;
+                const int k = (from + (turns == 2 ? u >> 1 : u) * share.stages) * (E2M1 ? 256 : 128) + 8 * l;
+                x[b] = make_uint4(0, 0, 0, 0);
+                if (u < n && r < a.T && k < a.K) x[b] = *reinterpret_cast<const uint4*>(a.x + (size_t)r * a.K + k);
+            }
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            if (r0 + i * kRows >= rows) break;
-            const int r = r0 + i * kRows + (E2M1 ? 0 : lane / 16);
-            uint8_t* row = st + p.b + r * 128;
-            uint8_t* atom = st + p.sfb + r % 32 * 16 + r / 32 * 4;
-            int s;
-            if (E2M1) {
-                const uint32_t c = e2m1_quantise(u[i], s);
-                *reinterpret_cast<uint32_t*>(row + ((l / 4 ^ (r & 7)) << 4) + l % 4 * 4) = c;
-                if (l % 4 == 0) atom[l / 16 * kLinAtom + l / 4 % 4] = (uint8_t)s;
-            } else {
-                const uint2 c = e4m3_quantise(u[i], s);
-                if (r < rows) {
-                    *reinterpret_cast<uint2*>(row + ((l / 2 ^ (r & 7)) << 4) + l % 2 * 8) = c;
-                    if (l == 0) *reinterpret_cast<uint32_t*>(atom) = (uint32_t)s * 0x01010101u;
+            for (int b = 0; b < kBatch; b++) {
+                const int u = u0 + b, half = turns == 2 ? u & 1 : 0, r = E2M1 ? w + half * kLoadWarps : 2 * w + lane / 16;
+                if (u >= n) break;
+                if (half == 0) {
+                    const bool ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+                }
+                uint8_t* st = ring + slot * p.stage;
+                uint8_t* row = st + p.b + r * 128;
+                uint8_t* atom = st + p.sfb + r * 16;
+                int s;
+                if (E2M1) {
+                    const uint32_t c = e2m1_quantise(x[b], s);
+                    if (r < a.T) {
+                        *reinterpret_cast<uint32_t*>(row + ((l / 4 ^ (r & 7)) << 4) + l % 4 * 4) = c;
+                        if (l % 4 == 0) atom[l / 16 * kLinAtom + l / 4 % 4] = (uint8_t)s;
+                    }
+                } else {
+                    const uint2 c = e4m3_quantise(x[b], s);
+                    if (r < a.T) {
+                        *reinterpret_cast<uint2*>(row + ((l / 2 ^ (r & 7)) << 4) + l % 2 * 8) = c;
+                        if (l == 0) *reinterpret_cast<uint32_t*>(atom) = (uint32_t)s * 0x01010101u;
+                    }
+                }
+                if (half != turns - 1) continue;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0 && !(a.withhold && blockIdx.x == 0 && from == 0 && u < turns)) mbar_arrive(&ctl.full[slot]);
+                slot += share.stages;
+                if (slot >= (uint32_t)p.ring) {
+                    slot -= p.ring;
+                    parity ^= 1;
                 }
             }
         }
+        from += (n > 0 ? n / turns : 0) * share.stages - (k1 - k0);
     }
+    return true;
 }
 
 // The MMA's thread: per stage the scales to tensor memory and four products.  Its
@@ -175,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t* ring = smem + sizeof(Control);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x < kRing) {
-        mbar_init(&ctl.full[threadIdx.x], 2);
+        mbar_init(&ctl.full[threadIdx.x], 1 + (QUANT ? QuantShare(E2M1, a.T, p.ring).rows : 1));
         mbar_init(&ctl.empty[threadIdx.x], 1);
         mbar_fence_init();
     } else if (threadIdx.x == 32) {
@@ -271,21 +312,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp >= kWarpLoad) {
         pdl_wait();
         // every loaders-th stage
-        bool ok = warp - kWarpLoad < p.loaders;
+        bool ok = !QUANT && warp - kWarpLoad < p.loaders;
         uint32_t slot = warp - kWarpLoad, parity = 1;
         int k = k0 + warp - kWarpLoad;
         for (int i = first; i < tiles && ok; i += stride, k -= k1 - k0) {
             const int t0 = i / p.rtiles * p.nt;
             for (; k < k1; k += p.loaders) {
                 Scales<E2M1, kMaxNt> sc;
-                if (!QUANT) sc.load(a, p.nt, t0, k, lane);
+                sc.load(a, p.nt, t0, k, lane);
                 ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                if (QUANT)
-                    quantise_stage<E2M1>(a, p, ring + slot * p.stage, t0, k, lane);
-                else
-                    sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
+                sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);
@@ -296,7 +334,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
-        ok = ok || warp - kWarpLoad >= p.loaders;
+        ok = ok || QUANT || warp - kWarpLoad >= p.loaders;
+        if (QUANT)
+            ok = quantise_rows<E2M1>(a, p, ctl, ring, k0, k1, first, tiles, stride, warp - kWarpLoad, lane);
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
         pdl_wait();
@@ -518,7 +558,18 @@ cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, con
 const void* const kKernels[4] = {(const void*)k_linear<0, 0>, (const void*)k_linear<1, 0>, (const void*)k_linear<0, 1>,
                                  (const void*)k_linear<1, 1>};
 
-bool linear_takes_bf16(int T) { return T <= 4; }
+bool linear_takes_bf16(const LinearArgs& a0)
+{
+    // Every CTA quantises its slice of K, so that a kernel ahead, at 1.3 us and a launch, is saved
+    // where a warp has few turns (16 rows, two stages a CTA 4.2 us, before 5.0; eight rows, six
+    // stages 6.4, before 6.2; 16 rows in E2M1, six stages 8.4, before 6.5).
+    if (a0.T > kQuantRows) return false;
+    LinearArgs a = a0;
+    a.codes = nullptr;
+    const Plan p = make_plan(a);
+    const QuantShare q(a.e2m1, a.T, p.ring);
+    return (p.steps + p.split - 1) / p.split * q.turns <= 6 * q.stages;
+}
 
 cudaError_t linear_init_device()
 {

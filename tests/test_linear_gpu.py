@@ -76,6 +76,18 @@ def test_token_counts_around_the_tiles(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("K,N", [(96, 40), (512, 200), (1440, 384), (4096, 1024), (2048, 30000)])
+def test_few_bf16_rows_are_quantised_alike(fmt, K, N):
+    """In the product's kernel or ahead of it: the codes' product bit for bit, whichever sizes take which."""
+    rng = np.random.default_rng([K, N])
+    with handle(20, K) as h:
+        w = Weights(h, N, K, rng)
+        x, q, s = rows(h, 20, K, fmt, rng)
+        for T in (1, 2, 3, 4, 5, 7, 8, 9, 13, 15, 16, 17, 20):
+            assert torch.equal(product(h, w, fmt, x, T), product(h, w, fmt, q, T, scales=s)), T
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_repeats_are_equal_bit_for_bit(fmt):
     rng = np.random.default_rng(6)
     with handle() as h:
