@@ -88,6 +88,35 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
             : "memory");
 }
 
+// The tokens' scales into the atoms of every loaders-th stage, by one warp.
+template <int E2M1>
+__device__ __forceinline__ bool gather_scales(const LinearArgs& a, const Plan& p, Control& ctl, uint8_t* ring, int k0, int k1, int first, int tiles,
+                                              int stride, int warp, int lane)
+{
+    if (warp >= p.loaders) return true;
+    uint32_t slot = warp, parity = 1;
+    int k = k0 + warp;
+    for (int i = first; i < tiles; i += stride, k -= k1 - k0) {
+        const int t0 = i / p.rtiles * p.nt;
+        for (; k < k1; k += p.loaders) {
+            Scales<E2M1, kMaxNt> sc;
+            sc.load(a, p.nt, t0, k, lane);
+            const bool ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+            sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);
+            slot += p.loaders;
+            if (slot >= (uint32_t)p.ring) {
+                slot -= p.ring;
+                parity ^= 1;
+            }
+        }
+    }
+    return true;
+}
+
 // Up to 16 token rows quantised from bf16 into the swizzled operand and the atoms, by eight
 // warps: a turn is 256 elements of a stage, a row of E2M1 or two rows of E4M3, and a warp has
 // one or two turns of every stage, or with few rows, of every second or fourth.
@@ -311,32 +340,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp >= kWarpLoad) {
         pdl_wait();
-        // every loaders-th stage
-        bool ok = !QUANT && warp - kWarpLoad < p.loaders;
-        uint32_t slot = warp - kWarpLoad, parity = 1;
-        int k = k0 + warp - kWarpLoad;
-        for (int i = first; i < tiles && ok; i += stride, k -= k1 - k0) {
-            const int t0 = i / p.rtiles * p.nt;
-            for (; k < k1; k += p.loaders) {
-                Scales<E2M1, kMaxNt> sc;
-                sc.load(a, p.nt, t0, k, lane);
-                ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);
-                slot += p.loaders;
-                if (slot >= (uint32_t)p.ring) {
-                    slot -= p.ring;
-                    parity ^= 1;
-                }
-            }
-        }
-        ok = ok || QUANT || warp - kWarpLoad >= p.loaders;
-        if (QUANT)
-            ok = quantise_rows<E2M1>(a, p, ctl, ring, k0, k1, first, tiles, stride, warp - kWarpLoad, lane);
+        const bool ok = QUANT ? quantise_rows<E2M1>(a, p, ctl, ring, k0, k1, first, tiles, stride, warp - kWarpLoad, lane)
+                              : gather_scales<E2M1>(a, p, ctl, ring, k0, k1, first, tiles, stride, warp - kWarpLoad, lane);
         if (!ok && lane == 0) give_up(a, &ctl.abort);
     } else {
         pdl_wait();
