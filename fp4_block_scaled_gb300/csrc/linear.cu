@@ -475,12 +475,12 @@ double tile_cost(const LinearArgs& a, const Plan& p)
     return 3.2 + std::max(serial, feed) + (p.split > 1 ? 0.2 + 0.02 * p.nt : 0.2 + 0.004 * p.nt * waves);
 }
 
-// And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage, 3 more a tile where y is not
-// stored by TMA.
+// And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage, 2.2 (f32 3) more a tile where y is
+// not stored by TMA.
 double pair_cost(const LinearArgs& a, int steps)
 {
     const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, linear_pairs()));
-    return 4.2 + waves * (steps * (a.e2m1 ? 0.365 : 0.3) + (a.N % (a.out_f32 ? 4 : 8) ? 3.0 : 0.0));
+    return 4.2 + waves * (steps * (a.e2m1 ? 0.365 : 0.3) + (a.N % (a.out_f32 ? 4 : 8) ? (a.out_f32 ? 3.0 : 2.2) : 0.0));
 }
 
 // Shared and tensor memory of a plan whose tile and split are set; false if it has no room.

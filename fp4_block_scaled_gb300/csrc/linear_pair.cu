@@ -9,7 +9,7 @@
 // stay and take tiles in turn; the epilogue of one overlaps the products of the next, for
 // which two accumulators of 256 columns would leave no tensor memory to the scales: they
 // share 48 columns.  Outputs leave through shared memory by TMA stores of whole lines (32-byte
-// stores of single rows cost 12 % of the time, odd rows by single values 6 times that).
+// stores of single rows cost 12 % of the time).
 //
 // Bounds (GB300): 16384 tokens by 4096 x 6144 in E2M1 take 119 us from codes, 6.9 PFLOP/s, 92 %
 // of four times the measured bf16 rate (the K = 64 steps' nominal ratio); 8191 by 4096 x 5760 in
@@ -20,6 +20,7 @@
 // one barrier a stage, the scales of a tile's first stage copied while the tile before is
 // emptied.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear.cuh"
 
@@ -106,11 +107,8 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, 
 }
 
 // 32 tokens (a lane each) by 128 bytes of features from n, by one warp: through its 4 KB of
-// shared memory, in TMA's swizzle, to whole lines of y.  Where y's rows do not begin on 16
-// bytes, which TMA needs, a row after the other by plain stores.
-template <int F32>
-__device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap* ymap, bool tma, uint8_t* out, int t, int n, int lane,
-                                          const uint32_t (&w)[32])
+// shared memory, in TMA's swizzle, to whole lines of y.
+__device__ __forceinline__ void stage_box(uint8_t* out, int lane, const uint32_t (&w)[32])
 {
     // (the box before has left)
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -118,25 +116,70 @@ __device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap
 #pragma unroll
     for (int j = 0; j < 8; j++)
         *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    if (tma) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) tma_store(ymap, n, t, out);
-        return;
+}
+
+// Where y's rows do not begin on 16 bytes, which TMA needs, plain stores of the 16 bytes
+// that are aligned: each row is turned round by its s elements behind such a boundary, so that
+// seven of its eight pieces lie as they do in y, and the eighth holds its first and last
+// elements, which go singly: 9389 tokens by 576 x 2541 take 31.5 us in bf16 and 42.9 in f32, where
+// TMA's by 2544 take 19.2 and 27.1 (a row's words after the other 100 cycles a row: 61.4 and 58.8).
+template <int F32>
+__device__ __forceinline__ void store_rows(const LinearArgs& a, uint8_t* out, int t, int n, int lane, const uint32_t (&box)[32])
+{
+    using Value = std::conditional_t<F32, uint32_t, uint16_t>;
+    constexpr int kPiece = 16 / sizeof(Value), kRow = 128 / sizeof(Value);
+    uint32_t w[32];
+    const int s = (int)((uint32_t)(t + lane) * (uint32_t)a.N) & (kPiece - 1), words = F32 ? s : s >> 1;
+#pragma unroll
+    for (int j = 0; j < 32; j++) w[j] = F32 ? box[j] : __funnelshift_l(box[(j + 31) & 31], box[j], s % 2 * 16);
+#pragma unroll
+    for (int by = 1; by <= 2; by *= 2) {
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) v[j] = words & by ? w[(j + 32 - by) & 31] : w[j];
+#pragma unroll
+        for (int j = 0; j < 32; j++) w[j] = v[j];
     }
+    stage_box(out, lane, w);
     __syncwarp();
-    constexpr int kEach = F32 ? 1 : 2;
-    const int c = n + kEach * lane;
-    for (int r = 0; r < 32 && t + r < a.T; r++) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(out + r * 128 + ((lane / 4 ^ (r & 7)) << 4) + lane % 4 * 4);
-        const size_t i = (size_t)(t + r) * a.N + c;
-        if (F32) {
-            if (c < a.N) ((uint32_t*)a.y)[i] = v;
+    const int have = min(kRow, a.N - n);
+#pragma unroll
+    for (int b = 0; b < 8; b++) {
+        const int r = 4 * b + lane / 8, c = lane % 8, sr = (int)((uint32_t)(t + r) * (uint32_t)a.N) & (kPiece - 1);
+        const int first = kPiece * c - sr;      // of the box's features
+        if (t + r >= a.T || first < 0 || first >= have) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(out + r * 128 + ((c ^ (r & 7)) << 4));
+        Value* y = (Value*)a.y + (size_t)(t + r) * a.N + n + first;
+        if (first + kPiece <= have) {
+            *reinterpret_cast<uint4*>(y) = v;
         } else {
-            if (c < a.N) ((uint16_t*)a.y)[i] = (uint16_t)v;
-            if (c + 1 < a.N) ((uint16_t*)a.y)[i + 1] = (uint16_t)(v >> 16);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < kPiece; k++)
+                if (first + k < have) y[k] = (Value)(F32 ? u[k % 4] : u[k / 2 % 4] >> k % 2 * 16);
         }
     }
+#pragma unroll
+    for (int b = 0; b < kPiece; b++) {
+        const int r = 32 / kPiece * b + lane / kPiece, e = lane % kPiece, sr = (int)((uint32_t)(t + r) * (uint32_t)a.N) & (kPiece - 1);
+        const int at = e < sr ? kRow + e - sr : e - sr;
+        if (t + r >= a.T || sr == 0 || at >= have) continue;
+        ((Value*)a.y)[(size_t)(t + r) * a.N + n + at] = *reinterpret_cast<const Value*>(out + r * 128 + ((r & 7) << 4) + e * sizeof(Value));
+    }
+}
+
+template <int F32>
+__device__ __forceinline__ void store_box(const LinearArgs& a, const CUtensorMap* ymap, bool tma, uint8_t* out, int t, int n, int lane,
+                                          const uint32_t (&w)[32])
+{
+    if (!tma) {
+        store_rows<F32>(a, out, t, n, lane, w);
+        return;
+    }
+    stage_box(out, lane, w);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) tma_store(ymap, n, t, out);
 }
 
 // The thread of the pair that issues for both CTAs.  (Little is computed between its

@@ -88,6 +88,25 @@ def test_few_bf16_rows_are_quantised_alike(fmt, K, N):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("T", [300, 4229])
+def test_outputs_of_any_row_length(fmt, T):
+    """Rows of y that begin on any element: of each feature the same sums."""
+    rng = np.random.default_rng(21)
+    K, N = 160, 584
+    with handle(20, K) as h:
+        w = Weights(h, N, K, rng)
+        _, q, s = rows(h, T, K, fmt, rng)
+        whole = product(h, w, fmt, q, T, scales=s)
+        check(whole, q, s, w, fmt)
+        for n in (1, 3, 6, 31, 34, 66, 253, 255, 257, 260, 322, 513, 577, 578, 579, 580, 581, 582, 583):
+            part = Weights(h, n, K, rng)
+            part.codes, part.scales = w.codes[:n].copy(), w.scales[:n].copy()
+            part.pack(h)
+            for out in ("f32", "bf16"):
+                assert torch.equal(product(h, part, fmt, q, T, out, scales=s), whole[:, :n].to(TORCH[out])), (n, out)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_repeats_are_equal_bit_for_bit(fmt):
     rng = np.random.default_rng(6)
     with handle() as h:
