@@ -103,7 +103,7 @@ __device__ __forceinline__ bool gather_scales(const LinearArgs& a, const Plan& p
             sc.load(a, p.nt, t0, k, lane);
             const bool ok = mbar_wait_or_abort(&ctl.empty[slot], parity, &ctl.abort, a.wait_ns);
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-            sc.store(p.nt, ring + slot * p.stage + p.sfb, lane);
+            sc.store(a, p.nt, t0, k, ring + slot * p.stage + p.sfb, lane);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);

@@ -141,27 +141,23 @@ __device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]
         : "r"(taddr));
 }
 
-// Four scale bytes of a row from `at`, 0 behind its end.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int at, int n)
-{
-    if (n % 4 == 0) return at < n ? *reinterpret_cast<const uint32_t*>(row + at) : 0u;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (at + i < n) w |= (uint32_t)row[at + i] << (8 * i);
-    return w;
-}
-
 // The scales of a stage's token rows, by one warp: lane l holds those of the rows l, l +
-// 32, ..., one word for each 128 elements (E4M3: the row's byte four times).
+// 32, ...  E2M1: eight bytes, and where a row's number is no multiple of four, so that they begin
+// anywhere, the three aligned words around them, all on their way at once (byte after byte, 9000
+// tokens by 4832 x 4096 took 112.6 us, so 80.0; 4864 is 75.0.  A path for both kinds
+// cost the aligned ones 3 %).  E4M3: the row's byte.
 template <int E2M1, int ROWS>
 struct Scales {
-    uint32_t w[ROWS / 32][E2M1 ? 2 : 1];
+    uint32_t w[ROWS / 32][E2M1 ? 3 : 1];
 
     // rows of the tile from t0, `rows` of them
     __device__ __forceinline__ void load(const LinearArgs& a, int rows, int t0, int step, int lane)
     {
         const int n = E2M1 ? a.K / 32 : (a.K + 127) / 128;
+        if (E2M1 && n % 4) {
+            load_anywhere(a, rows, t0, step, lane, n);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < ROWS / 32; i++) {
             if (32 * i >= rows) break;
@@ -169,17 +165,56 @@ struct Scales {
             const bool in = r < rows && t0 + r < a.T;
             const uint8_t* row = a.scales + (size_t)(t0 + r) * n;
             if (E2M1) {
-                w[i][0] = in ? scale_word(row, 8 * step, n) : 0u;
-                w[i][E2M1] = in ? scale_word(row, 8 * step + 4, n) : 0u;
+                w[i][0] = in ? *reinterpret_cast<const uint32_t*>(row + 8 * step) : 0u;
+                w[i][E2M1] = in && 8 * step + 4 < n ? *reinterpret_cast<const uint32_t*>(row + 8 * step + 4) : 0u;
             } else {
                 w[i][0] = in ? row[step] : 0u;
             }
         }
     }
 
-    __device__ __forceinline__ void store(int rows, uint8_t* atoms, int lane) const
+    // (words that hold a byte of the array, and of the last no byte behind it)
+    __device__ __forceinline__ void load_anywhere(const LinearArgs& a, int rows, int t0, int step, int lane, int n)
     {
-        const int per = rows > 128 ? 2 : 1;
+        const size_t size = (size_t)a.T * n;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; i++) {
+            if (32 * i >= rows) break;
+            const int r = lane + 32 * i;
+            const size_t from = ((size_t)(t0 + r) * n & ~(size_t)3) + 8 * step;
+            const int left = r < rows && t0 + r < a.T ? (int)min(size - from, (size_t)12) : 0;      // bytes of the array
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(a.scales + from);
+            w[i][0] = left >= 4 ? p[0] : 0u;
+            w[i][E2M1] = left >= 8 ? p[1] : 0u;
+            w[i][2 * E2M1] = left >= 12 ? p[2] : 0u;
+            if (left % 4) {
+                // the array's last word is not whole
+                uint32_t v = 0;
+                for (int b = 0; b < left % 4; b++) v |= (uint32_t)a.scales[size - left % 4 + b] << 8 * b;
+                w[i][0] = left < 4 ? v : w[i][0];
+                w[i][E2M1] = left / 4 == 1 ? v : w[i][E2M1];
+                w[i][2 * E2M1] = left / 4 == 2 ? v : w[i][2 * E2M1];
+            }
+        }
+    }
+
+    // (of the same rows and step)
+    __device__ __forceinline__ void store(const LinearArgs& a, int rows, int t0, int step, uint8_t* atoms, int lane) const
+    {
+        const int per = rows > 128 ? 2 : 1, n = a.K / 32;
+        if (E2M1 && n % 4) {
+            const int have = n - 8 * step;
+            const uint32_t lo = have < 4 ? ~(~0u << 8 * have) : ~0u, hi = have <= 4 ? 0u : have < 8 ? ~(~0u << 8 * (have - 4)) : ~0u;
+#pragma unroll
+            for (int i = 0; i < ROWS / 32; i++) {
+                if (32 * i >= rows) break;
+                uint8_t* at = atoms + (i / 4) * kLinAtom + lane * 16 + i % 4 * 4;
+                const uint32_t by = (uint32_t)(t0 + lane + 32 * i) * (uint32_t)n % 4 * 8;
+                *reinterpret_cast<uint32_t*>(at) = __funnelshift_r(w[i][0], w[i][E2M1], by) & lo;
+                *reinterpret_cast<uint32_t*>(at + per * kLinAtom) = __funnelshift_r(w[i][E2M1], w[i][2 * E2M1], by) & hi;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < ROWS / 32; i++) {
             if (32 * i >= rows) break;

@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 ok = mbar_wait_or_abort(&ctl.empty[slot], (c / kRing & 1) ^ 1, &ctl.abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                sc.store(128, ring + slot * S::bytes + S::sfa, lane);
+                sc.store(a, 128, t0, k, ring + slot * S::bytes + S::sfa, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0 && !(a.withhold && blockIdx.x == 0 && k == 0)) mbar_arrive(&ctl.full[slot]);

@@ -106,6 +106,28 @@ def test_outputs_of_any_row_length(fmt, T):
                 assert torch.equal(product(h, part, fmt, q, T, out, scales=s), whole[:, :n].to(TORCH[out])), (n, out)
 
 
+@pytest.mark.parametrize("T", [1, 2, 5, 20, 300, 4229])
+def test_rows_of_scales_of_any_length(T):
+    """Rows of scales that begin on any byte: each keeps its own, up to the array's last."""
+    rng = np.random.default_rng(22)
+    N = 40
+    with handle(20) as h:
+        for K in (32, 64, 96, 128, 160, 224, 288, 480, 736, 1056):
+            w = Weights(h, N, K, rng)
+            q = torch.from_numpy(rng.integers(0, 256, (T, K // 2), dtype=np.uint8)).cuda()
+            room = torch.full((T * (K // 32) + 64,), 255, dtype=torch.uint8, device="cuda")
+            s = room[:T * (K // 32)].view(T, K // 32)
+            s.copy_(torch.from_numpy(rng.integers(117, 124, (T, K // 32), dtype=np.uint8)))
+            check(product(h, w, "e2m1", q, T, scales=s), q, s, w, "e2m1")
+            # a scale of NaN at each end of every third row
+            s[1::3, 0] = 255
+            s[2::3, -1] = 255
+            bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+            bad[1::3], bad[2::3] = True, True
+            y = product(h, w, "e2m1", q, T, scales=s)
+            assert torch.equal(torch.isnan(y), bad[:, None].expand(T, N)), K
+
+
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_repeats_are_equal_bit_for_bit(fmt):
     rng = np.random.default_rng(6)
