@@ -7,8 +7,8 @@
 // that the threads of a row exchange (shuffles, and one barrier where a CTA holds the row).
 // Bound by HBM: 16384 rows of 4096, bf16 with a bf16 residual, to bf16 and E4M3, 91 us (98 % of
 // the copy rate); 16384 of 4096 without a residual 43 us (92 %); 4099 of 2880 14.6 us (84 %: 1.7
-// rounds of rows); a million of 128 93 us (81 %).  One row of 4096 takes 1.7 us, 128 rows 3.3:
-// a launch, a trip to memory, two exchanges.
+// rounds of rows); a million of 128 93 us (85 %); 11040 of 5760 without a residual to bf16 and
+// E4M3 52 us (90 %).  One row of 4096 takes 1.7 us, 128 rows 3.3: a launch, a trip to memory, two exchanges.
 #include <algorithm>
 
 #include "common.cuh"
@@ -19,7 +19,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormThreads = 2048;  // of an SM
+constexpr int kNormThreads = 2048;  // of an SM, at most
 constexpr int kNormWarps = 4;       // of a CTA where a warp or a part of one holds a row
 
 // (a plain load: the row may be written in place)
@@ -204,21 +204,31 @@ cudaError_t launch_norm(const NormArgs& a0, cudaStream_t s)
         threads = 32 * kNormWarps;
     } else {
         // one group a thread where the rows then run at once (128 rows of 4096 3.2 us, with two
-        // 4.1), two where there are more (16384 without a residual 58 us, with one 68)
+        // 4.1) and for the most bytes a group, fp32 rows with fp32 residuals (11040 of 7872 173 us, with
+        // two 182); else two (11040 of 4096 in bf16 37 us, with one 43)
         const int one = (groups + 31) / 32 * 32;
-        v = groups <= 1024 && a.T <= (long long)a.sms * (kNormThreads / one) ? 1 : groups <= 2048 ? 2 : 4;
+        v = groups <= 1024 && (a.T <= (long long)a.sms * (kNormThreads / one) || (a.x_f32 && a.res_f32)) ? 1 : groups <= 2048 ? 2 : 4;
         threads = ((groups + v - 1) / v + 31) / 32 * 32;
     }
-    // CTAs that take rows in turn: as many as run at once without a residual (4099 rows of 2880
-    // 15.7 us, with four times as many 18.3), four times as many with one (16384 of 4096 in
-    // bf16 91 us, with fewer 100)
-    const int waves = a.res ? 4 : 1;
     const int codes = !a.codes ? 0 : a.e2m1 ? 2 : 1, res = !a.res ? 0 : a.res_f32 ? 2 : 1;
     const void* fn = a.x_f32 ? (res == 0 ? pick<1, 0>(codes, v, row) : res == 1 ? pick<1, 1>(codes, v, row) : pick<1, 2>(codes, v, row))
                              : (res == 0 ? pick<0, 0>(codes, v, row) : res == 1 ? pick<0, 1>(codes, v, row) : pick<0, 2>(codes, v, row));
     cudaLaunchConfig_t cfg = {};
     const int rows = row ? threads / row : 1;       // of a CTA
-    cfg.gridDim = dim3((unsigned)std::min((a.T + rows - 1) / rows, a.sms * waves * (kNormThreads / threads)));
+    // CTAs that take rows in turn: as many as run at once (11040 rows of 5760 in bf16 51.7 us, with
+    // a third more 57.9), and with a residual or fp32 rows up to eight times as many, two rows
+    // or more each, since some SMs are faster then (11040 of 4096 in bf16 with a residual 59 us,
+    // with as many as run 65; not where an SM has one CTA, whose rows then do not overlap).
+    long long grid = (a.T + rows - 1LL) / rows;
+    if (grid > a.sms) {
+        int at_once = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&at_once, fn, threads, 0);
+        if (e != cudaSuccess) return e;
+        const long long slots = (long long)a.sms * at_once;
+        const long long times = at_once == 1 || (!a.res && !a.x_f32) ? 1 : std::max(1LL, std::min(8LL, grid / (2 * slots)));
+        grid = std::min(grid, slots * times);
+    }
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
