@@ -121,15 +121,17 @@ __device__ __forceinline__ void stage_box(uint8_t* out, int lane, const uint32_t
 // Where y's rows do not begin on 16 bytes, which TMA needs, plain stores of the 16 bytes
 // that are aligned: each row is turned round by its s elements behind such a boundary, so that
 // seven of its eight pieces lie as they do in y, and the eighth holds its first and last
-// elements, which go singly: 9389 tokens by 576 x 2541 take 31.5 us in bf16 and 42.9 in f32, where
-// TMA's by 2544 take 19.2 and 27.1 (a row's words after the other 100 cycles a row: 61.4 and 58.8).
+// elements, which go singly.  8192 tokens by 256 x 9727 take 48 us in bf16 and 93 in f32, where
+// TMA's by 9728 take 31 and 51 (each read after the store before it 54 and 113; a row's words
+// after the other 100 cycles a row, twice that again).
 template <int F32>
 __device__ __forceinline__ void store_rows(const LinearArgs& a, uint8_t* out, int t, int n, int lane, const uint32_t (&box)[32])
 {
     using Value = std::conditional_t<F32, uint32_t, uint16_t>;
     constexpr int kPiece = 16 / sizeof(Value), kRow = 128 / sizeof(Value);
     uint32_t w[32];
-    const int s = (int)((uint32_t)(t + lane) * (uint32_t)a.N) & (kPiece - 1), words = F32 ? s : s >> 1;
+    auto turn = [&](int r) { return (int)((uint32_t)(t + r) * (uint32_t)a.N) & (kPiece - 1); };
+    const int s = turn(lane), words = F32 ? s : s >> 1;
 #pragma unroll
     for (int j = 0; j < 32; j++) w[j] = F32 ? box[j] : __funnelshift_l(box[(j + 31) & 31], box[j], s % 2 * 16);
 #pragma unroll
@@ -142,29 +144,38 @@ __device__ __forceinline__ void store_rows(const LinearArgs& a, uint8_t* out, in
     }
     stage_box(out, lane, w);
     __syncwarp();
-    const int have = min(kRow, a.N - n);
+    // Rows r0, r0 + 4, ... (every read is on its way before the first store; of the rows' turns
+    // there are two, one after the other, so that little is computed for each)
+    const int have = min(kRow, a.N - n), r0 = lane / 8, c = lane % 8, rows = a.T - t - r0;
+    uint4 v[8];
+    Value one[8];
 #pragma unroll
-    for (int b = 0; b < 8; b++) {
-        const int r = 4 * b + lane / 8, c = lane % 8, sr = (int)((uint32_t)(t + r) * (uint32_t)a.N) & (kPiece - 1);
-        const int first = kPiece * c - sr;      // of the box's features
-        if (t + r >= a.T || first < 0 || first >= have) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(out + r * 128 + ((c ^ (r & 7)) << 4));
-        Value* y = (Value*)a.y + (size_t)(t + r) * a.N + n + first;
-        if (first + kPiece <= have) {
-            *reinterpret_cast<uint4*>(y) = v;
-        } else {
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    for (int b = 0; b < 8; b++) v[b] = *reinterpret_cast<const uint4*>(out + (4 * b + r0) * 128 + ((c ^ ((4 * b + r0) & 7)) << 4));
+#pragma unroll
+    for (int b = 0; b < 8; b++) one[b] = *reinterpret_cast<const Value*>(out + (4 * b + r0) * 128 + (((4 * b + r0) & 7) << 4) + c % kPiece * sizeof(Value));
+    const size_t next = 8 * (size_t)a.N;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int sr = turn(r0 + 4 * h), first = kPiece * c - sr;      // of the box's features
+        const int at = c < sr ? kRow + c - sr : c - sr;
+        const bool whole = first >= 0 && first + kPiece <= have, single = c < kPiece && sr > 0 && at < have;
+        Value* y = (Value*)a.y + (size_t)(t + r0 + 4 * h) * a.N + n;
+        Value *to = y + first, *end = y + at;
+#pragma unroll
+        for (int b = h; b < 8; b += 2, to += next, end += next) {
+            if (whole && 4 * b < rows) *reinterpret_cast<uint4*>(to) = v[b];
+            if (single && 4 * b < rows) *end = one[b];
+        }
+        if (first < 0 || first >= have || whole) continue;
+        // the piece that y's last feature is in
+        to = y + first;
+#pragma unroll
+        for (int b = h; b < 8; b += 2, to += next) {
+            const uint32_t u[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
 #pragma unroll
             for (int k = 0; k < kPiece; k++)
-                if (first + k < have) y[k] = (Value)(F32 ? u[k % 4] : u[k / 2 % 4] >> k % 2 * 16);
+                if (4 * b < rows && first + k < have) to[k] = (Value)(F32 ? u[k % 4] : u[k / 2 % 4] >> k % 2 * 16);
         }
-    }
-#pragma unroll
-    for (int b = 0; b < kPiece; b++) {
-        const int r = 32 / kPiece * b + lane / kPiece, e = lane % kPiece, sr = (int)((uint32_t)(t + r) * (uint32_t)a.N) & (kPiece - 1);
-        const int at = e < sr ? kRow + e - sr : e - sr;
-        if (t + r >= a.T || sr == 0 || at >= have) continue;
-        ((Value*)a.y)[(size_t)(t + r) * a.N + n + at] = *reinterpret_cast<const Value*>(out + r * 128 + ((r & 7) << 4) + e * sizeof(Value));
     }
 }
 
