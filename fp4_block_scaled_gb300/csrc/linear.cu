@@ -390,24 +390,23 @@ __global__ void __launch_bounds__(kThreads, 2)
                                          min(p.width, c1 - o * p.width) * kLinRows * 4, smem_u32(&ctl.red), o);
                 }
             } else {
-                size_t at = (size_t)t0 * a.N + n;
-                for (int c0 = 0; c0 < cols; c0 += 32) {
-                    uint32_t r[2][16];
-                    const int have = cols - c0;
-                    tc_ld16_nowait(from + c0, r[0]);
-                    if (have > 16) tc_ld16_nowait(from + c0 + 16, r[1]);
+                // (a store a token: little is computed between them)
+                const size_t size = a.out_f32 ? 4 : 2, next = a.N * size;
+                uint8_t* to = (uint8_t*)a.y + ((size_t)t0 * a.N + n) * size;
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    uint32_t r[16];
+                    tc_ld16_nowait(from + c0, r);
                     tc_wait_ld();
-                    tc_ld_fence_regs<16>(r[0]);
-                    tc_ld_fence_regs<16>(r[1]);
+                    tc_ld_fence_regs<16>(r);
                     if (n >= a.N) continue;
                     if (a.out_f32) {
 #pragma unroll
-                        for (int j = 0; j < 32; j++, at += a.N)
-                            if (j < have) ((float*)a.y)[at] = __uint_as_float(r[j / 16][j % 16]);
+                        for (int j = 0; j < 16; j++, to += next)
+                            if (j < cols - c0) *reinterpret_cast<uint32_t*>(to) = r[j];
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j++, at += a.N)
-                            if (j < have) ((__nv_bfloat16*)a.y)[at] = __float2bfloat16_rn(__uint_as_float(r[j / 16][j % 16]));
+                        for (int j = 0; j < 16; j++, to += next)
+                            if (j < cols - c0) *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(__uint_as_float(r[j]));
                     }
                 }
             }
@@ -461,26 +460,31 @@ int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
 long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 
 // Time of a product in microseconds, as measured in CUDA graphs of products one after the
-// other (K = 512 .. 8192, N = 300 .. 8192, T = 1 .. 3000; what the rule takes is within 15 % of the
+// other (K = 96 .. 8192, N = 300 .. 8192, T = 1 .. 3840; what the rule takes is within 15 % of the
 // best tile and split): a start and end of 3.2, the longer of a CTA's stages (a row of a TMA
 // box takes 2.2 to 2.8 cycles) and of what all of them fetch through L2, and the
-// epilogue; a split product's sums meet in 0.2 and 0.02 a token.
+// epilogue, a store a token, which runs beside the next tile's stages where there are several;
+// a split product's sums meet in 0.2 and 0.02 a token.
 double tile_cost(const LinearArgs& a, const Plan& p)
 {
     const long long tiles = tiles_of(p);
     const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
     const double stage = std::max(0.215, (kLinRows + p.nt) * (a.e2m1 ? 0.00145 : 0.00113));
-    const double serial = waves * ((p.steps + p.split - 1) / p.split) * stage;
+    const double serial = ((p.steps + p.split - 1) / p.split) * stage, output = 0.5 + 0.0085 * p.nt;
     const double feed = (double)tiles * p.steps * ((a.e2m1 ? 17408 : 8704) + p.nt * 132) * 0.77e-7;
-    return 3.2 + std::max(serial, feed) + (p.split > 1 ? 0.2 + 0.02 * p.nt : 0.2 + 0.004 * p.nt * waves);
+    if (p.split > 1) return 3.4 + std::max(serial, feed) + 0.02 * p.nt;
+    if (waves == 1.0) return 3.4 + std::max(serial, feed) + 0.006 * p.nt;
+    return 3.4 + std::max(waves * (std::max(serial, output) + 0.3 * std::min(serial, output)), feed);
 }
 
-// And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage, 2.2 (f32 3) more a tile where y is
-// not stored by TMA.
+// And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage and what of a tile's output does not
+// overlap with them, or the output's time where that is longer.
 double pair_cost(const LinearArgs& a, int steps)
 {
     const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, linear_pairs()));
-    return 4.2 + waves * (steps * (a.e2m1 ? 0.365 : 0.3) + (a.N % (a.out_f32 ? 4 : 8) ? (a.out_f32 ? 3.0 : 2.2) : 0.0));
+    const bool rows = a.N % (a.out_f32 ? 4 : 8) != 0;      // without TMA
+    const double more = a.out_f32 ? (rows ? 2.0 : 0.5) : rows ? 1.0 : 0.0, output = a.out_f32 ? (rows ? 4.6 : 3.4) : rows ? 2.4 : 1.7;
+    return 4.2 + waves * std::max(steps * (a.e2m1 ? 0.365 : 0.3) + more, output);
 }
 
 // Shared and tensor memory of a plan whose tile and split are set; false if it has no room.

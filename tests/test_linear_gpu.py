@@ -90,7 +90,7 @@ def test_few_bf16_rows_are_quantised_alike(fmt, K, N):
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 @pytest.mark.parametrize("T", [300, 4229])
 def test_outputs_of_any_row_length(fmt, T):
-    """Rows of y that begin on any element: of each feature the same sums."""
+    """Rows of y that begin on any element; on pairs of CTAs, which do not cut K, the same sums of each feature."""
     rng = np.random.default_rng(21)
     K, N = 160, 584
     with handle(20, K) as h:
@@ -103,7 +103,11 @@ def test_outputs_of_any_row_length(fmt, T):
             part.codes, part.scales = w.codes[:n].copy(), w.scales[:n].copy()
             part.pack(h)
             for out in ("f32", "bf16"):
-                assert torch.equal(product(h, part, fmt, q, T, out, scales=s), whole[:, :n].to(TORCH[out])), (n, out)
+                y = product(h, part, fmt, q, T, out, scales=s)
+                if T > 4096:
+                    assert torch.equal(y, whole[:, :n].to(TORCH[out])), (n, out)
+                else:
+                    check(y, q, s, part, fmt, out)
 
 
 @pytest.mark.parametrize("T", [1, 2, 5, 20, 300, 4229])
