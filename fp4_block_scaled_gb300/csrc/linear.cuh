@@ -144,7 +144,7 @@ __device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]
 // The scales of a stage's token rows, by one warp: lane l holds those of the rows l, l +
 // 32, ...  E2M1: eight bytes, and where a row's number is no multiple of four, so that they begin
 // anywhere, the three aligned words around them, all on their way at once (byte after byte, 9000
-// tokens by 4832 x 4096 took 112.6 us, so 80.0; 4864 is 75.0.  A path for both kinds
+// tokens by 4832 x 4096, quantised, took 112.6 us, so 80.0; 4864 is 75.0.  A path for both kinds
 // cost the aligned ones 3 %).  E4M3: the row's byte.
 template <int E2M1, int ROWS>
 struct Scales {

@@ -11,7 +11,7 @@
 // share 48 columns.  Outputs leave through shared memory by TMA stores of whole lines (32-byte
 // stores of single rows cost 12 % of the time).
 //
-// Bounds (GB300): 16384 tokens by 4096 x 6144 in E2M1 take 119 us from codes, 6.9 PFLOP/s, 92 %
+// Bounds (GB300): 16384 tokens by 4096 x 6144 in E2M1 take 121 us from codes, 6.8 PFLOP/s, 90 %
 // of four times the measured bf16 rate (the K = 64 steps' nominal ratio); 8191 by 4096 x 5760 in
 // E4M3 109 us, 3.5 PFLOP/s, 94 % of twice that rate.  The tensor pipe is active 77 % and 89 % of
 // the time (ncu), the rest is the first stage of a tile behind the last of the one before, and
