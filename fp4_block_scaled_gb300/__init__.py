@@ -51,6 +51,7 @@ EXPORTS = [
 LIN_EXPORTS = [                     # of include/moe_lin.h
     "moe_lin_create", "moe_lin_status", "moe_lin_destroy", "moe_rms_norm", "moe_mx_quant", "moe_mx_values",
     "moe_linear_packed_bytes", "moe_linear_pack", "moe_linear", "moe_lin_call", "moe_lin_test_set_wait",
+    "moe_lin_test_plan",
 ]
 
 MOE_KV_BF16 = 0
@@ -117,6 +118,14 @@ class moe_norm_desc(ctypes.Structure):
 
 class moe_linear_desc(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("out_features", ctypes.c_int), ("in_features", ctypes.c_int)]
+
+
+class moe_lin_test_device(ctypes.Structure):
+    _fields_ = [("sms", ctypes.c_int), ("pairs", ctypes.c_int), ("clusters", ctypes.c_int * 9)]
+
+
+class moe_lin_test_plan_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("tokens", "tiles", "split", "ring", "smem", "tmem")]
 
 
 _lib = None
@@ -203,6 +212,7 @@ def lib() -> ctypes.CDLL:
             "moe_linear": (I, [P, linp, I, P, P, I, P, I, P]),
             "moe_lin_call": (I, [I, ctypes.c_char_p]),
             "moe_lin_test_set_wait": (I, [P, ctypes.c_ulonglong, I]),
+            "moe_lin_test_plan": (I, [ctypes.POINTER(moe_lin_test_device), I, I, I, I, I, I, ctypes.POINTER(moe_lin_test_plan_t)]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -746,3 +756,12 @@ def moe_lin_test_set_wait(h, wait_ns: int, withhold: bool) -> None:
     """Test hook: bounded-wait limit of the products and the withheld report
     that makes their waits run out (see include/moe_lin.h)."""
     _check(lib().moe_lin_test_set_wait(h, int(wait_ns), 1 if withhold else 0), "moe_lin_test_set_wait")
+
+
+def moe_lin_test_plan(dev: moe_lin_test_device, act_mode: int, T: int, out_features: int, in_features: int, out_dtype: int = MOE_OUT_BF16,
+                      bf16_rows: bool = False) -> moe_lin_test_plan_t:
+    """Test hook: moe_linear's plan for a device's figures (see include/moe_lin.h); needs no GPU."""
+    p = moe_lin_test_plan_t()
+    _check(lib().moe_lin_test_plan(ctypes.byref(dev), int(act_mode), 1 if bf16_rows else 0, int(T), int(out_features), int(in_features),
+                                   int(out_dtype), ctypes.byref(p)), "moe_lin_test_plan")
+    return p

@@ -14,7 +14,7 @@ using namespace moe;
 struct moe_lin_s {
     moe_lin_config cfg;
     int device;
-    int sms;
+    LinDevice dev;
     int* status;
     uint32_t wait_ns;
     int withhold;
@@ -105,8 +105,9 @@ int moe_lin_create(moe_lin_t* out, const moe_lin_config* cfg, int device)
     h->cfg = *cfg;
     h->device = device;
     h->wait_ns = kLinWaitNs;
-    if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        linear_init_device() != cudaSuccess) {
+    if (cudaDeviceGetAttribute(&h->dev.sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        linear_init_device(h->dev) != cudaSuccess) {
+        cudaGetLastError();
         delete h;
         return MOE_ERR_CUDA;
     }
@@ -191,7 +192,7 @@ int moe_rms_norm(moe_lin_t h, const moe_norm_desc* d, const void* x, const void*
     a.res_f32 = d->residual_dtype == MOE_OUT_F32;
     a.e2m1 = act_mode == MOE_ACT_E2M1_UE8M0_32;
     a.eps = d->eps;
-    a.sms = h->sms;
+    a.sms = h->dev.sms;
     LinGuard guard(h->device);
     return cuda_rc(launch_norm(a, (cudaStream_t)stream));
 }
@@ -274,13 +275,12 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
     a.e2m1 = act_mode == MOE_ACT_E2M1_UE8M0_32;
     a.y = y;
     a.out_f32 = out_dtype == MOE_OUT_F32;
-    a.sms = h->sms;
     a.status = h->status;
     a.wait_ns = h->wait_ns;
     a.withhold = h->withhold;
     LinGuard guard(h->device);
     if (!x_scales) {
-        if (linear_takes_bf16(a)) {
+        if (linear_takes_bf16(a, h->dev)) {
             a.codes = a.scales = nullptr;
             a.x = (const uint16_t*)x;
         } else {
@@ -288,7 +288,7 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
             if (e != cudaSuccess) return MOE_ERR_CUDA;
         }
     }
-    return cuda_rc(launch_linear(a, (cudaStream_t)stream));
+    return cuda_rc(launch_linear(a, h->dev, (cudaStream_t)stream));
 }
 
 int moe_lin_test_set_wait(moe_lin_t h, unsigned long long wait_ns, int withhold)
@@ -296,6 +296,29 @@ int moe_lin_test_set_wait(moe_lin_t h, unsigned long long wait_ns, int withhold)
     if (!h || wait_ns > kLinWaitNs) return MOE_ERR_INVALID_ARG;
     h->wait_ns = wait_ns ? (uint32_t)wait_ns : kLinWaitNs;
     h->withhold = withhold != 0;
+    return MOE_OK;
+}
+
+int moe_lin_test_plan(const moe_lin_test_device* dev, int act_mode, int bf16_rows, int T, int out_features, int in_features, int out_dtype,
+                      moe_lin_test_plan_t* plan)
+{
+    if (!dev || !plan || dev->sms <= 0 || dev->pairs <= 0 || !is_codes(act_mode) || !is_type(out_dtype) || T <= 0 || out_features <= 0)
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_rows(T, in_features);
+    if (!rc) rc = check_rows(out_features, in_features);
+    if (rc) return rc;
+    LinDevice d{dev->sms, dev->pairs, {}};
+    for (int i = 2; i <= kLinClusterMax; i++) d.clusters[i] = dev->clusters[i];
+    LinearArgs a{};
+    a.T = T;
+    a.N = out_features;
+    a.K = in_features;
+    a.e2m1 = act_mode == MOE_ACT_E2M1_UE8M0_32;
+    a.out_f32 = out_dtype == MOE_OUT_F32;
+    // (never read: a plan only asks whether there are codes)
+    const uint8_t codes = 0;
+    if (!bf16_rows || !linear_takes_bf16(a, d)) a.codes = &codes;
+    linear_plan(a, d, plan);
     return MOE_OK;
 }
 

@@ -69,6 +69,14 @@ struct NormArgs {
 constexpr int kNormMaxN = 32768;
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
 
+// What a product's plan goes by on its device, asked once for a handle.
+constexpr int kLinClusterMax = 8;       // CTAs of a cluster along K, at most (the portable size)
+struct LinDevice {
+    int sms;
+    int pairs;                          // pairs of CTAs (linear_pair.cu) that run at once
+    int clusters[kLinClusterMax + 1];   // clusters of each size (linear.cu) that run at once
+};
+
 struct LinearArgs {
     const uint8_t* packed;
     const uint8_t* codes;       // rows of x: [T][K / 2] E2M1 or [T][K] E4M3
@@ -78,19 +86,21 @@ struct LinearArgs {
     int e2m1;
     void* y;                    // [T][N]
     int out_f32;
-    int sms;
     int* status;
     uint32_t wait_ns;           // limit of every bounded wait in the kernels
     int withhold;               // test hook: the first CTA never reports its first stage's scales
 };
 constexpr uint32_t kLinWaitNs = 2000000000u;
+// With the device current: its figures, and the kernels' shared-memory limits.
+cudaError_t linear_init_device(LinDevice& dev);
+cudaError_t linear_pair_init_device(LinDevice& dev);
 // Whether the kernel quantises bf16 rows itself; else they are quantised ahead of it.
-bool linear_takes_bf16(const LinearArgs& a);
-cudaError_t linear_init_device();
-// Many tokens on pairs of CTAs (linear_pair.cu), and how many pairs run at once.
-int linear_pairs();
-cudaError_t linear_pair_init_device();
-cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s);
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+bool linear_takes_bf16(const LinearArgs& a, const LinDevice& dev);
+cudaError_t launch_linear(const LinearArgs& a, const LinDevice& dev, cudaStream_t s);
+// Many tokens on pairs of CTAs (linear_pair.cu).
+size_t linear_pair_smem(bool e2m1);
+cudaError_t launch_linear_pair(const LinearArgs& a, const LinDevice& dev, cudaStream_t s);
+// The plan that launch_linear makes, for tests (no device is asked).
+void linear_plan(const LinearArgs& a, const LinDevice& dev, moe_lin_test_plan_t* plan);
 
 }  // namespace moe

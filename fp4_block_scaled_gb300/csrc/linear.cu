@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kRing = 16;                  // stages, at most
 constexpr int kMaxNt = 192;                // tokens of a tile, at most
-constexpr int kSplitMax = 8;               // CTAs of a cluster along K, at most (the portable size)
+constexpr int kSplitMax = kLinClusterMax;
 constexpr int kWarpProd = 4, kWarpMma = 5, kWarpLoad = 6, kLoadWarps = 8;
 constexpr int kThreads = (kWarpLoad + kLoadWarps) * 32;
 
@@ -454,8 +454,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled g_encode = nullptr;
-int g_clusters[kSplitMax + 1];         // clusters of each size that run at once
+// The driver's encoder of tensor maps, asked for once in a process; null if it has none.
+EncodeTiled encoder()
+{
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12080, cudaEnableDefault, &got);
+        return e == cudaSuccess && got == cudaDriverEntryPointSuccess ? (EncodeTiled)p : (EncodeTiled) nullptr;
+    }();
+    return fn;
+}
 
 long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 
@@ -465,10 +474,10 @@ long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 // box takes 2.2 to 2.8 cycles) and of what all of them fetch through L2, and the
 // epilogue, a store a token, which runs beside the next tile's stages where there are several;
 // a split product's sums meet in 0.2 and 0.02 a token.
-double tile_cost(const LinearArgs& a, const Plan& p)
+double tile_cost(const LinearArgs& a, const LinDevice& dev, const Plan& p)
 {
     const long long tiles = tiles_of(p);
-    const double waves = p.split > 1 ? 1.0 : (double)((tiles + a.sms - 1) / a.sms);
+    const double waves = p.split > 1 ? 1.0 : (double)((tiles + dev.sms - 1) / dev.sms);
     const double stage = std::max(0.215, (kLinRows + p.nt) * (a.e2m1 ? 0.00145 : 0.00113));
     const double serial = ((p.steps + p.split - 1) / p.split) * stage, output = 0.5 + 0.0085 * p.nt;
     const double feed = (double)tiles * p.steps * ((a.e2m1 ? 17408 : 8704) + p.nt * 132) * 0.77e-7;
@@ -479,16 +488,16 @@ double tile_cost(const LinearArgs& a, const Plan& p)
 
 // And of one on pairs of CTAs: 0.365 (E4M3 0.3) a stage and what of a tile's output does not
 // overlap with them, or the output's time where that is longer.
-double pair_cost(const LinearArgs& a, int steps)
+double pair_cost(const LinearArgs& a, const LinDevice& dev, int steps)
 {
-    const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, linear_pairs()));
+    const double tiles = (double)((a.T + 255) / 256) * ((a.N + 255) / 256), waves = ceil(tiles / std::max(1, dev.pairs));
     const bool rows = a.N % (a.out_f32 ? 4 : 8) != 0;      // without TMA
     const double more = a.out_f32 ? (rows ? 2.0 : 0.5) : rows ? 1.0 : 0.0, output = a.out_f32 ? (rows ? 4.6 : 3.4) : rows ? 2.4 : 1.7;
     return 4.2 + waves * std::max(steps * (a.e2m1 ? 0.365 : 0.3) + more, output);
 }
 
 // Shared and tensor memory of a plan whose tile and split are set; false if it has no room.
-bool lay_out(const LinearArgs& a, Plan& p)
+bool lay_out(const LinearArgs& a, const LinDevice& dev, Plan& p)
 {
     const int sf = p.nt > 128 ? 2 : 1, h = a.e2m1 ? 2 : 1, slice = (p.steps + p.split - 1) / p.split;
     p.b = kLinCodeBytes;
@@ -500,7 +509,7 @@ bool lay_out(const LinearArgs& a, Plan& p)
     p.groups = (p.split + p.group - 1) / p.group;
     p.sfcols = 4 * h * (1 + sf);
     const uint32_t part = p.split > 1 ? p.split * p.width * kLinRows * 4 : 0, fixed = sizeof(Control) + part;
-    const bool one = p.split > 1 || tiles_of(p) <= a.sms;       // a CTA has one tile
+    const bool one = p.split > 1 || tiles_of(p) <= dev.sms;       // a CTA has one tile
     p.acc = one ? 0 : p.nt;
     p.ring = std::min({kRing, (int)((kLinSmemMax - fixed) / p.stage), (512 - p.nt - p.acc) / p.sfcols, one ? std::max(slice, 3) : kRing});
     // Where four stages fit half an SM and a CTA has no more than twice its stages, two CTAs share
@@ -521,14 +530,14 @@ bool lay_out(const LinearArgs& a, Plan& p)
 }
 
 // The cheapest tile and split; no tile (nt = 0) where pairs of CTAs are cheaper.
-Plan make_plan(const LinearArgs& a)
+Plan make_plan(const LinearArgs& a, const LinDevice& dev)
 {
     Plan p{};
     p.rtiles = lin_tiles(a.N);
     p.steps = a.e2m1 ? lin_units(a.K) : (a.K + 127) / 128;
     p.units = lin_units(a.K);
     Plan best = p;
-    double least = a.codes && a.T > 64 ? pair_cost(a, p.steps) : HUGE_VAL;
+    double least = a.codes && a.T > 64 ? pair_cost(a, dev, p.steps) : HUGE_VAL;
     // (beyond 4096 tokens no tile of one CTA was cheaper)
     const int widest = a.codes && a.T > 4096 ? 0 : std::min(kMaxNt, (a.T + 15) / 16 * 16);
     for (p.nt = widest; p.nt > 0; p.nt -= 16) {
@@ -540,14 +549,14 @@ Plan make_plan(const LinearArgs& a)
         const long long tiles = tiles_of(q);
         for (q.split = 1; q.split <= std::min(kSplitMax, q.steps); q.split++) {
             // clusters that run at once: two CTAs an SM where they are small
-            if (q.split > 1 && (tiles * q.split > a.sms || tiles > g_clusters[q.split] * (q.nt <= 32 ? 2 : 1))) break;
-            const double cost = tile_cost(a, q);
-            if (cost < least && lay_out(a, q)) {
+            if (q.split > 1 && (tiles * q.split > dev.sms || tiles > dev.clusters[q.split] * (q.nt <= 32 ? 2 : 1))) break;
+            const double cost = tile_cost(a, dev, q);
+            if (cost < least && lay_out(a, dev, q)) {
                 least = cost;
                 best = q;
             }
         }
-        if (tiles > 8 * a.sms) break;
+        if (tiles > 8 * dev.sms) break;
     }
     return best;
 }
@@ -558,7 +567,7 @@ cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, con
                        const cuuint64_t* strides, const cuuint32_t* box)
 {
     const cuuint32_t ones[3] = {1, 1, 1};
-    return g_encode(map, type, (cuuint32_t)rank, (void*)base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encoder()(map, type, (cuuint32_t)rank, (void*)base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
@@ -567,7 +576,7 @@ cudaError_t linear_map(CUtensorMap* map, CUtensorMapDataType type, int rank, con
 const void* const kKernels[4] = {(const void*)k_linear<0, 0>, (const void*)k_linear<1, 0>, (const void*)k_linear<0, 1>,
                                  (const void*)k_linear<1, 1>};
 
-bool linear_takes_bf16(const LinearArgs& a0)
+bool linear_takes_bf16(const LinearArgs& a0, const LinDevice& dev)
 {
     // Every CTA quantises its slice of K, so that a kernel ahead, at 1.3 us and a launch, is saved
     // where a warp has few turns (16 rows, two stages a CTA 4.2 us, before 5.0; eight rows, six
@@ -575,21 +584,14 @@ bool linear_takes_bf16(const LinearArgs& a0)
     if (a0.T > kQuantRows) return false;
     LinearArgs a = a0;
     a.codes = nullptr;
-    const Plan p = make_plan(a);
+    const Plan p = make_plan(a, dev);
     const QuantShare q(a.e2m1, a.T, p.ring);
     return (p.steps + p.split - 1) / p.split * q.turns <= 6 * q.stages;
 }
 
-cudaError_t linear_init_device()
+cudaError_t linear_init_device(LinDevice& dev)
 {
-    if (!g_encode) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult got;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12080, cudaEnableDefault, &got);
-        if (e != cudaSuccess) return e;
-        if (got != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        g_encode = (EncodeTiled)fn;
-    }
+    if (!encoder()) return cudaErrorNotSupported;
     for (const void* fn : kKernels) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmemMax);
         if (e != cudaSuccess) return e;
@@ -605,17 +607,24 @@ cudaError_t linear_init_device()
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&g_clusters[split], kKernels[0], &cfg) != cudaSuccess) g_clusters[split] = 0;
-        cudaGetLastError();
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&dev.clusters[split], kKernels[0], &cfg);
+        if (e != cudaSuccess) return e;
     }
-    return linear_pair_init_device();
+    return linear_pair_init_device(dev);
 }
 
-cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
+void linear_plan(const LinearArgs& a, const LinDevice& dev, moe_lin_test_plan_t* plan)
+{
+    const Plan p = make_plan(a, dev);
+    *plan = p.nt == 0 ? moe_lin_test_plan_t{0, 0, 0, 0, (int)linear_pair_smem(a.e2m1), 512}
+                      : moe_lin_test_plan_t{p.nt, p.ttiles * p.rtiles, p.split, p.ring, (int)p.smem, p.tmem};
+}
+
+cudaError_t launch_linear(const LinearArgs& a0, const LinDevice& dev, cudaStream_t s)
 {
     LinearArgs a = a0;
-    Plan p = make_plan(a);
-    if (p.nt == 0) return launch_linear_pair(a, s);
+    Plan p = make_plan(a, dev);
+    if (p.nt == 0) return launch_linear_pair(a, dev, s);
     CUtensorMap wmap, xmap{};
     const cuuint64_t wd[3] = {a.e2m1 ? 128u : 256u, kLinRows, (cuuint64_t)p.rtiles * p.units};
     const cuuint64_t ws[2] = {128, kLinUnitBytes};
@@ -629,7 +638,7 @@ cudaError_t launch_linear(const LinearArgs& a0, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)p.ttiles * p.rtiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : std::min(tiles, (long long)a.sms)));
+    cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : std::min(tiles, (long long)dev.sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = s;

@@ -437,34 +437,30 @@ const void* kernel(bool e2m1, bool f32)
                 : (f32 ? (const void*)k_linear_pair<0, 1> : (const void*)k_linear_pair<0, 0>);
 }
 
-size_t smem_bytes(bool e2m1) { return sizeof(Control) + kRing * (e2m1 ? Stage<1>::bytes : Stage<0>::bytes) + 4 * kOutBytes; }
-
-int g_pairs;        // that run at once
-
 }  // namespace
 
-int linear_pairs() { return g_pairs; }
+size_t linear_pair_smem(bool e2m1) { return sizeof(Control) + kRing * (e2m1 ? Stage<1>::bytes : Stage<0>::bytes) + 4 * kOutBytes; }
 
-cudaError_t linear_pair_init_device()
+cudaError_t linear_pair_init_device(LinDevice& dev)
 {
     for (int i = 0; i < 4; i++) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(i & 1));
+        const cudaError_t e = cudaFuncSetAttribute(kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_pair_smem(i & 1));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(true);
+    cfg.dynamicSmemBytes = linear_pair_smem(true);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(&g_pairs, kernel(true, false), &cfg);
+    return cudaOccupancyMaxActiveClusters(&dev.pairs, kernel(true, false), &cfg);
 }
 
-cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
+cudaError_t launch_linear_pair(const LinearArgs& a0, const LinDevice& dev, cudaStream_t s)
 {
     LinearArgs a = a0;
     int units = lin_units(a.K), ftiles = (a.N + kFeatures - 1) / kFeatures;
@@ -489,9 +485,9 @@ cudaError_t launch_linear_pair(const LinearArgs& a0, cudaStream_t s)
     }
     const long long tiles = (a.T + kTokens - 1LL) / kTokens * ftiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, (long long)g_pairs)));
+    cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, (long long)dev.pairs)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(a.e2m1);
+    cfg.dynamicSmemBytes = linear_pair_smem(a.e2m1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -121,6 +121,25 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
  * MOE_ERR_DEVICE_TIMEOUT.  Errors: INVALID_ARG. */
 int moe_lin_test_set_wait(moe_lin_t h, unsigned long long wait_ns, int withhold);
 
+/* Test hook: the plan of moe_linear for these sizes on a device with the figures
+ * given, the pure host function that the call itself uses (no handle, no GPU).
+ * bf16_rows != 0: of a call without x_scales. */
+typedef struct {
+    int sms;
+    int pairs;              /* pairs of CTAs that run at once                   */
+    int clusters[9];        /* [c]: clusters of c = 2 .. 8 CTAs that do         */
+} moe_lin_test_device;
+typedef struct {
+    int tokens;             /* of a tile; 0: tiles of pairs of CTAs             */
+    int tiles;              /* (of pairs: 0, as are split and ring)             */
+    int split;              /* CTAs of the cluster that cut K for a tile        */
+    int ring;               /* stages                                           */
+    int smem;               /* bytes of shared memory of a CTA                  */
+    int tmem;               /* columns of tensor memory of a CTA                */
+} moe_lin_test_plan_t;
+int moe_lin_test_plan(const moe_lin_test_device* dev, int act_mode, int bf16_rows, int T, int out_features, int in_features,
+                      int out_dtype, moe_lin_test_plan_t* plan);
+
 /* Calls above with their arguments as one array of 64-bit words, in their
  * order: the same call, for language bindings that pay for every argument.
  * INVALID_ARG: an unknown op, no array, an integer outside its type. */
