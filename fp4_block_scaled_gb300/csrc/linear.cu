@@ -466,6 +466,10 @@ EncodeTiled encoder()
     return fn;
 }
 
+// Shared memory of an SM, and of it what each CTA takes beyond its own.
+constexpr uint32_t kSmShared = 228 * 1024, kCtaReserved = 1024;
+static_assert(kSmShared - kCtaReserved == kLinSmemMax, "a CTA with every column takes all of it");
+
 long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 
 // Time of a product in microseconds, as measured in CUDA graphs of products one after the
@@ -513,10 +517,9 @@ bool lay_out(const LinearArgs& a, const LinDevice& dev, Plan& p)
     p.acc = one ? 0 : p.nt;
     p.ring = std::min({kRing, (int)((kLinSmemMax - fixed) / p.stage), (512 - p.nt - p.acc) / p.sfcols, one ? std::max(slice, 3) : kRing});
     // Where four stages fit half an SM and a CTA has no more than twice its stages, two CTAs share
-    // one, so that a kernel can begin beside the one before it, each with at most half of the tensor memory (one token by 4096 x 6144 6.5 us,
-    // before 6.8; their registers allow no third).  Else a CTA takes more than half of the
-    // shared memory: no two CTAs of clusters may share an SM and wait for each other's tensor
-    // memory.
+    // one, so that a kernel can begin beside the one before it, each with at most half of the tensor
+    // memory (one token by 4096 x 6144 6.5 us, before 6.8; their registers allow no third).  Else a
+    // CTA has more than half of the shared memory, as its ring is made for.
     const int two = fixed < kLinSmemTwo ? (int)((kLinSmemTwo - fixed) / p.stage) : 0;
     const bool share = one && two >= 4 && slice <= 2 * two && p.nt + std::min(p.ring, two) * p.sfcols <= 256;
     if (share) p.ring = std::min(p.ring, two);
@@ -525,6 +528,12 @@ bool lay_out(const LinearArgs& a, const LinDevice& dev, Plan& p)
     p.smem = share ? p.part + part : std::max(p.part + part, kLinSmemMax / 2 + 4096);
     p.tmem = 32;
     while (p.tmem < p.nt + p.acc + p.ring * p.sfcols) p.tmem *= 2;
+    // CTAs of a cluster wait for each other's tensor memory without a limit of time, and those of
+    // products on two streams may meet on an SM: none of them may hold columns that another one
+    // beside it lacks.  So each takes at least the share of the SM's shared memory that it takes of
+    // its 512 columns, and what fits the one fits the other.  (CTAs without a cluster wait for
+    // nobody that could wait for their columns.)
+    if (p.split > 1) p.smem = std::max(p.smem, (uint32_t)((unsigned long long)kSmShared * p.tmem / 512 - kCtaReserved));
     // a split tile's sums are laid down in the ring
     return p.ring >= 3 && (p.split == 1 || p.ring * p.stage >= (uint32_t)p.nt * kLinRows * 4);
 }

@@ -51,3 +51,42 @@ def test_refusals():
         with pytest.raises(moe.MoeError) as e:
             moe.moe_lin_test_plan(device(), E2M1, *a)
         assert e.value.code == moe.MOE_ERR_UNSUPPORTED
+
+
+SM_SHARED, RESERVED = 228 * 1024, 1024       # of an SM, and of it for each CTA; a CTA takes at most 227 KB
+
+
+def plans(dev):
+    """The distinct plans over the range of sizes: every number of tokens up to a tile and around the tiles behind, features and
+    reductions from one to many tiles and stages."""
+    tokens = [*range(1, 200, 3), 16, 32, 64, 128, 192, *range(200, 1000, 37), *range(1000, 4400, 211), 5000, 16384, 70001]
+    found = {}
+    for m in (E4M3, E2M1):
+        for N in (1, 129, 640, 1024, 2048, 4099, 6144, 12288, 40000):
+            for K in (32, 256, 288, 512, 768, 1024, 1536, 2048, 2880, 4096, 8192, 32768):
+                for T in tokens:
+                    for out, bf16_rows in ((BF16, False), (F32, False), (BF16, True))[:3 if T <= 16 else 2]:
+                        found.setdefault(plan(dev, m, T, N, K, out, bf16_rows), (m, T, N, K, out, bf16_rows))
+    return found
+
+
+@pytest.mark.parametrize("dev", [GB300, device(132), device(152, 70)], ids=["152", "132", "few_pairs"])
+def test_shared_and_tensor_memory_of_every_plan(dev):
+    """CTAs of clusters wait for one another's tensor memory without a limit of time, and those of two streams' products may
+    meet on an SM.  Each has at least the share of its shared memory that it takes of the 512 columns, so that whatever fits the
+    one fits the other; and none lies beside a pair's CTA, which takes every column, or beside a layer kernel's of 212 KB or
+    more, which waits for its whole grid."""
+    found = plans(dev)
+    pairs = [p for p in found if p[0] == 0]
+    split = [p for p in found if p[2] > 1]
+    assert len(pairs) == 2 and len(split) > 100
+    for p, at in found.items():
+        tokens, tiles, cut, ring, smem, tmem = p
+        assert 0 < smem <= 227 * 1024 and tmem in (32, 64, 128, 256, 512), at
+        if tokens:
+            assert tokens % 16 == 0 and tokens <= 192 and 3 <= ring <= 16 and 1 <= cut <= 8, at
+        if cut > 1:
+            assert (smem + RESERVED) * 512 >= SM_SHARED * tmem, at
+            assert tiles * cut <= dev.sms
+            for other in [q[4] for q in pairs] + [212 * 1024]:
+                assert smem + other + 2 * RESERVED > SM_SHARED, at
