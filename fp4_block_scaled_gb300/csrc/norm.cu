@@ -196,7 +196,7 @@ const void* pick(int codes, int v, int row)
 cudaError_t launch_norm(const NormArgs& a0, cudaStream_t s)
 {
     NormArgs a = a0;
-    const int groups = a.n / 8;
+    const int groups = a.n / 8, codes = !a.codes ? 0 : a.e2m1 ? 2 : 1, res = !a.res ? 0 : a.res_f32 ? 2 : 1;
     const int row = groups > 64 ? 0 : groups > 16 ? 32 : groups > 8 || (a.codes && !a.e2m1) ? 16 : 8;
     int v, threads;
     if (row) {
@@ -207,10 +207,9 @@ cudaError_t launch_norm(const NormArgs& a0, cudaStream_t s)
         // 4.1) and for the most bytes a group, fp32 rows with fp32 residuals (11040 of 7872 173 us, with
         // two 182); else two (11040 of 4096 in bf16 37 us, with one 43)
         const int one = (groups + 31) / 32 * 32;
-        v = groups <= 1024 && (a.T <= (long long)a.sms * (kNormThreads / one) || (a.x_f32 && a.res_f32)) ? 1 : groups <= 2048 ? 2 : 4;
+        v = groups <= 1024 && (a.T <= (long long)a.sms * (kNormThreads / one) || (a.x_f32 && res == 2)) ? 1 : groups <= 2048 ? 2 : 4;
         threads = ((groups + v - 1) / v + 31) / 32 * 32;
     }
-    const int codes = !a.codes ? 0 : a.e2m1 ? 2 : 1, res = !a.res ? 0 : a.res_f32 ? 2 : 1;
     const void* fn = a.x_f32 ? (res == 0 ? pick<1, 0>(codes, v, row) : res == 1 ? pick<1, 1>(codes, v, row) : pick<1, 2>(codes, v, row))
                              : (res == 0 ? pick<0, 0>(codes, v, row) : res == 1 ? pick<0, 1>(codes, v, row) : pick<0, 2>(codes, v, row));
     cudaLaunchConfig_t cfg = {};
