@@ -6,8 +6,8 @@
 // u = r / sqrt(mean(r^2) + eps) * w with r = x + residual: the sum of squares is the only thing
 // that the threads of a row exchange (shuffles, and one barrier where a CTA holds the row).
 // Bound by HBM: 16384 rows of 4096, bf16 with a bf16 residual, to bf16 and E4M3, 91 us (98 % of
-// the copy rate); 16384 of 4096 without a residual 43 us (92 %); 4099 of 2880 14.6 us (84 %: 1.7
-// rounds of rows); a million of 128 93 us (85 %); 11040 of 5760 without a residual to bf16 and
+// the copy rate); 16384 of 4096 without a residual 43 us (92 %); 4099 of 2880 14.6 us (84 %: 2.7
+// rows a CTA); a million of 128 93 us (85 %); 11040 of 5760 without a residual to bf16 and
 // E4M3 52 us (90 %).  One row of 4096 takes 1.7 us, 128 rows 3.3: a launch, a trip to memory, two exchanges.
 #include <algorithm>
 
@@ -61,9 +61,40 @@ __device__ __forceinline__ uint4 bf16x8(const float (&v)[8])
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// Eight elements of the row that a thread holds: as floats, or, where they are of bf16, as
+// they lie in memory, in half the registers.
+template <int PACKED>
+struct Held8;
+
+template <>
+struct Held8<0> {
+    float v[8];
+
+    __device__ __forceinline__ void hold(const float (&f)[8], const uint4&)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = f[i];
+    }
+
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = v[i];
+    }
+};
+
+template <>
+struct Held8<1> {
+    uint4 u;
+
+    __device__ __forceinline__ void hold(const float (&)[8], const uint4& b) { u = b; }
+    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(u, f); }
+};
+
 // RES: 0 none, 1 bf16, 2 fp32.  CODES: 0 none, 1 E4M3, 2 E2M1.  V: groups of eight
 // elements a thread holds.  ROW: the lanes that hold a row (8, 16 or 32), 0 if the CTA does.
-// A CTA takes rows in turn and loads the next ones before it computes the present ones.
+// A CTA takes rows in turn and, but for those of four groups a thread, loads the next ones before
+// it computes the present ones.
 template <int XF32, int RES, int CODES, int V, int ROW>
 __global__ void __launch_bounds__(ROW ? 32 * kNormWarps : 1024) k_norm(NormArgs a)
 {
@@ -73,9 +104,18 @@ __global__ void __launch_bounds__(ROW ? 32 * kNormWarps : 1024) k_norm(NormArgs 
     const int tid = ROW ? (int)threadIdx.x % kLanes : (int)threadIdx.x, step = ROW ? ROW : (int)blockDim.x;
     const int rows = ROW ? 32 * kNormWarps / kLanes : 1, sub = ROW ? (int)threadIdx.x / kLanes : 0;
     const int groups = a.n / 8;
+    // A CTA of up to 1024 threads has 64 registers a thread, which hold no row of four groups, the
+    // next one and the weights.  So there a row of bf16 is kept as such, weights are read from L1 for
+    // each row where the next one takes their place, and of four groups no row comes ahead (spilled
+    // instead, 2048 rows of 32768 in bf16 with an fp32 residual took 201 us, so 142; in fp32 257, so 164;
+    // 16384 of 4096 in bf16 with an fp32 residual 134, so 132).
+    constexpr bool kRow32 = RES == 0 ? XF32 : RES == 2;
+    constexpr bool kAhead = ROW || V < 4;
+    constexpr bool kWeights = ROW || V == 1 || (V == 2 && RES <= !XF32);
+    constexpr int kPacked = !ROW && V > 1 && !kRow32;
     pdl_trigger();
     pdl_wait();
-    uint4 w[V];
+    uint4 w[kWeights ? V : 1];
     Raw8<XF32> x[V];
     Raw8<RES == 2> res[V];
     // (threads behind the row's end or the last row take part in the shuffles, with zeros)
@@ -93,43 +133,45 @@ __global__ void __launch_bounds__(ROW ? 32 * kNormWarps : 1024) k_norm(NormArgs 
         }
     };
     long long first = (long long)blockIdx.x * rows;
-    load(first + sub);
+    if (kAhead) load(first + sub);
 #pragma unroll
     for (int j = 0; j < V; j++)
-        if (a.weight && j * step + tid < groups) w[j] = __ldg(reinterpret_cast<const uint4*>(a.weight) + j * step + tid);
+        if (kWeights && a.weight && j * step + tid < groups) w[kWeights ? j : 0] = __ldg(reinterpret_cast<const uint4*>(a.weight) + j * step + tid);
     for (int buf = 0; first < a.T; first += (long long)gridDim.x * rows, buf ^= 1) {
         const long long t = first + sub;
         const size_t base = (size_t)t * a.n;
-        float v[V][8];
+        Held8<kPacked> row[V];
+        float ss = 0.0f;
+        if (!kAhead) load(t);
 #pragma unroll
         for (int j = 0; j < V; j++) {
             const int g = j * step + tid;
             const bool in = g < groups && t < a.T;
-            x[j].unpack(v[j]);
+            float v[8];
+            uint4 b = x[j].u[0];
+            x[j].unpack(v);
             if (RES) {
                 float r[8];
                 res[j].unpack(r);
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[j][i] += r[i];
+                for (int i = 0; i < 8; i++) v[i] += r[i];
             }
             if (RES == 1) {
                 // the norm is of the residual that is stored
-                const uint4 b = bf16x8(v[j]);
-                unpack8(b, v[j]);
+                b = bf16x8(v);
+                unpack8(b, v);
                 if (a.res_out && in) *reinterpret_cast<uint4*>((uint16_t*)a.res_out + base + 8 * g) = b;
             } else if (RES == 2 && a.res_out && in) {
                 float4* o = reinterpret_cast<float4*>((float*)a.res_out + base + 8 * g);
-                o[0] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
-                o[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
+            row[j].hold(v, b);
+#pragma unroll
+            for (int i = 0; i < 8; i++) ss = fmaf(v[i], v[i], ss);
         }
         const long long next = first + (long long)gridDim.x * rows;
-        if (next < a.T) load(next + sub);
-        float ss = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; j++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) ss = fmaf(v[j][i], v[j][i], ss);
+        if (kAhead && next < a.T) load(next + sub);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         if (!ROW) {
@@ -142,17 +184,19 @@ __global__ void __launch_bounds__(ROW ? 32 * kNormWarps : 1024) k_norm(NormArgs 
         for (int j = 0; j < V; j++) {
             const int g = j * step + tid;
             const bool in = g < groups && t < a.T;
+            float v[8];
+            row[j].get(v);
             if (a.weight && in) {
                 float wf[8];
-                unpack8(w[j], wf);
+                unpack8(kWeights ? w[kWeights ? j : 0] : __ldg(reinterpret_cast<const uint4*>(a.weight) + g), wf);
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[j][i] = v[j][i] * inv * wf[i];
+                for (int i = 0; i < 8; i++) v[i] = v[i] * inv * wf[i];
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[j][i] *= inv;
+                for (int i = 0; i < 8; i++) v[i] *= inv;
             }
             // the codes are those of the bf16 output
-            uint4 u = bf16x8(v[j]);
+            uint4 u = bf16x8(v);
             if (a.out && in) *reinterpret_cast<uint4*>(a.out + base + 8 * g) = u;
             if (CODES == 0) continue;
             if (!in) u = make_uint4(0, 0, 0, 0);

@@ -47,3 +47,43 @@ def test_the_type_of_an_absent_residual_counts_for_nothing(x_type, n):
             outs.append(torch.zeros((T, n), dtype=torch.bfloat16, device="cuda"))
             moe.moe_rms_norm(h, moe.norm(w, n, 1e-6, TYPE[x_type], TYPE[t]), x, T, out=outs[-1])
     assert close(outs[0], norm64(x, w, 1e-6)) and torch.equal(*outs)
+
+
+def turns(h, T, n, x_type, res, codes, in_place, eps=1e-5):
+    """One call; every row and every code held to the formula; nothing behind the last row."""
+    x, r, w = inputs(T, n, x_type, res)
+    row = x.float() if r is None else (x.float() + r.float()).to(r.dtype)
+    in_place = in_place and x_type == "bf16"
+    out = torch.full((T + 1, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    ro = None if r is None else torch.full((T + 1, n), 7.0, dtype=r.dtype, device="cuda")
+    if in_place:                                                 # rows go over their own inputs
+        out[:T].copy_(x)
+        x = out
+    if r is not None and (in_place or x_type == "f32"):
+        ro[:T].copy_(r)
+        r = ro
+    q, s = code_buffers(T, n, codes) if codes != "none" else (None, None)
+    d = moe.norm(w, n, eps, TYPE[x_type], TYPE["f32" if res == "f32" else "bf16"])
+    moe.moe_rms_norm(h, d, x, T, residual=r, residual_out=ro, out=out, act_mode=MODE[codes], codes=q, scales=s)
+    torch.cuda.synchronize()
+    assert moe.moe_lin_status(h) == moe.MOE_OK
+    assert close(out[:T], norm64(row, w, eps)) and torch.all(out[T] == 7.0)
+    if ro is not None:
+        assert torch.equal(ro[:T], row.to(ro.dtype)) and torch.all(ro[T] == 7.0)
+    if codes != "none":
+        q2, s2 = code_buffers(T, n, codes)
+        moe.moe_mx_quant(h, out, T, n, MODE[codes], q2, s2)
+        torch.cuda.synchronize()
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+TYPES = [(x, r) for x in ("bf16", "f32") for r in ("none", "bf16", "f32")]
+
+
+@pytest.mark.parametrize("x_type,res", TYPES)
+@pytest.mark.parametrize("T,n", [(1, 16640), (400, 16640), (333, 20000), (500, 32768)])
+def test_wide_rows_in_turn(x_type, res, T, n):
+    """Four groups a thread."""
+    with handle() as h:
+        for codes, in_place in (("e4m3", False), ("e2m1", True), ("none", False)):
+            turns(h, T, n, x_type, res, codes, in_place)
