@@ -81,9 +81,45 @@ TYPES = [(x, r) for x in ("bf16", "f32") for r in ("none", "bf16", "f32")]
 
 
 @pytest.mark.parametrize("x_type,res", TYPES)
+@pytest.mark.parametrize("T,n", [(9001, 64), (9001, 128), (4099, 288), (5003, 544), (3001, 4096), (1501, 8192), (801, 12000), (700, 16384)])
+def test_rows_in_turn(x_type, res, T, n):
+    """More rows than run at once, in every kernel form: a part of a warp, a warp, a CTA with one or two groups a thread."""
+    with handle() as h:
+        for codes, in_place in (("e4m3", True), ("e2m1", False), ("none", True)):
+            turns(h, T, n, x_type, res, codes, in_place)
+
+
+@pytest.mark.parametrize("x_type,res", TYPES)
 @pytest.mark.parametrize("T,n", [(1, 16640), (400, 16640), (333, 20000), (500, 32768)])
 def test_wide_rows_in_turn(x_type, res, T, n):
     """Four groups a thread."""
     with handle() as h:
         for codes, in_place in (("e4m3", False), ("e2m1", True), ("none", False)):
             turns(h, T, n, x_type, res, codes, in_place)
+
+
+@pytest.mark.parametrize("T,n,x_type,res", [(3001, 4096, "bf16", "bf16"), (1201, 2880, "f32", "none"), (20000, 96, "bf16", "f32"), (400, 32768, "f32", "f32")])
+def test_repeats_are_equal_bit_for_bit(T, n, x_type, res):
+    """A call alone, and one of many that nothing waits between, others' rows before and behind it."""
+    (x, r, w), (x2, r2, _) = inputs(T, n, x_type, res), inputs(T, n, x_type, res, 1)
+    d = moe.norm(w, n, 1e-6, TYPE[x_type], TYPE["f32" if res == "f32" else "bf16"])
+
+    def buffers():
+        return [torch.zeros((T, n), dtype=torch.bfloat16, device="cuda"), None if r is None else torch.zeros_like(r), *code_buffers(T, n, "e4m3")]
+
+    def call(h, x, r, b):
+        moe.moe_rms_norm(h, d, x, T, residual=r, residual_out=b[1], out=b[0], act_mode=MODE["e4m3"], codes=b[2], scales=b[3])
+
+    with handle() as h:
+        want, got, other = buffers(), buffers(), buffers()
+        call(h, x, r, want)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for _ in range(4):
+                call(h, x2, r2, other)
+                call(h, x, r, got)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got) if a is not None)
+            for b in got:
+                if b is not None:
+                    b.view(torch.uint8).fill_(0xEE if b.dtype == torch.uint8 else 0)
