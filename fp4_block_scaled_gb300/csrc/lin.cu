@@ -65,9 +65,9 @@ int check_rows(int rows, int n)
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-cudaError_t quantise(const void* x, int rows, int n, int mode, uint8_t* codes, uint8_t* scales, cudaStream_t s)
+cudaError_t quantise(int sms, const void* x, int rows, int n, int mode, uint8_t* codes, uint8_t* scales, cudaStream_t s)
 {
-    return launch_mx_quant(MxQuantArgs{(const uint16_t*)x, rows, n, mode == MOE_ACT_E2M1_UE8M0_32, codes, scales}, s);
+    return launch_mx_quant(MxQuantArgs{(const uint16_t*)x, rows, n, mode == MOE_ACT_E2M1_UE8M0_32, sms, codes, scales}, s);
 }
 
 // The words of a moe_lin_call, in order.
@@ -208,7 +208,7 @@ int moe_mx_quant(moe_lin_t h, const void* x, int rows, int n, int act_mode, uint
     const size_t nx = (size_t)rows * n * 2, nc = code_bytes(act_mode, rows, n), ns = scale_bytes(act_mode, rows, n);
     if (overlap(codes, nc, x, nx) || overlap(scales, ns, x, nx) || overlap(codes, nc, scales, ns)) return MOE_ERR_INVALID_ARG;
     LinGuard guard(h->device);
-    return cuda_rc(quantise(x, rows, n, act_mode, codes, scales, (cudaStream_t)stream));
+    return cuda_rc(quantise(h->dev.sms, x, rows, n, act_mode, codes, scales, (cudaStream_t)stream));
 }
 
 int moe_mx_values(moe_lin_t h, int act_mode, const uint8_t* codes, const uint8_t* scales, int rows, int n, int out_dtype, void* out,
@@ -284,7 +284,7 @@ int moe_linear(moe_lin_t h, const moe_linear_desc* w, int act_mode, const void* 
             a.codes = a.scales = nullptr;
             a.x = (const uint16_t*)x;
         } else {
-            const cudaError_t e = quantise(x, T, K, act_mode, h->codes, h->scales, (cudaStream_t)stream);
+            const cudaError_t e = quantise(h->dev.sms, x, T, K, act_mode, h->codes, h->scales, (cudaStream_t)stream);
             if (e != cudaSuccess) return MOE_ERR_CUDA;
         }
     }

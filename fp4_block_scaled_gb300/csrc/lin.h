@@ -10,9 +10,9 @@
 
 namespace moe {
 
-// Packed weights of a linear layer (linear.cu streams them, mxpack.cu makes them): tiles
-// of 128 output features, each cut along K into units of 256 elements, in that
-// order.  A unit is 128 rows of 128 bytes of codes (row-major, so that a tensor
+// Packed weights of a linear layer (mxquant.cu makes them, linear.cu and linear_pair.cu
+// stream them): tiles of 128 output features, each cut along K into units of 256 elements,
+// in that order.  A unit is 128 rows of 128 bytes of codes (row-major, so that a tensor
 // map can read it as E2M1 bytes or expand it to a byte an element) and then its two scale
 // atoms of 512 bytes, one for 128 elements each: byte (row % 32) * 16 + (row / 32)
 // * 4 + b holds the scale of row `row`'s block b, the order that tcgen05.cp moves
@@ -38,6 +38,7 @@ struct MxQuantArgs {
     const uint16_t* x;          // bf16 [rows][n]
     int rows, n;
     int e2m1;                   // else E4M3
+    int sms;
     uint8_t* codes;             // [rows][n / 2], or [rows][n]
     uint8_t* scales;            // [rows][n / 32], or [rows][ceil(n / 128)]
 };

@@ -159,7 +159,7 @@ cudaError_t launch_mx_quant(const MxQuantArgs& a0, cudaStream_t s)
     // two loads a thread where that leaves every SM many blocks (16384 x 4096 to E4M3 32.2 us, with
     // one 44, with four 34.4), else one (77 x 2880, quantisation and values, 2.9 us, with four 3.5)
     const long long groups = (long long)a.rows * (a.e2m1 ? a.n / 8 : (a.n + 127) / 128 * 16);
-    const bool many = groups > 4 * 1024 * 152;
+    const bool many = groups > 4096LL * a.sms;
     const void* fn = a.e2m1 ? (many ? (const void*)k_mx_quant<1, 2> : (const void*)k_mx_quant<1, 1>)
                             : (many ? (const void*)k_mx_quant<0, 2> : (const void*)k_mx_quant<0, 1>);
     const int per = many ? 512 : 256;
