@@ -90,3 +90,12 @@ def test_shared_and_tensor_memory_of_every_plan(dev):
             assert tiles * cut <= dev.sms
             for other in [q[4] for q in pairs] + [212 * 1024]:
                 assert smem + other + 2 * RESERVED > SM_SHARED, at
+
+
+@pytest.mark.parametrize("dev", [GB300, device(132)], ids=["152", "132"])
+def test_clusters_run_at_once(dev):
+    """A tile that is cut along K has a cluster of its own, and the costs by which it is cut count one round of them."""
+    found = [(p, at) for p, at in plans(dev).items() if p[2] > 1]
+    assert len(found) > 100
+    for (tokens, tiles, cut, ring, smem, tmem), at in found:
+        assert tiles <= dev.clusters[cut] * (SM_SHARED // (smem + RESERVED)), at
