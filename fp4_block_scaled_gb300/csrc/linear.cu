@@ -472,12 +472,12 @@ static_assert(kSmShared - kCtaReserved == kLinSmemMax, "a CTA with every column 
 
 long long tiles_of(const Plan& p) { return (long long)p.ttiles * p.rtiles; }
 
-// Time of a product in microseconds, as measured in CUDA graphs of products one after the
-// other (K = 96 .. 8192, N = 300 .. 8192, T = 1 .. 3840; what the rule takes is within 15 % of the
-// best tile and split): a start and end of 3.2, the longer of a CTA's stages (a row of a TMA
-// box takes 2.2 to 2.8 cycles) and of what all of them fetch through L2, and the
-// epilogue, a store a token, which runs beside the next tile's stages where there are several;
-// a split product's sums meet in 0.2 and 0.02 a token.
+// Time of a product in microseconds, fitted to what was measured in CUDA graphs of products one
+// after the other (K = 96 .. 8192, N = 300 .. 8192, T = 1 .. 3840): a start and end of 3.4, the
+// longer of a CTA's stages (0.215, or 2.2 to 2.8 cycles a row of its TMA boxes) and of what all of
+// them fetch through L2, and the output.  That is 0.006 a token of a single tile, 0.02 a token
+// where CTAs send their sums to one another, and 0.5 and 0.0085 a token, a store each, beside
+// the next tile's stages: what is longer of the two, and 0.3 of the other.
 double tile_cost(const LinearArgs& a, const LinDevice& dev, const Plan& p)
 {
     const long long tiles = tiles_of(p);

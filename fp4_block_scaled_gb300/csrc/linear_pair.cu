@@ -53,6 +53,14 @@ struct Stage {
     static_assert(sizeof(Control) + kRing * bytes + 4 * kOutBytes <= kLinSmemMax && kLoadWarps <= kRing && slots >= 2, "sizes");
 };
 
+// Arrives at a barrier of CTA `rank` of the pair: released at this CTA's scope alone, for at
+// the cluster's it waited for the memory of the whole CTA (1600 cycles).  That is enough because
+// whoever waits there reads nothing of this CTA's by loads of its own.  What follows in the
+// other CTA are tcgen05 instructions, of which this CTA's half is carried out here: on shared
+// memory that TMA wrote, or that this CTA's threads wrote and fenced to the async proxy ahead of
+// the barrier of their own CTA; and into columns that their warp has read (tcgen05.wait::ld,
+// tcgen05.fence).  A plain load of the other CTA's shared memory behind such a barrier
+// would need .release.cluster here and .acquire.cluster there.
 __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank)
 {
     asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tmbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(

@@ -45,7 +45,10 @@ void moe_lin_destroy(moe_lin_t h);
 /* Root-mean-square norm of T rows, the residual added first:
  *   r = x + residual, rounded to residual_dtype     (without a residual: x)
  *   u = bf16(r / sqrt(mean(r^2) + eps) * weight)
- * and u's codes: those that moe_mx_quant gives for u.  Computed in fp32.
+ * and u's codes: those that moe_mx_quant gives for u.  Computed in fp32, the
+ * squares too: a row whose squares sum beyond its range (elements from about
+ * 1e19) comes out as zeros, and one whose squares vanish (below 1e-23) is
+ * divided by sqrt(eps).
  *   d          host struct
  *   x          device [T][n] of x_dtype
  *   residual   device [T][n] of residual_dtype, or NULL

@@ -123,3 +123,17 @@ def test_repeats_are_equal_bit_for_bit(T, n, x_type, res):
             for b in got:
                 if b is not None:
                     b.view(torch.uint8).fill_(0xEE if b.dtype == torch.uint8 else 0)
+
+
+def test_rows_at_the_ends_of_fp32s_range():
+    """Squares beyond fp32 make a row of zeros, squares that vanish leave eps alone; neighbours are as ever."""
+    n = 4096
+    x = torch.ones((5, n), device="cuda")
+    x[1], x[3] = 1e20, 1e-25
+    w = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((5, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    with handle() as h:
+        moe.moe_rms_norm(h, moe.norm(w, n, 2.0 ** -20, TYPE["f32"], TYPE["f32"]), x, 5, out=out)
+    assert not out[1].any() and close(out[3], x[3].double() * 2.0 ** 10)
+    for t in (0, 2, 4):
+        assert close(out[t], norm64(x[t:t + 1], w, 2.0 ** -20)[0])
