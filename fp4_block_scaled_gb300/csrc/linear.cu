@@ -547,7 +547,11 @@ Plan make_plan(const LinearArgs& a, const LinDevice& dev)
     p.units = lin_units(a.K);
     Plan best = p;
     double least = a.codes && a.T > 64 ? pair_cost(a, dev, p.steps) : HUGE_VAL;
-    // (beyond 4096 tokens no tile of one CTA was cheaper)
+    // Codes of more than 4096 tokens go to the pairs alone, which cut no K, so that there a feature's
+    // sums are the same whatever T and N.  That costs time where tiles of 256 x 256 fit the sizes badly:
+    // with tiles of one CTA looked at too, 216 products of 4200 to 16384 tokens by 24 to 4096 features
+    // took from 0.59 (5000 by 256 x 1024 in E4M3 to fp32 10.2 us, so 6.0) to 1.21 (4200 by 4096 x 1024
+    // 16.7, so 20.2) of theirs.
     const int widest = a.codes && a.T > 4096 ? 0 : std::min(kMaxNt, (a.T + 15) / 16 * 16);
     for (p.nt = widest; p.nt > 0; p.nt -= 16) {
         const int ttiles = (a.T + p.nt - 1) / p.nt;
